@@ -11,8 +11,13 @@ from .binding import (EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3_B128, EP_ERR_BAD_GROUP,
                       ep_combine_reduce, ep_combine_strerror, ep_combine_version,
                       ep_group_local_picks, ep_pack_weights,
                       ep_grouped_gemm_scatter, ep_grouped_gemm_swiglu, ep_signal_completion,
+                      EP_GROUP_MAX, EP_GROUP_TOP2, EP_LOGITS_BF16, EP_LOGITS_F16, EP_LOGITS_F32,
+                      EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, EP_W4_E2M1, EP_W4_INT4,
+                      EP_W4_SCALE_BF16, EP_W4_SCALE_F16, ep_combine_backward,
+                      ep_grouped_gemm_scatter_w4, ep_grouped_gemm_swiglu_w4, ep_pack_weights_w4,
+                      ep_route_topk, ep_route_topk_backward, make_route_params, make_w4_format,
                       load_library, make_params)
-from .context import EpCombine
+from .context import EpCombine, PackedW4
 
 __all__ = [
     "EP_DTYPE_BF16", "EP_DTYPE_FP8_E4M3_B128", "EP_ERR_BAD_GROUP", "EP_ERR_FLAG_TIMEOUT",
@@ -23,5 +28,9 @@ __all__ = [
     "ep_combine_version", "ep_group_local_picks", "ep_grouped_gemm_scatter", "ep_pack_weights",
     "ep_grouped_gemm_swiglu",
     "ep_signal_completion",
-    "load_library", "make_params", "EpCombine",
+    "EP_GROUP_MAX", "EP_GROUP_TOP2", "EP_LOGITS_BF16", "EP_LOGITS_F16", "EP_LOGITS_F32",
+    "EP_SCORE_SIGMOID", "EP_SCORE_SOFTMAX", "EP_W4_E2M1", "EP_W4_INT4", "EP_W4_SCALE_BF16",
+    "EP_W4_SCALE_F16", "ep_combine_backward", "ep_grouped_gemm_scatter_w4",
+    "ep_grouped_gemm_swiglu_w4", "ep_pack_weights_w4", "ep_route_topk", "ep_route_topk_backward",
+    "make_route_params", "make_w4_format", "load_library", "make_params", "EpCombine", "PackedW4",
 ]

@@ -33,11 +33,25 @@ EP_FLAG_W_SLICE_MAJOR = 0x10
 EP_FLAG_DEVICE_EPOCH = 0x20
 EP_FLAG_SEND_TILE = 0x40
 EP_MAX_RANKS = 8
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_GROUP_MAX = 0
+EP_GROUP_TOP2 = 1
+EP_LOGITS_F32 = 0
+EP_LOGITS_BF16 = 1
+EP_LOGITS_F16 = 2
+EP_MAX_ROUTED_EXPERTS = 1024
+EP_MAX_ROUTE_GROUPS = 64
+EP_W4_INT4 = 0
+EP_W4_E2M1 = 1
+EP_W4_SCALE_BF16 = 0
+EP_W4_SCALE_F16 = 1
 
 EXPORTED = ("ep_combine_init", "ep_combine_destroy", "ep_gemm_tile", "ep_group_local_picks",
             "ep_dispatch_rows", "ep_pack_weights", "ep_advance_epoch",
             "ep_grouped_gemm_scatter", "ep_grouped_gemm_scatter_noalloc", "ep_grouped_gemm_swiglu",
-            "ep_grouped_gemm_swiglu_fp8",
+            "ep_grouped_gemm_swiglu_fp8", "ep_grouped_gemm_swiglu_w4", "ep_grouped_gemm_scatter_w4",
+            "ep_pack_weights_w4", "ep_route_topk", "ep_route_topk_backward", "ep_combine_backward",
             "ep_grouped_gemm_scatter_combine", "ep_signal_completion",
             "ep_combine_reduce", "ep_combine_query_error", "ep_combine_strerror",
             "ep_combine_version")
@@ -71,6 +85,27 @@ class EpCombineBuffers(ctypes.Structure):
         ("trace", ctypes.c_void_p),
         ("trace_records", ctypes.c_int64),
         ("epoch_word", ctypes.c_void_p),
+    ]
+
+
+class EpRouteParams(ctypes.Structure):
+    _fields_ = [
+        ("n_experts", ctypes.c_int32),
+        ("n_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class EpW4Format(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("scales", ctypes.c_int32),
     ]
 
 
@@ -127,6 +162,19 @@ def load_library(path: str | None = None):
     lib.ep_signal_completion.restype = ctypes.c_int
     lib.ep_combine_reduce.argtypes = [vp, vp, vp, i32, vp, u64, vp]
     lib.ep_combine_reduce.restype = ctypes.c_int
+    route, w4 = ctypes.POINTER(EpRouteParams), ctypes.POINTER(EpW4Format)
+    lib.ep_route_topk.argtypes = [vp, route, vp, vp, i32, vp, vp, vp]
+    lib.ep_route_topk.restype = ctypes.c_int
+    lib.ep_route_topk_backward.argtypes = [vp, route, vp, vp, vp, i32, vp, vp]
+    lib.ep_route_topk_backward.restype = ctypes.c_int
+    lib.ep_combine_backward.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp]
+    lib.ep_combine_backward.restype = ctypes.c_int
+    lib.ep_pack_weights_w4.argtypes = [vp, w4, vp, vp, i32, i32, vp, vp, vp]
+    lib.ep_pack_weights_w4.restype = ctypes.c_int
+    lib.ep_grouped_gemm_swiglu_w4.argtypes = [vp, w4, vp, vp, vp, vp, i32, vp, vp]
+    lib.ep_grouped_gemm_swiglu_w4.restype = ctypes.c_int
+    lib.ep_grouped_gemm_scatter_w4.argtypes = [vp, w4, vp, vp, vp, vp, vp, i32, i32, vp, u64, vp]
+    lib.ep_grouped_gemm_scatter_w4.restype = ctypes.c_int
     lib.ep_combine_query_error.argtypes = [vp, vp]
     lib.ep_combine_query_error.restype = ctypes.c_int
     lib.ep_combine_strerror.argtypes = [ctypes.c_int]
@@ -327,6 +375,90 @@ def ep_combine_reduce(h, topk_ids, topk_w, tokens_per_rank, out, epoch, stream=N
                                _ptr(topk_w, torch.float32, "topk_w"), int(tokens_per_rank),
                                _ptr(out, torch.bfloat16, "out"), int(epoch), _stream(stream))
     return _check(rc, "ep_combine_reduce")
+
+
+_LOGITS = {torch.float32: EP_LOGITS_F32, torch.bfloat16: EP_LOGITS_BF16,
+           torch.float16: EP_LOGITS_F16}
+_W4_SCALES = {torch.bfloat16: EP_W4_SCALE_BF16, torch.float16: EP_W4_SCALE_F16}
+
+
+def make_route_params(*, n_experts, logits_dtype, n_groups=1, topk_groups=1,
+                      score=EP_SCORE_SOFTMAX, group_score=EP_GROUP_MAX, renormalize=True,
+                      scale=1.0) -> EpRouteParams:
+    if logits_dtype not in _LOGITS:
+        raise ValueError(f"logits must be float32, bfloat16 or float16, not {logits_dtype}")
+    return EpRouteParams(n_experts, n_groups, topk_groups, score, group_score, int(renormalize),
+                         _LOGITS[logits_dtype], scale)
+
+
+def make_w4_format(*, codes, group, scale_dtype) -> EpW4Format:
+    if scale_dtype not in _W4_SCALES:
+        raise ValueError(f"scales must be bfloat16 or float16, not {scale_dtype}")
+    return EpW4Format(codes, group, _W4_SCALES[scale_dtype])
+
+
+def ep_route_topk(h, params: EpRouteParams, logits, bias, tokens_per_rank, topk_ids, topk_w,
+                  stream=None) -> int:
+    rc = load_library().ep_route_topk(
+        h, ctypes.byref(params), _ptr(logits, tuple(_LOGITS), "logits", allow_none=True),
+        _ptr(bias, torch.float32, "bias", allow_none=True), int(tokens_per_rank),
+        _ptr(topk_ids, torch.int32, "topk_ids", allow_none=True),
+        _ptr(topk_w, torch.float32, "topk_w", allow_none=True), _stream(stream))
+    return _check(rc, "ep_route_topk")
+
+
+def ep_route_topk_backward(h, params: EpRouteParams, logits, topk_ids, grad_w, tokens_per_rank,
+                           grad_logits, stream=None) -> int:
+    rc = load_library().ep_route_topk_backward(
+        h, ctypes.byref(params), _ptr(logits, tuple(_LOGITS), "logits", allow_none=True),
+        _ptr(topk_ids, torch.int32, "topk_ids", allow_none=True),
+        _ptr(grad_w, torch.float32, "grad_w", allow_none=True), int(tokens_per_rank),
+        _ptr(grad_logits, tuple(_LOGITS), "grad_logits", allow_none=True), _stream(stream))
+    return _check(rc, "ep_route_topk_backward")
+
+
+def ep_combine_backward(h, grad_out, topk_ids, topk_w, tokens_per_rank, offsets, src_info, m_total,
+                        grad_rows, grad_w, stream=None) -> int:
+    rc = load_library().ep_combine_backward(
+        h, _ptr(grad_out, torch.bfloat16, "grad_out", allow_none=True),
+        _ptr(topk_ids, torch.int32, "topk_ids", allow_none=True),
+        _ptr(topk_w, torch.float32, "topk_w", allow_none=True), int(tokens_per_rank),
+        _ptr(offsets, torch.int32, "offsets", allow_none=True),
+        _ptr(src_info, torch.int32, "src_info", allow_none=True), int(m_total),
+        _ptr(grad_rows, torch.bfloat16, "grad_rows", allow_none=True),
+        _ptr(grad_w, torch.float32, "grad_w", allow_none=True), _stream(stream))
+    return _check(rc, "ep_combine_backward")
+
+
+def ep_pack_weights_w4(h, fmt: EpW4Format, codes, scales, rows, k, codes_out, scales_out,
+                       stream=None) -> int:
+    two = tuple(_W4_SCALES)
+    rc = load_library().ep_pack_weights_w4(
+        h, ctypes.byref(fmt), _ptr(codes, torch.uint8, "codes"), _ptr(scales, two, "scales"),
+        int(rows), int(k), _ptr(codes_out, torch.uint8, "codes_out"),
+        _ptr(scales_out, two, "scales_out"), _stream(stream))
+    return _check(rc, "ep_pack_weights_w4")
+
+
+def ep_grouped_gemm_swiglu_w4(h, fmt: EpW4Format, x1, w1, w1_scale, offsets, m_total, h_out,
+                              stream=None) -> int:
+    rc = load_library().ep_grouped_gemm_swiglu_w4(
+        h, ctypes.byref(fmt), _ptr(x1, torch.bfloat16, "x1", allow_none=True),
+        _ptr(w1, torch.uint8, "w1"), _ptr(w1_scale, tuple(_W4_SCALES), "w1_scale"),
+        _ptr(offsets, torch.int32, "offsets"), int(m_total),
+        _ptr(h_out, torch.bfloat16, "h_out", allow_none=True), _stream(stream))
+    return _check(rc, "ep_grouped_gemm_swiglu_w4")
+
+
+def ep_grouped_gemm_scatter_w4(h, fmt: EpW4Format, x, w, w_scale, offsets, src_info, m_total,
+                               p3_control=0, c_local=None, epoch=1, stream=None) -> int:
+    rc = load_library().ep_grouped_gemm_scatter_w4(
+        h, ctypes.byref(fmt), _ptr(x, torch.bfloat16, "x", allow_none=True),
+        _ptr(w, torch.uint8, "w"), _ptr(w_scale, tuple(_W4_SCALES), "w_scale"),
+        _ptr(offsets, torch.int32, "offsets"),
+        _ptr(src_info, torch.int32, "src_info", allow_none=True), int(m_total), int(p3_control),
+        _ptr(c_local, torch.bfloat16, "c_local", allow_none=True), int(epoch), _stream(stream))
+    return _check(rc, "ep_grouped_gemm_scatter_w4")
 
 
 def ep_combine_query_error(h, stream=None) -> int:

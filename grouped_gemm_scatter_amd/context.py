@@ -4,9 +4,33 @@ creates the library handle and counts step epochs.  Every computation is a
 call into the HIP library."""
 from __future__ import annotations
 
+from contextlib import nullcontext
+from dataclasses import dataclass
+
 import torch
 
 from . import binding as B
+
+_SCORES = {"softmax": B.EP_SCORE_SOFTMAX, "sigmoid": B.EP_SCORE_SIGMOID}
+_GROUP_SCORES = {"max": B.EP_GROUP_MAX, "top2": B.EP_GROUP_TOP2}
+_W4_CODES = {"int4": B.EP_W4_INT4, "e2m1": B.EP_W4_E2M1}
+
+
+def _choice(table: dict, value, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, not {value!r}")
+    return table[value]
+
+
+@dataclass(frozen=True)
+class PackedW4:
+    """A stack of 4-bit expert weights in the layout that the w4 products read
+    (EpCombine.pack_weights_w4)."""
+    codes: torch.Tensor      # uint8, E_l*rows*k/2 values
+    scales: torch.Tensor     # bfloat16 or float16, E_l*rows*(k/group) values
+    rows: int
+    k: int
+    format: B.EpW4Format
 
 
 class EpCombine:
@@ -46,6 +70,7 @@ class EpCombine:
                          for _ in range(n_ranks)]
         self.words = torch.zeros(n_experts_per_device * n_ranks + n_ranks, dtype=torch.int64,
                                  device=self.device)
+        self._device_index = self.words.get_device()
         self.rank_counter = torch.zeros(n_ranks, dtype=torch.int32, device=self.device)
         self.tile_counter = torch.zeros(n_experts_per_device, dtype=torch.int32, device=self.device)
         self.error_word = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -107,6 +132,159 @@ class EpCombine:
                              f"({self.dtype}), got {t.dtype}")
         if t.numel() < elems:
             raise ValueError(f"{name}: {t.numel()} elements, at least {elems} needed")
+
+    def _shape(self, t, name: str, shape: tuple, dtype):
+        """Raises unless `t` is a contiguous tensor of this shape and type on the
+        handle's device."""
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device.type != "cuda" or t.get_device() != self._device_index:
+            raise ValueError(f"{name} must be on the handle's device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+    def _on(self, stream):
+        """Context in which what a call returns is allocated: the stream it runs on."""
+        if stream is None:
+            return nullcontext()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        return torch.cuda.stream(stream)
+
+    def _empty(self, shape, dtype, stream):
+        with self._on(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def route(self, logits, *, bias=None, n_groups: int = 1, topk_groups: int = 1,
+              score: str = "softmax", group_score: str = "max", renormalize: bool = True,
+              scale: float = 1.0, topk_ids=None, topk_w=None, stream=None):
+        """Routing to experts: logits [R][T][n_experts] (float32, bfloat16 or float16) to
+        (topk_ids int32, topk_w float32), both [R][T][top_k], which `group` and `combine`
+        take as they are.  `score` is "softmax" or "sigmoid"; `bias` float32 [n_experts]
+        moves the choice of experts and not their weights; with n_groups > 1 only the
+        topk_groups best groups are picked from, by their largest choice ("max") or the
+        sum of their two largest ("top2")."""
+        R, T, E = logits.shape
+        params = B.make_route_params(
+            n_experts=E, logits_dtype=logits.dtype, n_groups=n_groups, topk_groups=topk_groups,
+            score=_choice(_SCORES, score, "score"),
+            group_score=_choice(_GROUP_SCORES, group_score, "group_score"),
+            renormalize=renormalize, scale=scale)
+        shape = (self.n_ranks, T, self.top_k)
+        self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
+        if bias is not None:
+            self._shape(bias, "bias", (E,), torch.float32)
+        if topk_ids is None:
+            topk_ids = self._empty(shape, torch.int32, stream)
+        else:
+            self._shape(topk_ids, "topk_ids", shape, torch.int32)
+        if topk_w is None:
+            topk_w = self._empty(shape, torch.float32, stream)
+        else:
+            self._shape(topk_w, "topk_w", shape, torch.float32)
+        B.ep_route_topk(self.handle, params, logits, bias, T, topk_ids, topk_w, stream)
+        return topk_ids, topk_w
+
+    def route_backward(self, logits, topk_ids, grad_w, *, score: str = "softmax",
+                       renormalize: bool = True, scale: float = 1.0, grad_logits=None,
+                       stream=None):
+        """Gradient of `route`'s topk_w with respect to its logits (in their type), from
+        the picks it returned and the gradient grad_w [R][T][top_k] of their weights."""
+        R, T, E = logits.shape
+        params = B.make_route_params(n_experts=E, logits_dtype=logits.dtype,
+                                     score=_choice(_SCORES, score, "score"),
+                                     renormalize=renormalize, scale=scale)
+        shape = (self.n_ranks, T, self.top_k)
+        self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
+        self._shape(topk_ids, "topk_ids", shape, torch.int32)
+        self._shape(grad_w, "grad_w", shape, torch.float32)
+        if grad_logits is None:
+            grad_logits = self._empty(logits.shape, logits.dtype, stream)
+        else:
+            self._shape(grad_logits, "grad_logits", logits.shape, logits.dtype)
+        B.ep_route_topk_backward(self.handle, params, logits, topk_ids, grad_w, T, grad_logits,
+                                 stream)
+        return grad_logits
+
+    def combine_backward(self, grad_out, topk_ids, topk_w, offsets, src_info, m_total, *,
+                         grad_rows=None, grad_w=None, rows: bool = True, stream=None):
+        """Gradient of the step's combine: (grad_w [R][T][top_k] float32, grad_rows
+        [m_total][hidden_n] bfloat16) from grad_out [R][T][hidden_n] and what the step left
+        in the receive buffers.  `grad_rows` may be a buffer of more rows, whose rows from
+        m_total on stay as they are; rows=False leaves it out (None is returned)."""
+        T, N, m = grad_out.shape[1], self.hidden_n, int(m_total)
+        shape = (self.n_ranks, T, self.top_k)
+        self._shape(grad_out, "grad_out", (self.n_ranks, T, N), torch.bfloat16)
+        self._shape(topk_ids, "topk_ids", shape, torch.int32)
+        self._shape(topk_w, "topk_w", shape, torch.float32)
+        if rows:
+            self._need(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, 4)
+            self._need(src_info, "src_info", 2 * m, 4)
+            if grad_rows is None:
+                grad_rows = self._empty((m, N), torch.bfloat16, stream)
+            self._need(grad_rows, "grad_rows", m * N, 2)
+        elif grad_rows is not None:
+            raise ValueError("grad_rows given with rows=False")
+        if grad_w is None:
+            grad_w = self._empty(shape, torch.float32, stream)
+        else:
+            self._shape(grad_w, "grad_w", shape, torch.float32)
+        # an empty tensor has no address: no rows are asked for then
+        out = grad_rows if rows and m > 0 else None
+        B.ep_combine_backward(self.handle, grad_out, topk_ids, topk_w, T, offsets, src_info, m,
+                              out, grad_w, stream)
+        return grad_w, grad_rows
+
+    def pack_weights_w4(self, w, scales, *, codes: str = "int4", stream=None) -> PackedW4:
+        """4-bit expert weights laid out once for up_swiglu_w4 and gemm_scatter_w4: w
+        [E_l][rows][k/2] uint8 codes (even k in the low half of a byte) and scales
+        [E_l][rows][k/group] (bfloat16 or float16), group 32, 64 or 128; `codes` is "int4"
+        (value code - 8) or "e2m1"."""
+        n, k = w.shape[1], 2 * w.shape[2]
+        if scales.dim() != 3 or scales.shape[2] < 1 or k % scales.shape[2]:
+            raise ValueError("scales must be [E_l][rows][k/group]")
+        fmt = B.make_w4_format(codes=_choice(_W4_CODES, codes, "codes"),
+                               group=k // scales.shape[2], scale_dtype=scales.dtype)
+        El = self.n_experts_per_device
+        self._shape(w, "w", (El, n, k // 2), torch.uint8)
+        self._shape(scales, "scales", (El, n, scales.shape[2]), scales.dtype)
+        c = self._empty(w.shape, torch.uint8, stream)
+        s = self._empty(scales.shape, scales.dtype, stream)
+        B.ep_pack_weights_w4(self.handle, fmt, w, scales, n, k, c, s, stream)
+        return PackedW4(c, s, n, k, fmt)
+
+    def _need_w4(self, w: PackedW4, rows: int, k: int):
+        if not isinstance(w, PackedW4):
+            raise ValueError("the weights must come from pack_weights_w4")
+        have, want = (w.codes.shape[0], w.rows, w.k), (self.n_experts_per_device, rows, k)
+        if have != want:
+            raise ValueError(f"packed weights of (experts, rows, k) {want} expected, got {have}")
+
+    def up_swiglu_w4(self, x1, w1: PackedW4, offsets, m_total, h_out, *, stream=None):
+        """up_swiglu on 4-bit weights packed from [E_l][2*hidden_k][hidden_n] codes."""
+        hid, inter = self.hidden_n, self.hidden_k
+        self._need(x1, "x1", m_total * hid, 2)
+        self._need_w4(w1, 2 * inter, hid)
+        self._need(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, 4)
+        self._need(h_out, "h_out", m_total * inter, 2)
+        return B.ep_grouped_gemm_swiglu_w4(self.handle, w1.format, x1, w1.codes, w1.scales, offsets,
+                                           m_total, h_out, stream)
+
+    def gemm_scatter_w4(self, x, w: PackedW4, offsets, src_info, m_total, *, p3_control: int = 0,
+                        c_local=None, epoch: int | None = None, stream=None):
+        """gemm_scatter on 4-bit weights packed from [E_l][hidden_n][hidden_k] codes."""
+        K, N = self.hidden_k, self.hidden_n
+        self._need(x, "x", m_total * K, 2)
+        self._need_w4(w, N, K)
+        self._need(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, 4)
+        self._need(src_info, "src_info", 2 * m_total, 4)
+        if p3_control < 0:
+            self._need(c_local, "c_local", m_total * N, 2)
+        return B.ep_grouped_gemm_scatter_w4(self.handle, w.format, x, w.codes, w.scales, offsets,
+                                            src_info, m_total, p3_control, c_local,
+                                            self._epoch(epoch), stream)
 
     def gemm_scatter(self, x, w, offsets, src_info, m_total, *, x_scale=None, w_scale=None,
                      p3_control: int = 0, c_local=None, epoch: int | None = None, stream=None,

@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -196,7 +197,7 @@ int call_tile(const ep_combine_handle* h, int32_t m_total) {
 
 extern "C" {
 
-int ep_combine_version(void) { return 100; }
+int ep_combine_version(void) { return 200; }
 
 const char* ep_combine_strerror(int code) {
   switch (code) {
@@ -542,6 +543,225 @@ int ep_grouped_gemm_scatter_combine(ep_combine_t h, const void* x, const void* w
   if (rc != EP_OK) return rc;
   return gemm_scatter(h, x, w, x_scale, w_scale, offsets, src_info, m_total, 0, nullptr, epoch,
                       stream, h->b.rank_counter, h->b.tile_counter, &c);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Whether the handle's device is the current one (its buffers, and the caller's,
+// live there).
+bool on_device(const ep_combine_handle* h) {
+  int dev = -1;
+  return hipGetDevice(&dev) == hipSuccess && dev == h->device;
+}
+
+// Checks a router call and fills its common arguments.
+int route_args(const ep_combine_handle* h, const ep_route_params* p, const void* logits,
+               int32_t tokens_per_rank, ep::RouteArgs* a) {
+  if (!h || !p) return EP_ERR_INVALID_ARG;
+  if (tokens_per_rank < 0 || tokens_per_rank > h->p.max_tokens_per_rank) return EP_ERR_INVALID_ARG;
+  if (p->n_experts < h->p.top_k || p->n_groups < 1) return EP_ERR_INVALID_ARG;
+  if (p->n_experts > EP_MAX_ROUTED_EXPERTS || p->n_groups > EP_MAX_ROUTE_GROUPS)
+    return EP_ERR_UNSUPPORTED;
+  if (p->n_experts % p->n_groups || p->topk_groups < 1 || p->topk_groups > p->n_groups)
+    return EP_ERR_INVALID_ARG;
+  if (p->score != EP_SCORE_SOFTMAX && p->score != EP_SCORE_SIGMOID) return EP_ERR_INVALID_ARG;
+  if (p->group_score != EP_GROUP_MAX && p->group_score != EP_GROUP_TOP2) return EP_ERR_INVALID_ARG;
+  if (p->renormalize != 0 && p->renormalize != 1) return EP_ERR_INVALID_ARG;
+  if (p->logits_dtype < EP_LOGITS_F32 || p->logits_dtype > EP_LOGITS_F16) return EP_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale)) return EP_ERR_INVALID_ARG;
+  if (tokens_per_rank > 0 && (!logits || !aligned16(logits))) return EP_ERR_INVALID_ARG;
+  if (!on_device(h)) return EP_ERR_INVALID_ARG;
+  *a = ep::RouteArgs{};
+  a->logits = static_cast<const uint8_t*>(logits);
+  a->tokens = int64_t(h->p.n_ranks) * tokens_per_rank;
+  a->n_experts = p->n_experts;
+  a->n_groups = p->n_groups;
+  a->topk_groups = p->topk_groups;
+  a->top_k = h->p.top_k;
+  a->score = p->score;
+  a->group_score = p->group_score;
+  a->renormalize = p->renormalize;
+  a->dtype = p->logits_dtype;
+  a->scale = p->scale;
+  return EP_OK;
+}
+
+bool w4_format_ok(const ep_w4_format* f) {
+  return f && (f->codes == EP_W4_INT4 || f->codes == EP_W4_E2M1) &&
+         (f->group == 32 || f->group == 64 || f->group == 128) &&
+         (f->scales == EP_W4_SCALE_BF16 || f->scales == EP_W4_SCALE_F16);
+}
+
+bool overlap(const void* p, uint64_t np, const void* q, uint64_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ep_route_topk(ep_combine_t h, const ep_route_params* params, const void* logits,
+                  const float* bias, int32_t tokens_per_rank, int32_t* topk_ids, float* topk_w,
+                  void* stream) {
+  ep::RouteArgs a{};
+  const int rc = route_args(h, params, logits, tokens_per_rank, &a);
+  if (rc != EP_OK) return rc;
+  if (tokens_per_rank == 0) return EP_OK;
+  if (!topk_ids || !topk_w) return EP_ERR_INVALID_ARG;
+  a.bias = bias;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  const hipError_t err = ep::launch_route(a, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+int ep_route_topk_backward(ep_combine_t h, const ep_route_params* params, const void* logits,
+                           const int32_t* topk_ids, const float* grad_w, int32_t tokens_per_rank,
+                           void* grad_logits, void* stream) {
+  ep::RouteArgs a{};
+  const int rc = route_args(h, params, logits, tokens_per_rank, &a);
+  if (rc != EP_OK) return rc;
+  if (tokens_per_rank == 0) return EP_OK;
+  if (!topk_ids || !grad_w || !grad_logits || !aligned16(grad_logits)) return EP_ERR_INVALID_ARG;
+  const uint64_t bytes =
+      uint64_t(a.tokens) * a.n_experts * (a.dtype == EP_LOGITS_F32 ? 4 : 2);
+  if (overlap(logits, bytes, grad_logits, bytes)) return EP_ERR_INVALID_ARG;
+  a.topk_ids = const_cast<int32_t*>(topk_ids);
+  a.grad_w = grad_w;
+  a.grad_logits = static_cast<uint8_t*>(grad_logits);
+  const hipError_t err = ep::launch_route_backward(a, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* topk_ids,
+                        const float* topk_w, int32_t tokens_per_rank, const int32_t* offsets,
+                        const int32_t* src_info, int32_t m_total, void* grad_rows, float* grad_w,
+                        void* stream) {
+  if (!h || m_total < 0) return EP_ERR_INVALID_ARG;
+  if (tokens_per_rank < 0 || tokens_per_rank > h->p.max_tokens_per_rank) return EP_ERR_INVALID_ARG;
+  if (!on_device(h)) return EP_ERR_INVALID_ARG;
+  if (tokens_per_rank == 0) return EP_OK;
+  if (!grad_out || !aligned16(grad_out) || !topk_ids || !topk_w || !grad_w)
+    return EP_ERR_INVALID_ARG;
+  if (grad_rows && (!aligned16(grad_rows) || !offsets || (m_total > 0 && !src_info)))
+    return EP_ERR_INVALID_ARG;
+  ep::CombineBackwardArgs a{};
+  a.grad_out = static_cast<const uint8_t*>(grad_out);
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  for (int i = 0; i < h->p.n_ranks; ++i) a.recv[i] = static_cast<const uint8_t*>(h->b.recv_buf[i]);
+  a.offsets = offsets;
+  a.src_info = src_info;
+  a.grad_rows = static_cast<uint8_t*>(grad_rows);
+  a.grad_w = grad_w;
+  a.err = h->b.error_word;
+  a.m_total = m_total;
+  a.n_ranks = h->p.n_ranks;
+  a.tokens = tokens_per_rank;
+  a.top_k = h->p.top_k;
+  a.N = h->p.hidden_n;
+  a.msg_bytes = h->p.msg_bytes;
+  a.expert_lo = h->p.my_rank * h->p.n_experts_per_device;
+  a.n_experts = h->p.n_experts_per_device;
+  const hipError_t err =
+      ep::launch_combine_backward(a, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+int ep_pack_weights_w4(ep_combine_t h, const ep_w4_format* format, const void* codes,
+                       const void* scales, int32_t rows, int32_t k, void* codes_out,
+                       void* scales_out, void* stream) {
+  if (!h || !w4_format_ok(format) || rows < 1 || k < 1) return EP_ERR_INVALID_ARG;
+  if (h->p.dtype != EP_DTYPE_BF16 || rows % 16 || k % 128) return EP_ERR_UNSUPPORTED;
+  for (const void* p : {codes, scales, const_cast<const void*>(codes_out),
+                        const_cast<const void*>(scales_out)})
+    if (!p || !aligned16(p)) return EP_ERR_INVALID_ARG;
+  const int64_t experts = h->p.n_experts_per_device;
+  const uint64_t nc = uint64_t(experts) * rows * k / 2;
+  const uint64_t ns = uint64_t(experts) * rows * (k / format->group) * 2;
+  if (overlap(codes, nc, codes_out, nc) || overlap(codes, nc, scales_out, ns) ||
+      overlap(scales, ns, codes_out, nc) || overlap(scales, ns, scales_out, ns) ||
+      overlap(codes_out, nc, scales_out, ns))
+    return EP_ERR_INVALID_ARG;
+  if (!on_device(h)) return EP_ERR_INVALID_ARG;
+  const hipError_t err = ep::launch_pack_w4(
+      static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
+      static_cast<uint8_t*>(codes_out), static_cast<uint16_t*>(scales_out), experts, rows, k,
+      format->group, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format, const void* x1,
+                              const void* w1, const void* w1_scale, const int32_t* offsets,
+                              int32_t m_total, void* h_out, void* stream) {
+  if (!h || !w4_format_ok(format) || !w1 || !w1_scale || !offsets || m_total < 0)
+    return EP_ERR_INVALID_ARG;
+  if (m_total > 0 && (!x1 || !h_out)) return EP_ERR_INVALID_ARG;
+  if ((x1 && !aligned16(x1)) || !aligned16(w1) || !aligned16(w1_scale) ||
+      (h_out && !aligned16(h_out)))
+    return EP_ERR_INVALID_ARG;
+  if (h->p.dtype != EP_DTYPE_BF16) return EP_ERR_UNSUPPORTED;
+  const int hidden = h->p.hidden_n, inter = h->p.hidden_k;
+  if (inter % 128) return EP_ERR_UNSUPPORTED;
+  // 32-bit byte offsets inside X1
+  if (uint64_t(m_total) * hidden * 2 >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
+  if (!on_device(h)) return EP_ERR_INVALID_ARG;
+
+  ep::W4Args a{};
+  a.g.x = static_cast<const uint8_t*>(x1);
+  a.g.w = static_cast<const uint8_t*>(w1);
+  a.g.offsets = offsets;
+  a.g.c_local = static_cast<uint8_t*>(h_out);
+  a.g.m_total = m_total;
+  a.g.K = hidden;
+  a.g.N = 2 * inter;
+  a.g.s = sink_state(h, 1);     // rank / expert counts and the error word only
+  a.scales = static_cast<const uint16_t*>(w1_scale);
+  a.codes = format->codes;
+  a.group = format->group;
+  a.scale_f16 = format->scales == EP_W4_SCALE_F16;
+  const hipError_t err = ep::launch_gemm_w4(a, true, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format, const void* x,
+                               const void* w, const void* w_scale, const int32_t* offsets,
+                               const int32_t* src_info, int32_t m_total, int32_t p3_control,
+                               void* c_local, uint64_t epoch, void* stream) {
+  if (!h || !w4_format_ok(format) || !w || !w_scale || !offsets || m_total < 0)
+    return EP_ERR_INVALID_ARG;
+  if (m_total > 0 && (!x || !src_info)) return EP_ERR_INVALID_ARG;
+  const bool sink_on = p3_control >= 0;
+  if (!sink_on && m_total > 0 && (!c_local || !aligned16(c_local))) return EP_ERR_INVALID_ARG;
+  if (sink_on && !epoch_ok(h, epoch)) return EP_ERR_INVALID_ARG;
+  if ((x && !aligned16(x)) || !aligned16(w) || !aligned16(w_scale)) return EP_ERR_INVALID_ARG;
+  if (h->p.dtype != EP_DTYPE_BF16 || h->p.hidden_k % 128 || h->p.send_waves ||
+      (h->p.flags & (EP_FLAG_EPILOGUE_ONLY | EP_FLAG_TRACE | EP_FLAG_SEND_TILE)))
+    return EP_ERR_UNSUPPORTED;
+  if (uint64_t(m_total) * h->p.hidden_k * 2 >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
+  if (!on_device(h)) return EP_ERR_INVALID_ARG;
+
+  ep::W4Args a{};
+  a.g.x = static_cast<const uint8_t*>(x);
+  a.g.w = static_cast<const uint8_t*>(w);
+  a.g.offsets = offsets;
+  a.g.src_info = src_info;
+  a.g.c_local = static_cast<uint8_t*>(c_local);
+  a.g.m_total = m_total;
+  a.g.K = h->p.hidden_k;
+  a.g.N = h->p.hidden_n;
+  a.g.sink_on = sink_on ? 1 : 0;
+  a.g.s = sink_state(h, epoch);
+  a.scales = static_cast<const uint16_t*>(w_scale);
+  a.codes = format->codes;
+  a.group = format->group;
+  a.scale_f16 = format->scales == EP_W4_SCALE_F16;
+  const hipError_t err =
+      ep::launch_gemm_w4(a, false, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
 }
 
 int ep_advance_epoch(ep_combine_t h, void* stream) {

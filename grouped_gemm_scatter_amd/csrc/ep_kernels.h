@@ -147,6 +147,64 @@ hipError_t launch_dispatch(const DispatchArgs& a, int num_cus, hipStream_t st);
 hipError_t launch_pack_slice_major(const uint8_t* w, uint8_t* out, int64_t experts, int N, int K,
                                    int num_cus, hipStream_t st);
 
+// Router scores, group limit and top-k picks of every token.
+struct RouteArgs {
+  const uint8_t* logits;     // [tokens][n_experts]
+  const float* bias;         // [n_experts] or null
+  int32_t* topk_ids;         // [tokens][top_k], written by the forward pass
+  float* topk_w;             // [tokens][top_k], written by the forward pass
+  const float* grad_w;       // [tokens][top_k] (backward)
+  uint8_t* grad_logits;      // [tokens][n_experts] (backward)
+  int64_t tokens;            // of all ranks
+  int32_t n_experts;
+  int32_t n_groups;
+  int32_t topk_groups;
+  int32_t top_k;
+  int32_t score;             // EP_SCORE_*
+  int32_t group_score;       // EP_GROUP_*
+  int32_t renormalize;
+  int32_t dtype;             // EP_LOGITS_*
+  float scale;
+};
+hipError_t launch_route(const RouteArgs& a, int num_cus, hipStream_t st);
+hipError_t launch_route_backward(const RouteArgs& a, int num_cus, hipStream_t st);
+
+// Gradient of the combine.
+struct CombineBackwardArgs {
+  const uint8_t* grad_out;   // [R][tokens][N] bf16
+  const int32_t* topk_ids;   // [R][tokens][top_k]
+  const float* topk_w;       // [R][tokens][top_k]
+  const uint8_t* recv[kMaxRanks];
+  const int32_t* offsets;    // [E_l*R + 1] (grad_rows only)
+  const int32_t* src_info;   // [m_total][2] (grad_rows only)
+  uint8_t* grad_rows;        // [m_total][N] bf16, or null
+  float* grad_w;             // [R][tokens][top_k]
+  int32_t* err;
+  int32_t m_total;
+  int32_t n_ranks;
+  int32_t tokens;            // per rank
+  int32_t top_k;
+  int32_t N;
+  int32_t msg_bytes;
+  int32_t expert_lo;
+  int32_t n_experts;         // E_l
+};
+hipError_t launch_combine_backward(const CombineBackwardArgs& a, int num_cus, hipStream_t st);
+
+// 4-bit weights: the packed codes are g.w; g.N counts GEMM columns (2I for the
+// up-projection).
+struct W4Args {
+  GemmArgs g;
+  const uint16_t* scales;    // packed
+  int32_t codes;             // EP_W4_INT4 / EP_W4_E2M1
+  int32_t group;             // 32, 64 or 128
+  int32_t scale_f16;         // scales are fp16, else bf16
+};
+hipError_t launch_gemm_w4(const W4Args& a, bool swiglu, int num_cus, hipStream_t st);
+hipError_t launch_pack_w4(const uint8_t* codes, const uint16_t* scales, uint8_t* codes_out,
+                          uint16_t* scales_out, int64_t experts, int rows, int k, int group,
+                          int num_cus, hipStream_t st);
+
 // Local grouping of the routing (count, scan, place; three launches on st).
 hipError_t launch_grouping(const GroupArgs& a, hipStream_t st);
 

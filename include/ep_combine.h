@@ -424,6 +424,159 @@ EP_API int ep_grouped_gemm_scatter_combine(ep_combine_t h, const void* x, const 
                                            const float* topk_w, int32_t tokens_per_rank,
                                            void* out, uint64_t epoch, void* stream);
 
+/* Routing to experts: the router's logits to the picks and weights that every
+   other call of the library takes (topk_ids, topk_w).  Token (rk, t) has one
+   logit l_i for each of the n_experts global experts.
+     present   l_i is neither NaN nor -infinity (-infinity is how a caller takes
+               an expert out of service); +infinity counts as the largest number
+     scores    s = softmax of the present logits, or s_i = 1 / (1 + e^-l_i); 0
+               for an expert that is not present
+     choice    c_i = s_i + bias_i, or l_i itself without a bias; an expert whose
+               bias is NaN or -infinity is never picked
+     groups    with n_groups > 1, expert i belongs to group i / (n_experts /
+               n_groups); a group's value is the largest choice of its pickable
+               experts (EP_GROUP_MAX), or the sum of the two largest s_i + bias_i
+               (EP_GROUP_TOP2; one if only one is pickable); only experts of the
+               topk_groups groups with the largest values are picked
+     picks     the handle's top_k largest choices, in descending order
+     weights   w_k = scale * s_k, with renormalize scale * s_k / (sum of the
+               picks' s), the bias left out
+   Ties go to the lowest group and expert index.  A comparison that involves
+   a computed score is made in binary64, weights are computed in binary32; a
+   renormalised weight does not underflow, however negative the logits.  A token
+   with fewer pickable experts than top_k gets the id -1 (a dropped pick: no
+   row, no combine term) and the weight 0 in its last places. */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+#define EP_GROUP_MAX 0
+#define EP_GROUP_TOP2 1
+#define EP_LOGITS_F32 0
+#define EP_LOGITS_BF16 1
+#define EP_LOGITS_F16 2
+#define EP_MAX_ROUTED_EXPERTS 1024
+#define EP_MAX_ROUTE_GROUPS 64
+
+typedef struct ep_route_params {
+  int32_t n_experts;             /* E_g: global experts, top_k..EP_MAX_ROUTED_EXPERTS */
+  int32_t n_groups;              /* divides n_experts, at most EP_MAX_ROUTE_GROUPS; 1: no groups */
+  int32_t topk_groups;           /* groups kept, 1..n_groups */
+  int32_t score;                 /* EP_SCORE_* */
+  int32_t group_score;           /* EP_GROUP_* */
+  int32_t renormalize;           /* 0 or 1 */
+  int32_t logits_dtype;          /* EP_LOGITS_*: type of the logits and of their gradient */
+  float scale;                   /* factor on the weights, finite */
+} ep_route_params;
+
+/* logits   device, [R][tokens_per_rank][n_experts], logits_dtype, 16-byte aligned.
+   bias     device, [n_experts] fp32, or NULL.
+   topk_ids device, [R][tokens_per_rank][top_k] int32, written.
+   topk_w   device, [R][tokens_per_rank][top_k] fp32, written.
+   tokens_per_rank  0..max_tokens_per_rank.
+   One launch on `stream`, deterministic; uses the handle's n_ranks and top_k and
+   touches none of its buffers.  EP_ERR_INVALID_ARG for a bad size, flag or
+   pointer, or when the handle's device is not the current one;
+   EP_ERR_UNSUPPORTED for more experts or groups than the limits. */
+EP_API int ep_route_topk(ep_combine_t h, const ep_route_params* params, const void* logits,
+                         const float* bias, int32_t tokens_per_rank, int32_t* topk_ids,
+                         float* topk_w, void* stream);
+
+/* Gradient of ep_route_topk's weights with respect to the logits, for the picks
+   it returned (the picks themselves and the bias have none).  With g_k =
+   scale * grad_w_k, p_k the renormalised scores of the picks and s the scores:
+     softmax             dl_i = s_i (sum of g_k over picks k of i - sum_k g_k s_k), every i
+     softmax, renorm.    dl at pick k = p_k (g_k - sum_j g_j p_j), 0 elsewhere
+     sigmoid             dl at pick k = g_k s_k (1 - s_k), 0 elsewhere
+     sigmoid, renorm.    dl at pick k = p_k (g_k - sum_j g_j p_j) (1 - s_k), 0 elsewhere
+   computed in binary32 and rounded once to the logits' type.  A pick whose id is
+   outside [0, n_experts) or whose logit is not present adds nothing, whatever its
+   gradient; picks of the same id add up.
+   params   those of the forward call (the groups play no part).
+   logits, topk_ids, tokens_per_rank  as for ep_route_topk.
+   grad_w      device, [R][tokens_per_rank][top_k] fp32.
+   grad_logits device, [R][tokens_per_rank][n_experts], the logits' type, 16-byte
+               aligned, every value written.  Not the logits themselves.
+   One launch, deterministic. */
+EP_API int ep_route_topk_backward(ep_combine_t h, const ep_route_params* params,
+                                  const void* logits, const int32_t* topk_ids,
+                                  const float* grad_w, int32_t tokens_per_rank,
+                                  void* grad_logits, void* stream);
+
+/* Gradient of ep_combine_reduce on this GPU's share, from the receive buffers that
+   the step's combine read (call it before they are written again, ordered after
+   that combine; no flag is waited for):
+     grad_w[rk][t][k] = sum_n grad_out[rk][t][n] * slot(rk, t, k)[n]  (fp32) for a
+                        local pick, 0 for any other: what ep_route_topk_backward
+                        takes, once summed over the GPUs of the layer
+     grad_rows[m][:]  = bf16( topk_w[rk][t][k] * grad_out[rk][t][:] ) for the grouped
+                        row m of pick (rk, t, k): the gradient of the rows that
+                        ep_grouped_gemm_scatter sent
+   grad_out  device, [R][tokens_per_rank][N] bf16, 16-byte aligned.
+   topk_ids, topk_w, tokens_per_rank  as for ep_combine_reduce.
+   offsets, src_info, m_total  the layout that ep_group_local_picks made of topk_ids
+             (rows of a run in ascending (t, k)); a local pick without a row there
+             latches EP_ERR_BAD_GROUP and only its row is not written.
+   grad_rows device, [m_total][N] bf16, 16-byte aligned, or NULL (then offsets and
+             src_info may be NULL too); rows from m_total on are left as they are.
+   grad_w    device, [R][tokens_per_rank][top_k] fp32, every value written.
+   One launch, deterministic. */
+EP_API int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* topk_ids,
+                               const float* topk_w, int32_t tokens_per_rank,
+                               const int32_t* offsets, const int32_t* src_info, int32_t m_total,
+                               void* grad_rows, float* grad_w, void* stream);
+
+/* Expert weights in 4 bits with a scale for every `group` consecutive k of a row:
+     w[e][n][k] = scale[e][n][k / group] * v(code[e][n][k])
+   with v(c) = c - 8 (EP_W4_INT4) or the OCP e2m1 value of c (EP_W4_E2M1: sign, two
+   exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives). */
+#define EP_W4_INT4 0
+#define EP_W4_E2M1 1
+#define EP_W4_SCALE_BF16 0
+#define EP_W4_SCALE_F16 1
+
+typedef struct ep_w4_format {
+  int32_t codes;                 /* EP_W4_INT4 or EP_W4_E2M1 */
+  int32_t group;                 /* 32, 64 or 128 */
+  int32_t scales;                /* EP_W4_SCALE_*: the scales' 2-byte type */
+} ep_w4_format;
+
+/* One-time layout of a stack of 4-bit weights for the two calls below: a permutation
+   of the codes and of the scales within each expert (the same sizes), in which what
+   one wave multiplies at a time is one contiguous run.
+   codes      device, [E_l][rows][k/2]: byte b of a row holds code 2b in its low and
+              code 2b + 1 in its high half.
+   scales     device, [E_l][rows][k/group], 2 bytes each.
+   codes_out, scales_out  device, the same sizes, written; 16-byte aligned like the
+              inputs, overlapping none of them (EP_ERR_INVALID_ARG otherwise).
+   rows a multiple of 16 and k of 128 (EP_ERR_UNSUPPORTED).  bf16 handles only
+   (EP_ERR_UNSUPPORTED for fp8): they give E_l. */
+EP_API int ep_pack_weights_w4(ep_combine_t h, const ep_w4_format* format, const void* codes,
+                              const void* scales, int32_t rows, int32_t k, void* codes_out,
+                              void* scales_out, void* stream);
+
+/* ep_grouped_gemm_swiglu on 4-bit weights, for decode: few rows per expert, so that
+   streaming the weights is all of the time.  h_out = bf16( silu(g) * u ), g and u
+   summed in fp32 from exact code values, one scale per group (fp32), over k.
+   x1, offsets, m_total, h_out as there (any number of rows is right; many rows per
+   expert are faster in bf16 weights); w1 and w1_scale as packed from
+   [E_l][2I][hidden] codes.  A row of x1 holding an infinity or a NaN gives
+   non-finite outputs in that row only.  bf16 handles only (EP_ERR_UNSUPPORTED), I a
+   multiple of 128. */
+EP_API int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format, const void* x1,
+                                     const void* w1, const void* w1_scale,
+                                     const int32_t* offsets, int32_t m_total, void* h_out,
+                                     void* stream);
+
+/* ep_grouped_gemm_scatter on 4-bit weights: the same sink, counts, elections, flags,
+   gate, epoch and errors, w and w_scale as packed from [E_l][N][K] codes, K a
+   multiple of 128 (EP_ERR_UNSUPPORTED).  bf16 handles without EP_FLAG_EPILOGUE_ONLY,
+   EP_FLAG_TRACE, EP_FLAG_SEND_TILE or send waves (EP_ERR_UNSUPPORTED);
+   EP_FLAG_W_SLICE_MAJOR plays no part. */
+EP_API int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format, const void* x,
+                                      const void* w, const void* w_scale,
+                                      const int32_t* offsets, const int32_t* src_info,
+                                      int32_t m_total, int32_t p3_control, void* c_local,
+                                      uint64_t epoch, void* stream);
+
 /* Synchronizes the stream, returns the latched device error bits (>= 0) and
    clears them, or a negative code if the read failed. */
 EP_API int ep_combine_query_error(ep_combine_t h, void* stream);
