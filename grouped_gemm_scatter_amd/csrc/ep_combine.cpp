@@ -690,7 +690,7 @@ int ep_pack_weights_w4(ep_combine_t h, const ep_w4_format* format, const void* c
   const hipError_t err = ep::launch_pack_w4(
       static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
       static_cast<uint8_t*>(codes_out), static_cast<uint16_t*>(scales_out), experts, rows, k,
-      format->group, h->num_cus, static_cast<hipStream_t>(stream));
+      format->group, format->codes == EP_W4_INT4, h->num_cus, static_cast<hipStream_t>(stream));
   return err == hipSuccess ? EP_OK : EP_ERR_HIP;
 }
 

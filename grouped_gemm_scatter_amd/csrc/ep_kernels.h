@@ -203,7 +203,7 @@ struct W4Args {
 hipError_t launch_gemm_w4(const W4Args& a, bool swiglu, int num_cus, hipStream_t st);
 hipError_t launch_pack_w4(const uint8_t* codes, const uint16_t* scales, uint8_t* codes_out,
                           uint16_t* scales_out, int64_t experts, int rows, int k, int group,
-                          int num_cus, hipStream_t st);
+                          bool int4, int num_cus, hipStream_t st);
 
 // Local grouping of the routing (count, scan, place; three launches on st).
 hipError_t launch_grouping(const GroupArgs& a, hipStream_t st);

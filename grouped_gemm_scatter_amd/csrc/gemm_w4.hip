@@ -13,10 +13,12 @@
 // codes of k = 32 i + 8 (L / 16) + 0..7, so a wave loads 1 KB contiguously and every
 // dword is one MFMA's operand.  A row's scales of those 128 k are contiguous too.
 //
-// A workgroup of 4 waves takes 64 rows x 128 GEMM columns of one expert (its work
-// table, sink and completion are those of the other grouped GEMMs); a wave takes 32
-// columns, two 16-column blocks, in the up-projection a gate block and the up
-// block of the same outputs, so SwiGLU needs no exchange.
+// The decode tile: a workgroup of 4 waves takes 64 rows x 256 GEMM columns of one
+// expert (work table, sink and completion are those of the other grouped GEMMs), each
+// wave four 16-column blocks over the whole of K, in the up-projection two gate
+// blocks and the up blocks of the same outputs, so SwiGLU needs no exchange.
+// The thin tile, for launches with too few decode tiles to fill the GPU: 16 rows x 64
+// columns, every wave a quarter of K, the quarters' sums joined through LDS.
 #include "ep_combine.h"
 #include "gemm_common.h"
 
@@ -28,38 +30,307 @@ using namespace gemm;
 typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
 
 constexpr int kW4Threads = 256;
-constexpr int kW4Rows = 64;        // rows of a tile
-constexpr int kW4Cols = 128;       // GEMM columns of a tile
+constexpr int kW4Waves = kW4Threads / 64;
 
-// The 8 codes of a packed dword as bf16 values.
+// Tile of a launch: ROWS x COLS GEMM columns, K split over SPLIT waves, BLOCKS
+// 16-column blocks a wave.
+struct DecodeTile {
+  static constexpr int ROWS = 64, COLS = 256, SPLIT = 1, BLOCKS = 4;
+};
+struct ThinTile {
+  static constexpr int ROWS = 16, COLS = 64, SPLIT = 4, BLOCKS = 4;
+};
+
+// The 8 codes of a packed dword as bf16 values: e2m1 values, or (code - 8) / 16.
 template <int CODES>
 __device__ __forceinline__ bf16x8 decode8(uint32_t v) {
-  bf16x8 r;
   if constexpr (CODES == EP_W4_E2M1) {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.f, 0);
     const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.f, 1);
     const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.f, 2);
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.f, 3);
-    r = bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
   } else {
+    // packed as two's complement nibbles, codes 0..3 in the low and 4..7 in the high
+    // halves of the bytes; the conversion takes a byte's low half and gives 1/16 of it
+    bf16x8 r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = (__bf16)((float)((v >> (4 * j)) & 15) - 8.f);
+    for (int j = 0; j < 4; ++j) {
+      r[j] = (__bf16)__builtin_amdgcn_cvt_off_f32_i4((int)(v >> (8 * j)));
+      r[4 + j] = (__bf16)__builtin_amdgcn_cvt_off_f32_i4((int)((v >> 4) >> (8 * j)));
+    }
+    return r;
   }
-  return r;
 }
 
-__device__ __forceinline__ float scale_value(uint16_t s, int f16) {
-  return f16 ? (float)__builtin_bit_cast(_Float16, s) : bf16_lo(s);
+// A row's 2-byte scales of 128 k as one value.
+template <int N> struct ScaleWord { typedef uint16_t type; };
+template <> struct ScaleWord<2> { typedef uint32_t type; };
+template <> struct ScaleWord<4> { typedef uint64_t type; };
+
+// A weight format: code type, group and type of the scales.
+template <int CODES_, int GROUP_, bool F16>
+struct Format {
+  static constexpr int CODES = CODES_, GROUP = GROUP_;
+  typedef typename ScaleWord<128 / GROUP>::type word;
+  static __device__ __forceinline__ float scale(uint16_t s) {
+    float v;
+    if constexpr (F16) v = (float)__builtin_bit_cast(_Float16, s);
+    else v = bf16_lo(s);
+    return CODES == EP_W4_INT4 ? 16.f * v : v;
+  }
+};
+
+// The codes and scales of one step of 128 k: NT 16-column blocks.
+template <class F, int NT>
+struct Weights {
+  u32x4 w[NT];
+  typename F::word s[NT];
+};
+
+// Where a wave's column blocks are (wave-uniform): first 1 KB run and first scales.
+template <int NT>
+struct Blocks {
+  const uint8_t* w[NT];
+  const uint16_t* s[NT];
+};
+
+template <class F, int NT>
+__device__ __forceinline__ void load_weights(Weights<F, NT>& st, const Blocks<NT>& src, int kt,
+                                             int lane) {
+  typedef typename F::word word;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    st.w[i] = load16_nt(src.w[i] + (size_t)kt * 1024 + lane * 16);
+    st.s[i] = reinterpret_cast<const word*>(src.s[i] + (size_t)kt * 16 * (128 / F::GROUP))[lane & 15];
+  }
 }
 
-template <int CODES, int GROUP, bool SWIGLU>
-__global__ __launch_bounds__(kW4Threads) void gemm_w4_kernel(W4Args wa) {
-  constexpr int MT = kW4Rows / 16;                   // 16-row blocks
-  constexpr int SPT = 128 / GROUP;                   // scales of a row per 128 k
-  constexpr int OUT = SWIGLU ? kW4Cols / 2 : kW4Cols;  // output columns of a tile
+// One step: x(j, q) is the X fragment of row block j and quarter q of the 128 k.
+template <class F, int MT, int NT, class X>
+__device__ __forceinline__ void multiply_step(f32x4 (&acc)[NT][MT], const Weights<F, NT>& st,
+                                              X x) {
+  constexpr int SPT = 128 / F::GROUP, QPS = 4 / SPT;    // scales of a row per 128 k; quarters a scale
+#pragma unroll
+  for (int s = 0; s < SPT; ++s) {
+    bf16x8 xf[MT][QPS];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int q = 0; q < QPS; ++q) xf[j][q] = x(j, s * QPS + q);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      f32x4 part[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < QPS; ++q) {
+        const bf16x8 wf = decode8<F::CODES>(st.w[i][s * QPS + q]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][q], wf, part[j], 0, 0, 0);
+      }
+      const float sc = F::scale((uint16_t)(st.s[i] >> (16 * s)));
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(sc, part[j][r], acc[i][j][r]);
+      // the sums are made here: left free, the compiler sinks them past the next branch
+      // and keeps every `part` of the step in registers until then
+#pragma unroll
+      for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[i][j]));
+    }
+  }
+}
+
+// Waits for this wave's LDS accesses only, then for the workgroup: loads from global
+// memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);                // lgkmcnt(0)
+  raw_barrier();
+}
+
+// The decode tile's K loop.  All waves multiply the same X rows, which pass through
+// LDS, two buffers of 128 k: the workgroup loads step k + 2 into registers while step k
+// is multiplied, and writes it to LDS at the next step.  A row's sixteen 16-byte
+// chunks are stored XORed with the row, so that neither the writes (a row by sixteen
+// lanes) nor the reads (a chunk of sixteen rows) meet in a bank.  The weights of three
+// steps are in registers or on their way.
+template <class F, int MT, int NT>
+__device__ __forceinline__ void multiply_shared(f32x4 (&acc)[NT][MT], const Blocks<NT>& src,
+                                                const uint8_t* x, const uint32_t (&xoff)[MT],
+                                                uint8_t* xs, int KT, int tid) {
+  constexpr int BUF = MT * 4096;
+  const int lane = tid & 63, row = tid >> 4;
+  uint8_t* put = xs + row * 256 + ((tid & 15) ^ row) * 16;
+  u32x4 xr[MT];
+  Weights<F, NT> st[3];
+  auto load_x = [&](int k) {
+    const uint8_t* xk = x + (size_t)k * 256;
+#pragma unroll
+    for (int p = 0; p < MT; ++p) xr[p] = load16(xk + xoff[p]);
+  };
+  auto put_x = [&](int k) {
+#pragma unroll
+    for (int p = 0; p < MT; ++p)
+      *reinterpret_cast<u32x4*>(put + (k & 1) * BUF + p * 4096) = xr[p];
+  };
+  auto step = [&](int k, Weights<F, NT>& w) {
+    if (k + 1 < KT) put_x(k + 1);
+    if (k + 2 < KT) load_x(k + 2);
+    const uint8_t* xb = xs + (k & 1) * BUF + (lane & 15) * 256;
+    multiply_step(acc, w, [&](int j, int q) {
+      return *reinterpret_cast<const bf16x8*>(xb + j * 4096 +
+                                              ((4 * q + (lane >> 4)) ^ (lane & 15)) * 16);
+    });
+    if (k + 3 < KT) load_weights(w, src, k + 3, lane);
+    lds_barrier();
+  };
+  load_x(0);
+#pragma unroll
+  for (int d = 0; d < 3; ++d)
+    if (d < KT) load_weights(st[d], src, d, lane);
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  put_x(0);
+  if (KT > 1) load_x(1);
+  lds_barrier();
+  for (int k = 0; k < KT; k += 3) {
+    step(k, st[0]);
+    if (k + 1 < KT) step(k + 1, st[1]);
+    if (k + 2 < KT) step(k + 2, st[2]);
+  }
+}
+
+// The thin tile's: steps [k0, k1) of 16 rows, each wave its own k, X straight from L2.
+template <class F, int NT>
+struct ThinStep {
+  Weights<F, NT> w;
+  bf16x8 x[4];
+};
+
+template <class F, int NT>
+__device__ __forceinline__ void multiply_thin(f32x4 (&acc)[NT][1], const Blocks<NT>& src,
+                                              const uint8_t* x, uint32_t xoff, int k0, int k1,
+                                              int lane) {
+  ThinStep<F, NT> a, b;
+  auto load = [&](ThinStep<F, NT>& st, int k) {
+    load_weights(st.w, src, k, lane);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      st.x[q] = __builtin_bit_cast(bf16x8, load16(x + (size_t)k * 256 + xoff + q * 64));
+  };
+  auto multiply = [&](const ThinStep<F, NT>& st) {
+    multiply_step(acc, st.w, [&](int, int q) { return st.x[q]; });
+  };
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (k0 < k1) load(a, k0);
+  if (k0 + 1 < k1) load(b, k0 + 1);
+  for (int k = k0; k < k1; k += 2) {
+    multiply(a);
+    if (k + 2 < k1) load(a, k + 2);
+    if (k + 1 < k1) {
+      multiply(b);
+      if (k + 3 < k1) load(b, k + 3);
+    }
+  }
+}
+
+// Staged output rows: lane L holds rows 4 (L / 16) + 0..3 of column L % 16 of a block.
+template <int MT>
+__device__ __forceinline__ void stage_block(uint8_t* smem, int pitch, const f32x4 (&y)[MT], int col,
+                                            int lane) {
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<__bf16*>(smem + (j * 16 + (lane >> 4) * 4 + r) * pitch +
+                                 (col + (lane & 15)) * 2) = (__bf16)y[j][r];
+}
+
+template <int MT>
+__device__ __forceinline__ void swiglu(f32x4 (&g)[MT], const f32x4 (&u)[MT]) {
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) g[j][r] = g[j][r] / (1.f + expf(-g[j][r])) * u[j][r];
+}
+
+// The products of one tile with MT 16-row blocks, staged in LDS as bf16 rows.
+template <class T, class F, bool SWIGLU, int MT>
+__device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t, uint8_t* smem,
+                                             int pitch, uint8_t* xs, int tid, int wave) {
+  const GemmArgs& a = wa.g;
+  const int lane = tid & 63;
+  const int KT = a.K / 128, NB = a.N / 16;
+  constexpr int PER = T::COLS / 16;                  // blocks of a tile
+  constexpr int NT = T::BLOCKS;
+  const int tile = t.n_abs / T::COLS;
+  const int first = T::SPLIT > 1 ? 0 : wave * NT;
+  // the wave's first output block of the tile, and its weight blocks
+  const int ob = SWIGLU ? first / 2 : first;
+  Blocks<NT> src;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    int nb = SWIGLU ? tile * (PER / 2) + ob + (i % (NT / 2)) + (i / (NT / 2)) * (NB / 2)
+                    : tile * PER + ob + i;
+    if constexpr (!SWIGLU) nb = min(nb, NB - 1);     // past the last column: not stored
+    const size_t blk = ((size_t)t.e * NB + nb) * KT;
+    src.w[i] = a.w + blk * 1024;
+    src.s[i] = wa.scales + blk * (16 * (128 / F::GROUP));
+  }
+  // rows past m_end read the group's last row; they are not stored
+  auto row_offset = [&](int r) { return (uint32_t)min(t.m_abs + r, t.g1 - 1) * (uint32_t)(a.K * 2); };
+  f32x4 acc[NT][MT];
+  if constexpr (T::SPLIT > 1) {
+    static_assert(T::SPLIT == kW4Waves && NT == kW4Waves && MT == 1, "one block a wave at the end");
+    // the wave's share of K
+    multiply_thin<F>(acc, src, a.x, row_offset(lane & 15) + (lane >> 4) * 16,
+                     wave * KT / T::SPLIT, (wave + 1) * KT / T::SPLIT, lane);
+    // wave w adds up block w of all shares, in the order of k
+    __shared__ f32x4 s_part[T::SPLIT][NT][64];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s_part[wave][i][lane] = acc[i][0];
+    __syncthreads();
+    f32x4 y[SWIGLU ? 2 : 1][1];
+    const int mine = SWIGLU ? wave % (NT / 2) : wave;
+#pragma unroll
+    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+      y[h][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < T::SPLIT; ++p) y[h][0] += s_part[p][mine + h * (NT / 2)][lane];
+    }
+    if constexpr (SWIGLU) swiglu(y[0], y[1]);
+    if (!SWIGLU || wave < NT / 2) stage_block(smem, pitch, y[0], mine * 16, lane);
+  } else {
+    uint32_t xoff[MT];
+#pragma unroll
+    for (int p = 0; p < MT; ++p) xoff[p] = row_offset(p * 16 + (tid >> 4)) + (tid & 15) * 16;
+    multiply_shared<F>(acc, src, a.x, xoff, xs, KT, tid);
+    if constexpr (SWIGLU) {
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i) {
+        swiglu(acc[i], acc[i + NT / 2]);
+        stage_block(smem, pitch, acc[i], (ob + i) * 16, lane);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) stage_block(smem, pitch, acc[i], (ob + i) * 16, lane);
+    }
+  }
+}
+
+template <class T, class F, bool SWIGLU>
+__global__ __launch_bounds__(kW4Threads, 2) void gemm_w4_kernel(W4Args wa) {
+  constexpr int OUT = SWIGLU ? T::COLS / 2 : T::COLS;  // output columns of a tile
   constexpr int PITCH = OUT * 2 + 16;                // bytes per staged output row
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kW4Rows * PITCH];
-  __shared__ uint64_t s_rowdst[kW4Rows];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[T::ROWS * PITCH];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[T::SPLIT > 1 ? 16 : 2 * T::ROWS * 256];
+  __shared__ uint64_t s_rowdst[T::ROWS];
   __shared__ int s_base[kMaxLocalExperts + 1];
   __shared__ int s_gbeg[kMaxLocalExperts + 1];
   __shared__ uint8_t* s_recv[kMaxRanks];
@@ -70,14 +341,16 @@ __global__ __launch_bounds__(kW4Threads) void gemm_w4_kernel(W4Args wa) {
   const GemmArgs& a = wa.g;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int K = a.K, N = a.N, KT = K / 128, NB = N / 16;
   const int El = a.s.n_experts;
+  const int width = SWIGLU ? a.N / 2 : a.N;          // output columns of a row
   if (tid == 0) {
 #pragma unroll
     for (int i = 0; i < kMaxRanks; ++i) s_recv[i] = a.s.recv[i];
   }
   init_done(s_done);
-  if (!build_work_table<kW4Rows, kW4Threads>(a, N / kW4Cols, s_base, s_gbeg, &s_bad)) return;
+  if (!build_work_table<T::ROWS, kW4Threads>(a, (a.N + T::COLS - 1) / T::COLS, s_base, s_gbeg,
+                                             &s_bad))
+    return;
   const int total = s_base[El];
   const int G = gridDim.x, per_xcd = G >> 3;         // G is a multiple of 8
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
@@ -89,7 +362,9 @@ __global__ __launch_bounds__(kW4Threads) void gemm_w4_kernel(W4Args wa) {
   for (int round = 0;; ++round) {
     const int item = round * G + xcd * per_xcd + slot;
     if (item >= total) break;
-    const TileWork t = tile_of<kW4Rows, kW4Cols>(a, s_base, s_gbeg, item);
+    TileWork t = tile_of<T::ROWS, T::COLS>(a, s_base, s_gbeg, item);
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.n_abs = __builtin_amdgcn_readfirstlane(t.n_abs);
     if (t.empty) {
       signal_empty_expert(a, t.e, pending);
       continue;
@@ -99,94 +374,34 @@ __global__ __launch_bounds__(kW4Threads) void gemm_w4_kernel(W4Args wa) {
       prologue_barrier(a, pending);
     }
     const RowInfo ri =
-        tid < kW4Rows ? load_row_info(a, t.e, t.g1, t.m_abs + tid) : RowInfo{-1, 0, 0};
-    // the wave's two 16-column blocks of the weights
-    int nb[2];
-    const int tile = t.n_abs / kW4Cols;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      nb[i] = SWIGLU ? tile * (OUT / 16) + wave + i * (NB / 2) : tile * (OUT / 16) + wave * 2 + i;
-    const int mt = (t.rows + 15) / 16;
-    f32x4 acc[2][MT];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    for (int kt = 0; kt < KT; ++kt) {
-      bf16x8 xf[MT][4];
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        if (j < mt) {
-          // rows past m_end read the group's last row; they are not stored
-          const int m = min(t.m_abs + j * 16 + (lane & 15), t.g1 - 1);
-          const uint8_t* xr = a.x + ((size_t)m * K + kt * 128 + (lane >> 4) * 8) * 2;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            xf[j][i] = __builtin_bit_cast(bf16x8, load16(xr + i * 64));
-        }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const size_t blk = ((size_t)t.e * NB + nb[i]) * KT + kt;
-        const u32x4 w = load16_nt(a.w + blk * 1024 + lane * 16);
-        const uint16_t* sp = wa.scales + (blk * 16 + (lane & 15)) * SPT;
-        f32x4 part[MT];
-#pragma unroll
-        for (int s = 0; s < SPT; ++s) {
-          const float sc = scale_value(sp[s], wa.scale_f16);
-#pragma unroll
-          for (int j = 0; j < MT; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < 4 / SPT; ++q) {
-            const bf16x8 wf = decode8<CODES>(w[s * (4 / SPT) + q]);
-#pragma unroll
-            for (int j = 0; j < MT; ++j)
-              if (j < mt)
-                part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][s * (4 / SPT) + q], wf,
-                                                                  part[j], 0, 0, 0);
-          }
-#pragma unroll
-          for (int j = 0; j < MT; ++j)
-            if (j < mt)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[i][j][r] = __builtin_fmaf(sc, part[j][r], acc[i][j][r]);
-        }
-      }
+        tid < T::ROWS ? load_row_info(a, t.e, t.g1, t.m_abs + tid) : RowInfo{-1, 0, 0};
+    const int mt = __builtin_amdgcn_readfirstlane((t.rows + 15) / 16);
+    if constexpr (T::ROWS == 16) {
+      tile_product<T, F, SWIGLU, 1>(wa, t, smem, PITCH, s_x, tid, wave);
+    } else {
+      if (mt == 1)
+        tile_product<T, F, SWIGLU, 1>(wa, t, smem, PITCH, s_x, tid, wave);
+      else if (mt == 2)
+        tile_product<T, F, SWIGLU, 2>(wa, t, smem, PITCH, s_x, tid, wave);
+      else if (mt == 3)
+        tile_product<T, F, SWIGLU, 3>(wa, t, smem, PITCH, s_x, tid, wave);
+      else
+        tile_product<T, F, SWIGLU, 4>(wa, t, smem, PITCH, s_x, tid, wave);
     }
-
-    // lane L holds rows 4 (L / 16) + 0..3 of column L % 16 of each block: staged in
-    // LDS as bf16 rows, then stored 16 bytes a thread
-#pragma unroll
-    for (int i = 0; i < (SWIGLU ? 1 : 2); ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        if (j < mt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float y = acc[i][j][r];
-            int col = (wave * 2 + i) * 16 + (lane & 15);
-            if constexpr (SWIGLU) {
-              y = y / (1.f + expf(-y)) * acc[1][j][r];
-              col = wave * 16 + (lane & 15);
-            }
-            const int m = j * 16 + (lane >> 4) * 4 + r;
-            *reinterpret_cast<__bf16*>(smem + m * PITCH + col * 2) = (__bf16)y;
-          }
     if constexpr (!SWIGLU) {
-      if (tid < kW4Rows) s_rowdst[tid] = row_destination(a, s_recv, ri, t.m_abs + tid);
+      if (tid < T::ROWS) s_rowdst[tid] = row_destination(a, s_recv, ri, t.m_abs + tid);
     }
     __syncthreads();
     constexpr int TPR = OUT * 2 / 16, RPP = kW4Threads / TPR;
-    const int cc = tid % TPR;
+    const int cc = tid % TPR, col = t.n_abs / T::COLS * OUT + cc * 8;
     for (int r = tid / TPR; r < t.rows; r += RPP) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * PITCH + cc * 16);
+      if (col >= width) continue;
       if constexpr (SWIGLU) {
-        store16_nt(a.c_local + ((size_t)(t.m_abs + r) * (N / 2) + tile * OUT) * 2 + cc * 16, v);
+        store16_nt(a.c_local + ((size_t)(t.m_abs + r) * width + col) * 2, v);
       } else {
         const uint64_t dst = s_rowdst[r];
-        if (dst)
-          store16_nt(reinterpret_cast<uint8_t*>(dst) + (size_t)t.n_abs * 2 + cc * 16, v);
+        if (dst) store16_nt(reinterpret_cast<uint8_t*>(dst) + (size_t)col * 2, v);
       }
     }
     if constexpr (!SWIGLU) {
@@ -200,7 +415,7 @@ __global__ __launch_bounds__(kW4Threads) void gemm_w4_kernel(W4Args wa) {
 
 // Output dword d of a block of 16 rows x 128 k: lane (d / 4) % 64, dword d % 4.
 __global__ __launch_bounds__(256) void pack_w4_codes_kernel(const uint8_t* codes, uint8_t* out,
-                                                            int64_t dwords, int k) {
+                                                            int64_t dwords, int k, bool int4) {
   const int64_t stride = (int64_t)gridDim.x * 256;
   const int KT = k / 128;
   for (int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x; o < dwords; o += stride) {
@@ -208,8 +423,16 @@ __global__ __launch_bounds__(256) void pack_w4_codes_kernel(const uint8_t* codes
     const int d = (int)(o & 255), lane = d >> 2, i = d & 3;
     const int64_t row = blk / KT * 16 + (lane & 15);     // row of the whole stack
     const int64_t k0 = blk % KT * 128 + 32 * i + 8 * (lane >> 4);
-    reinterpret_cast<uint32_t*>(out)[o] =
-        *reinterpret_cast<const uint32_t*>(codes + (row * k + k0) / 2);
+    uint32_t v = *reinterpret_cast<const uint32_t*>(codes + (row * k + k0) / 2);
+    if (int4) {
+      // codes 0..3 to the low, 4..7 to the high halves of the bytes, as two's
+      // complement of code - 8
+      uint32_t r = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r |= (v >> (4 * j) & 15u) << (8 * (j & 3) + (j & 4));
+      v = r ^ 0x88888888u;
+    }
+    reinterpret_cast<uint32_t*>(out)[o] = v;
   }
 }
 
@@ -225,42 +448,63 @@ __global__ __launch_bounds__(256) void pack_w4_scales_kernel(const uint16_t* sca
   }
 }
 
-template <int CODES, int GROUP>
-hipError_t launch(const W4Args& a, bool swiglu, dim3 grid, hipStream_t st) {
+template <class F>
+hipError_t launch(const W4Args& a, bool swiglu, bool thin, dim3 grid, hipStream_t st) {
   const dim3 block(kW4Threads);
-  if (swiglu)
-    hipLaunchKernelGGL((gemm_w4_kernel<CODES, GROUP, true>), grid, block, 0, st, a);
+  if (thin && swiglu)
+    hipLaunchKernelGGL((gemm_w4_kernel<ThinTile, F, true>), grid, block, 0, st, a);
+  else if (thin)
+    hipLaunchKernelGGL((gemm_w4_kernel<ThinTile, F, false>), grid, block, 0, st, a);
+  else if (swiglu)
+    hipLaunchKernelGGL((gemm_w4_kernel<DecodeTile, F, true>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((gemm_w4_kernel<CODES, GROUP, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((gemm_w4_kernel<DecodeTile, F, false>), grid, block, 0, st, a);
   return hipGetLastError();
+}
+
+template <int CODES, int GROUP>
+hipError_t launch(const W4Args& a, bool swiglu, bool thin, dim3 grid, hipStream_t st) {
+  return a.scale_f16 ? launch<Format<CODES, GROUP, true>>(a, swiglu, thin, grid, st)
+                     : launch<Format<CODES, GROUP, false>>(a, swiglu, thin, grid, st);
+}
+
+// Upper bound of the work items of a launch with this tile.
+template <class T>
+int64_t work_items(const W4Args& a) {
+  const int64_t nt = (a.g.N + T::COLS - 1) / T::COLS, El = a.g.s.n_experts;
+  return (int64_t(a.g.m_total) / T::ROWS + El) * nt + El;
 }
 
 }  // namespace
 
 hipError_t launch_gemm_w4(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
-  const int64_t nt = a.g.N / kW4Cols, El = a.g.s.n_experts;
-  const int64_t items = (int64_t(a.g.m_total) / kW4Rows + El) * nt + El;   // upper bound
-  int64_t g = items < 4 * (int64_t)num_cus ? items : 4 * (int64_t)num_cus;
+  // thin tiles where the experts that can have rows make fewer decode tiles than the
+  // GPU holds workgroups of them (two a CU)
+  const int64_t active = a.g.m_total < a.g.s.n_experts ? a.g.m_total : a.g.s.n_experts;
+  const bool thin = active * ((a.g.N + DecodeTile::COLS - 1) / DecodeTile::COLS) < 2 * num_cus;
+  const int64_t items = thin ? work_items<ThinTile>(a) : work_items<DecodeTile>(a);
+  const int64_t most = (thin ? 4 : 2) * (int64_t)num_cus;
+  const int64_t g = items < most ? items : most;
   const dim3 grid((int)((g + 7) / 8 * 8));
   switch (a.codes * 1000 + a.group) {
-    case 32: return launch<EP_W4_INT4, 32>(a, swiglu, grid, st);
-    case 64: return launch<EP_W4_INT4, 64>(a, swiglu, grid, st);
-    case 128: return launch<EP_W4_INT4, 128>(a, swiglu, grid, st);
-    case 1032: return launch<EP_W4_E2M1, 32>(a, swiglu, grid, st);
-    case 1064: return launch<EP_W4_E2M1, 64>(a, swiglu, grid, st);
-    case 1128: return launch<EP_W4_E2M1, 128>(a, swiglu, grid, st);
+    case 32: return launch<EP_W4_INT4, 32>(a, swiglu, thin, grid, st);
+    case 64: return launch<EP_W4_INT4, 64>(a, swiglu, thin, grid, st);
+    case 128: return launch<EP_W4_INT4, 128>(a, swiglu, thin, grid, st);
+    case 1032: return launch<EP_W4_E2M1, 32>(a, swiglu, thin, grid, st);
+    case 1064: return launch<EP_W4_E2M1, 64>(a, swiglu, thin, grid, st);
+    case 1128: return launch<EP_W4_E2M1, 128>(a, swiglu, thin, grid, st);
   }
   return hipErrorInvalidValue;
 }
 
 hipError_t launch_pack_w4(const uint8_t* codes, const uint16_t* scales, uint8_t* codes_out,
                           uint16_t* scales_out, int64_t experts, int rows, int k, int group,
-                          int num_cus, hipStream_t st) {
+                          bool int4, int num_cus, hipStream_t st) {
   const int64_t dwords = experts * rows * k / 8, count = experts * rows * (k / group);
   const int64_t most = 16 * (int64_t)num_cus;
   const int64_t gc = (dwords + 255) / 256, gs = (count + 255) / 256;
   hipLaunchKernelGGL(pack_w4_codes_kernel, dim3((int)(gc < most ? gc : most)), dim3(256), 0, st,
-                     codes, codes_out, dwords, k);
+                     codes, codes_out, dwords, k, int4);
   hipLaunchKernelGGL(pack_w4_scales_kernel, dim3((int)(gs < most ? gs : most)), dim3(256), 0, st,
                      scales, scales_out, count, k, group);
   return hipGetLastError();
