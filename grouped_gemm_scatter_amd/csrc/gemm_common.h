@@ -270,6 +270,13 @@ __device__ __forceinline__ uint64_t row_destination(const GemmArgs& a, uint8_t* 
   return (uint64_t)(s_recv[ri.rk] + slot_offset(ri.t, ri.k, a.s.top_k, a.s.msg_bytes));
 }
 
+// 8 bytes of a sent row, written through the XCD's L2: an agent-scope store, visible
+// to every XCD once it is acknowledged (vmcnt), without the write-back of the
+// L2 that a release fence makes.
+__device__ __forceinline__ void store8_through(void* p, uint64_t v) {
+  __hip_atomic_store(static_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Tiles whose rows are sent but whose completion is still to be counted.
 // Completion is deferred to the next tile's prologue, which drains this
 // workgroup's stores (vector memory operations of a wave complete in issue
@@ -301,10 +308,14 @@ __device__ __forceinline__ int tiles_of(const PendingTiles& p, int e) {
 // fetch-add per tile on its expert's tile counter (fence + RMW = a release
 // RMW), all RMWs before any result is examined.  An RMW that finds its
 // expert's last tile marks the expert done.
+// THROUGH: the rows were stored with store8_through, which an acknowledged store
+// has already made visible to the whole device, so at agent scope there is nothing
+// left to write back and no fence.
+template <bool THROUGH = false>
 __device__ __forceinline__ void complete_pending(const GemmArgs& a, PendingTiles& p) {
   if (p.n == 0) return;
   if (a.sink_on && threadIdx.x == 0) {
-    fence_release(a.s.system_scope);
+    if (!THROUGH || a.s.system_scope) fence_release(a.s.system_scope);
     int old[kPendingMax];
 #pragma unroll
     for (int i = 0; i < kPendingMax; ++i)
@@ -328,12 +339,13 @@ __device__ __forceinline__ void complete_pending(const GemmArgs& a, PendingTiles
 // release and acquire fences: the raw barrier orders execution only, and the
 // fences make every wave's row stores happen-before thread 0's agent-scope
 // release fence in complete_pending.  (p.n is the same in every thread.)
+template <bool THROUGH = false>
 __device__ __forceinline__ void prologue_barrier(const GemmArgs& a, PendingTiles& p) {
   if (p.n >= kPendingMax) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
     raw_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    complete_pending(a, p);
+    complete_pending<THROUGH>(a, p);
   } else {
     raw_barrier();
   }
@@ -361,11 +373,12 @@ __device__ __forceinline__ void load_run_bounds(const GemmArgs& a, int e,
 // (description), with at most four fences per workgroup.  In per-expert
 // completion mode the count words are instead release-stored one by one,
 // tagged with the step, and there is no election.
+template <bool THROUGH = false>
 __device__ __forceinline__ void flush_pending(const GemmArgs& a, PendingTiles& p) {
   if (p.n > 0) {
     wait_vm<0>();
     __syncthreads();
-    complete_pending(a, p);
+    complete_pending<THROUGH>(a, p);
   }
   if (!a.sink_on || threadIdx.x != 0) return;
   bool any = false;

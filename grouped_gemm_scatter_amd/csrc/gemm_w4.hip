@@ -37,6 +37,9 @@ constexpr int kW4Waves = kW4Threads / 64;
 struct DecodeTile {
   static constexpr int ROWS = 64, COLS = 256, SPLIT = 1, BLOCKS = 4;
 };
+struct NarrowTile {
+  static constexpr int ROWS = 64, COLS = 128, SPLIT = 1, BLOCKS = 2;
+};
 struct ThinTile {
   static constexpr int ROWS = 16, COLS = 64, SPLIT = 4, BLOCKS = 4;
 };
@@ -371,7 +374,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void gemm_w4_kernel(W4Args wa) {
     }
     if (pending.n >= kPendingMax) {
       wait_vm<0>();
-      prologue_barrier(a, pending);
+      prologue_barrier<true>(a, pending);
     }
     const RowInfo ri =
         tid < T::ROWS ? load_row_info(a, t.e, t.g1, t.m_abs + tid) : RowInfo{-1, 0, 0};
@@ -392,17 +395,26 @@ __global__ __launch_bounds__(kW4Threads, 2) void gemm_w4_kernel(W4Args wa) {
       if (tid < T::ROWS) s_rowdst[tid] = row_destination(a, s_recv, ri, t.m_abs + tid);
     }
     __syncthreads();
-    constexpr int TPR = OUT * 2 / 16, RPP = kW4Threads / TPR;
-    const int cc = tid % TPR, col = t.n_abs / T::COLS * OUT + cc * 8;
-    for (int r = tid / TPR; r < t.rows; r += RPP) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(smem + r * PITCH + cc * 16);
-      if (col >= width) continue;
-      if constexpr (SWIGLU) {
-        store16_nt(a.c_local + ((size_t)(t.m_abs + r) * width + col) * 2, v);
-      } else {
-        const uint64_t dst = s_rowdst[r];
-        if (dst) store16_nt(reinterpret_cast<uint8_t*>(dst) + (size_t)col * 2, v);
-      }
+    const int col0 = t.n_abs / T::COLS * OUT;
+    if (SWIGLU || !a.sink_on) {
+      constexpr int TPR = OUT * 2 / 16, RPP = kW4Threads / TPR;
+      const int cc = tid % TPR, col = col0 + cc * 8;
+      if (col < width)
+        for (int r = tid / TPR; r < t.rows; r += RPP)
+          store16_nt(a.c_local + ((size_t)(t.m_abs + r) * width + col) * 2,
+                     *reinterpret_cast<const u32x4*>(smem + r * PITCH + cc * 16));
+    } else {
+      // sent rows are written through: a fence per workgroup, each a write-back of its
+      // XCD's L2, took 39 of the 62 us of a one-token launch and 20 of a decode step's 95
+      constexpr int TPR = OUT * 2 / 8, RPP = kW4Threads / TPR;
+      const int cc = tid % TPR, col = col0 + cc * 4;
+      if (col < width)
+        for (int r = tid / TPR; r < t.rows; r += RPP) {
+          const uint64_t dst = s_rowdst[r];
+          if (dst)
+            store8_through(reinterpret_cast<uint8_t*>(dst) + (size_t)col * 2,
+                           *reinterpret_cast<const uint64_t*>(smem + r * PITCH + cc * 8));
+        }
     }
     if constexpr (!SWIGLU) {
       if (tid == 0) pending.e[pending.n] = t.e;
@@ -410,7 +422,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void gemm_w4_kernel(W4Args wa) {
     }
     __syncthreads();   // the staged tile is read; the next one may overwrite it
   }
-  if constexpr (!SWIGLU) flush_pending(a, pending);
+  if constexpr (!SWIGLU) flush_pending<true>(a, pending);
 }
 
 // Output dword d of a block of 16 rows x 128 k: lane (d / 4) % 64, dword d % 4.
@@ -448,51 +460,48 @@ __global__ __launch_bounds__(256) void pack_w4_scales_kernel(const uint16_t* sca
   }
 }
 
-template <class F>
-hipError_t launch(const W4Args& a, bool swiglu, bool thin, dim3 grid, hipStream_t st) {
-  const dim3 block(kW4Threads);
-  if (thin && swiglu)
-    hipLaunchKernelGGL((gemm_w4_kernel<ThinTile, F, true>), grid, block, 0, st, a);
-  else if (thin)
-    hipLaunchKernelGGL((gemm_w4_kernel<ThinTile, F, false>), grid, block, 0, st, a);
-  else if (swiglu)
-    hipLaunchKernelGGL((gemm_w4_kernel<DecodeTile, F, true>), grid, block, 0, st, a);
+template <class T, class F>
+hipError_t launch_tile(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
+  const int64_t nt = (a.g.N + T::COLS - 1) / T::COLS, El = a.g.s.n_experts;
+  const int64_t items = (int64_t(a.g.m_total) / T::ROWS + El) * nt + El;   // upper bound
+  const int64_t most = (T::SPLIT > 1 ? 4 : 2) * (int64_t)num_cus;
+  const int64_t g = items < most ? items : most;
+  const dim3 grid((int)((g + 7) / 8 * 8)), block(kW4Threads);
+  if (swiglu)
+    hipLaunchKernelGGL((gemm_w4_kernel<T, F, true>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((gemm_w4_kernel<DecodeTile, F, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((gemm_w4_kernel<T, F, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
-template <int CODES, int GROUP>
-hipError_t launch(const W4Args& a, bool swiglu, bool thin, dim3 grid, hipStream_t st) {
-  return a.scale_f16 ? launch<Format<CODES, GROUP, true>>(a, swiglu, thin, grid, st)
-                     : launch<Format<CODES, GROUP, false>>(a, swiglu, thin, grid, st);
+template <class F>
+hipError_t launch(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
+  // The decode tile where the experts that can have rows make two of them a CU (what
+  // a CU holds at once), half as wide a one where they do not, and the thin one where
+  // besides most experts fit its 16 rows.
+  const int64_t El = a.g.s.n_experts, m = a.g.m_total, active = m < El ? m : El;
+  const int64_t tiles = active * ((a.g.N + DecodeTile::COLS - 1) / DecodeTile::COLS);
+  if (tiles >= 2 * num_cus) return launch_tile<DecodeTile, F>(a, swiglu, num_cus, st);
+  if (m > 8 * El) return launch_tile<NarrowTile, F>(a, swiglu, num_cus, st);
+  return launch_tile<ThinTile, F>(a, swiglu, num_cus, st);
 }
 
-// Upper bound of the work items of a launch with this tile.
-template <class T>
-int64_t work_items(const W4Args& a) {
-  const int64_t nt = (a.g.N + T::COLS - 1) / T::COLS, El = a.g.s.n_experts;
-  return (int64_t(a.g.m_total) / T::ROWS + El) * nt + El;
+template <int CODES, int GROUP>
+hipError_t launch(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
+  return a.scale_f16 ? launch<Format<CODES, GROUP, true>>(a, swiglu, num_cus, st)
+                     : launch<Format<CODES, GROUP, false>>(a, swiglu, num_cus, st);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_w4(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
-  // thin tiles where the experts that can have rows make fewer decode tiles than the
-  // GPU holds workgroups of them (two a CU)
-  const int64_t active = a.g.m_total < a.g.s.n_experts ? a.g.m_total : a.g.s.n_experts;
-  const bool thin = active * ((a.g.N + DecodeTile::COLS - 1) / DecodeTile::COLS) < 2 * num_cus;
-  const int64_t items = thin ? work_items<ThinTile>(a) : work_items<DecodeTile>(a);
-  const int64_t most = (thin ? 4 : 2) * (int64_t)num_cus;
-  const int64_t g = items < most ? items : most;
-  const dim3 grid((int)((g + 7) / 8 * 8));
   switch (a.codes * 1000 + a.group) {
-    case 32: return launch<EP_W4_INT4, 32>(a, swiglu, thin, grid, st);
-    case 64: return launch<EP_W4_INT4, 64>(a, swiglu, thin, grid, st);
-    case 128: return launch<EP_W4_INT4, 128>(a, swiglu, thin, grid, st);
-    case 1032: return launch<EP_W4_E2M1, 32>(a, swiglu, thin, grid, st);
-    case 1064: return launch<EP_W4_E2M1, 64>(a, swiglu, thin, grid, st);
-    case 1128: return launch<EP_W4_E2M1, 128>(a, swiglu, thin, grid, st);
+    case 32: return launch<EP_W4_INT4, 32>(a, swiglu, num_cus, st);
+    case 64: return launch<EP_W4_INT4, 64>(a, swiglu, num_cus, st);
+    case 128: return launch<EP_W4_INT4, 128>(a, swiglu, num_cus, st);
+    case 1032: return launch<EP_W4_E2M1, 32>(a, swiglu, num_cus, st);
+    case 1064: return launch<EP_W4_E2M1, 64>(a, swiglu, num_cus, st);
+    case 1128: return launch<EP_W4_E2M1, 128>(a, swiglu, num_cus, st);
   }
   return hipErrorInvalidValue;
 }
