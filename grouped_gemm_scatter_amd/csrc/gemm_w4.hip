@@ -19,6 +19,8 @@
 // blocks and the up blocks of the same outputs, so SwiGLU needs no exchange.
 // The thin tile, for launches with too few decode tiles to fill the GPU: 16 rows x 64
 // columns, every wave a quarter of K, the quarters' sums joined through LDS.
+#include <type_traits>
+
 #include "ep_combine.h"
 #include "gemm_common.h"
 
@@ -44,6 +46,25 @@ struct ThinTile {
   static constexpr int ROWS = 16, COLS = 64, SPLIT = 4, BLOCKS = 4;
 };
 
+// 1/16 of the signed integer in the low half of byte B (the compiler itself takes a
+// shift for every code).
+template <int B>
+__device__ __forceinline__ float off_i4(uint32_t v) {
+  float f;
+  if constexpr (B == 0)
+    asm("v_cvt_off_f32_i4_e32 %0, %1" : "=v"(f) : "v"(v));
+  else if constexpr (B == 1)
+    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1"
+        : "=v"(f) : "v"(v));
+  else if constexpr (B == 2)
+    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2"
+        : "=v"(f) : "v"(v));
+  else
+    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
+        : "=v"(f) : "v"(v));
+  return f;
+}
+
 // The 8 codes of a packed dword as bf16 values: e2m1 values, or (code - 8) / 16.
 template <int CODES>
 __device__ __forceinline__ bf16x8 decode8(uint32_t v) {
@@ -56,13 +77,11 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t v) {
   } else {
     // packed as two's complement nibbles, codes 0..3 in the low and 4..7 in the high
     // halves of the bytes; the conversion takes a byte's low half and gives 1/16 of it
-    bf16x8 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r[j] = (__bf16)__builtin_amdgcn_cvt_off_f32_i4((int)(v >> (8 * j)));
-      r[4 + j] = (__bf16)__builtin_amdgcn_cvt_off_f32_i4((int)((v >> 4) >> (8 * j)));
-    }
-    return r;
+    const float l0 = off_i4<0>(v), l1 = off_i4<1>(v), l2 = off_i4<2>(v), l3 = off_i4<3>(v);
+    v >>= 4;
+    const float h0 = off_i4<0>(v), h1 = off_i4<1>(v), h2 = off_i4<2>(v), h3 = off_i4<3>(v);
+    return bf16x8{(__bf16)l0, (__bf16)l1, (__bf16)l2, (__bf16)l3,
+                  (__bf16)h0, (__bf16)h1, (__bf16)h2, (__bf16)h3};
   }
 }
 
@@ -179,15 +198,19 @@ __device__ __forceinline__ void multiply_shared(f32x4 (&acc)[NT][MT], const Bloc
     for (int p = 0; p < MT; ++p)
       *reinterpret_cast<u32x4*>(put + (k & 1) * BUF + p * 4096) = xr[p];
   };
-  auto step = [&](int k, Weights<F, NT>& w) {
-    if (k + 1 < KT) put_x(k + 1);
-    if (k + 2 < KT) load_x(k + 2);
+  // FULL: the loads of the steps ahead are known to be there.  Only then does the
+  // compiler know how many loads came after the ones that it waits for; with a load
+  // under a condition it waits for all of them.
+  auto step = [&](auto full, int k, Weights<F, NT>& w) {
+    constexpr bool FULL = decltype(full)::value;
+    if (FULL || k + 1 < KT) put_x(k + 1);
+    if (FULL || k + 2 < KT) load_x(k + 2);
     const uint8_t* xb = xs + (k & 1) * BUF + (lane & 15) * 256;
     multiply_step(acc, w, [&](int j, int q) {
       return *reinterpret_cast<const bf16x8*>(xb + j * 4096 +
                                               ((4 * q + (lane >> 4)) ^ (lane & 15)) * 16);
     });
-    if (k + 3 < KT) load_weights(w, src, k + 3, lane);
+    if (FULL || k + 3 < KT) load_weights(w, src, k + 3, lane);
     lds_barrier();
   };
   load_x(0);
@@ -201,10 +224,18 @@ __device__ __forceinline__ void multiply_shared(f32x4 (&acc)[NT][MT], const Bloc
   put_x(0);
   if (KT > 1) load_x(1);
   lds_barrier();
-  for (int k = 0; k < KT; k += 3) {
-    step(k, st[0]);
-    if (k + 1 < KT) step(k + 1, st[1]);
-    if (k + 2 < KT) step(k + 2, st[2]);
+  int k = 0;
+  for (; k + 5 < KT; k += 3) {
+    step(std::true_type{}, k, st[0]);
+    step(std::true_type{}, k + 1, st[1]);
+    step(std::true_type{}, k + 2, st[2]);
+  }
+  // the last three to five steps
+#pragma unroll 1
+  for (; k < KT; k += 3) {
+    step(std::false_type{}, k, st[0]);
+    if (k + 1 < KT) step(std::false_type{}, k + 1, st[1]);
+    if (k + 2 < KT) step(std::false_type{}, k + 2, st[2]);
   }
 }
 
@@ -233,14 +264,17 @@ __device__ __forceinline__ void multiply_thin(f32x4 (&acc)[NT][1], const Blocks<
   for (int i = 0; i < NT; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (k0 < k1) load(a, k0);
   if (k0 + 1 < k1) load(b, k0 + 1);
-  for (int k = k0; k < k1; k += 2) {
+  int k = k0;
+  for (; k + 3 < k1; k += 2) {
     multiply(a);
-    if (k + 2 < k1) load(a, k + 2);
-    if (k + 1 < k1) {
-      multiply(b);
-      if (k + 3 < k1) load(b, k + 3);
-    }
+    load(a, k + 2);
+    multiply(b);
+    load(b, k + 3);
   }
+  if (k < k1) multiply(a);
+  if (k + 2 < k1) load(a, k + 2);
+  if (k + 1 < k1) multiply(b);
+  if (k + 2 < k1) multiply(a);
 }
 
 // Staged output rows: lane L holds rows 4 (L / 16) + 0..3 of column L % 16 of a block.
