@@ -706,8 +706,9 @@ int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format, const 
   if (h->p.dtype != EP_DTYPE_BF16) return EP_ERR_UNSUPPORTED;
   const int hidden = h->p.hidden_n, inter = h->p.hidden_k;
   if (inter % 128) return EP_ERR_UNSUPPORTED;
-  // 32-bit byte offsets inside X1
+  // 32-bit byte offsets inside X1 and one expert's codes and scales
   if (uint64_t(m_total) * hidden * 2 >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
+  if (uint64_t(inter) * hidden >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
   if (!on_device(h)) return EP_ERR_INVALID_ARG;
 
   ep::W4Args a{};

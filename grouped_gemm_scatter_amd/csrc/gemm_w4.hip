@@ -19,8 +19,6 @@
 // blocks and the up blocks of the same outputs, so SwiGLU needs no exchange.
 // The thin tile, for launches with too few decode tiles to fill the GPU: 16 rows x 64
 // columns, every wave a quarter of K, the quarters' sums joined through LDS.
-#include <type_traits>
-
 #include "ep_combine.h"
 #include "gemm_common.h"
 
@@ -110,21 +108,61 @@ struct Weights {
   typename F::word s[NT];
 };
 
-// Where a wave's column blocks are (wave-uniform): first 1 KB run and first scales.
+// Loads through buffer descriptors: the address is a scalar base and offset plus one
+// 32-bit offset a lane, which all blocks and steps share.  (64-bit addresses of every
+// block kept so many registers that some spilled, and a reload in the K loop waits for
+// the weights in flight.)
+typedef __amdgpu_buffer_rsrc_t buffer;
+__device__ __forceinline__ buffer make_buffer(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)0xffffffff, 0x00020000);
+}
+constexpr int kNontemporal = 2;
+__device__ __forceinline__ u32x4 buffer_load16(buffer b, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, 0));
+}
+__device__ __forceinline__ u32x4 buffer_load16_nt(buffer b, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(u32x4,
+                            __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, kNontemporal));
+}
+__device__ __forceinline__ void buffer_load_to(uint16_t& v, buffer b, uint32_t vo, uint32_t so) {
+  v = __builtin_amdgcn_raw_buffer_load_b16(b, vo, so, 0);
+}
+__device__ __forceinline__ void buffer_load_to(uint32_t& v, buffer b, uint32_t vo, uint32_t so) {
+  v = __builtin_amdgcn_raw_buffer_load_b32(b, vo, so, 0);
+}
+__device__ __forceinline__ void buffer_load_to(uint64_t& v, buffer b, uint32_t vo, uint32_t so) {
+  v = __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(b, vo, so, 0));
+}
+
+// Where a wave's column blocks are: an expert's codes and scales, and the wave-uniform
+// number of each block's first run of 1 KB.
 template <int NT>
 struct Blocks {
-  const uint8_t* w[NT];
-  const uint16_t* s[NT];
+  buffer w, s;
+  uint32_t run[NT];
 };
 
 template <class F, int NT>
 __device__ __forceinline__ void load_weights(Weights<F, NT>& st, const Blocks<NT>& src, int kt,
                                              int lane) {
-  typedef typename F::word word;
+  constexpr uint32_t SB = 16 * (128 / F::GROUP) * 2;   // scale bytes of a run
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    st.w[i] = load16_nt(src.w[i] + (size_t)kt * 1024 + lane * 16);
-    st.s[i] = reinterpret_cast<const word*>(src.s[i] + (size_t)kt * 16 * (128 / F::GROUP))[lane & 15];
+    const uint32_t run = src.run[i] + kt;
+    st.w[i] = buffer_load16_nt(src.w, lane * 16, run * 1024);
+    buffer_load_to(st.s[i], src.s, (lane & 15) * (SB / 16), run * SB);
+  }
+}
+
+// acc += scale * part, for one block.  The sums are made here: left free, the compiler
+// sinks them past the next branch and keeps every `part` of a step in registers.
+template <int MT>
+__device__ __forceinline__ void add_group(f32x4 (&acc)[MT], const f32x4 (&part)[MT], float sc) {
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(sc, part[j][r], acc[j][r]);
+    asm volatile("" : "+v"(acc[j]));
   }
 }
 
@@ -133,36 +171,53 @@ template <class F, int MT, int NT, class X>
 __device__ __forceinline__ void multiply_step(f32x4 (&acc)[NT][MT], const Weights<F, NT>& st,
                                               X x) {
   constexpr int SPT = 128 / F::GROUP, QPS = 4 / SPT;    // scales of a row per 128 k; quarters a scale
+  // column blocks at a time: all of them against X fragments held for a whole group, or
+  // where those are many, two against fragments read a quarter at a time
+  constexpr int IB = QPS * MT > 8 ? 2 : NT;
 #pragma unroll
-  for (int s = 0; s < SPT; ++s) {
-    bf16x8 xf[MT][QPS];
+  for (int i0 = 0; i0 < NT; i0 += IB)
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
+    for (int s = 0; s < SPT; ++s) {
+      if constexpr (IB < NT) {
+        f32x4 part[IB][MT];
 #pragma unroll
-      for (int q = 0; q < QPS; ++q) xf[j][q] = x(j, s * QPS + q);
+        for (int q = 0; q < QPS; ++q) {
+          bf16x8 xf[MT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      f32x4 part[MT];
+          for (int j = 0; j < MT; ++j) xf[j] = x(j, s * QPS + q);
 #pragma unroll
-      for (int j = 0; j < MT; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int i = 0; i < IB; ++i) {
+            const bf16x8 wf = decode8<F::CODES>(st.w[i0 + i][s * QPS + q]);
 #pragma unroll
-      for (int q = 0; q < QPS; ++q) {
-        const bf16x8 wf = decode8<F::CODES>(st.w[i][s * QPS + q]);
+            for (int j = 0; j < MT; ++j)
+              part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  xf[j], wf, q ? part[i][j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < IB; ++i)
+          add_group(acc[i0 + i], part[i], F::scale((uint16_t)(st.s[i0 + i] >> (16 * s))));
+      } else {
+        bf16x8 xf[MT][QPS];
 #pragma unroll
         for (int j = 0; j < MT; ++j)
-          part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][q], wf, part[j], 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < QPS; ++q) xf[j][q] = x(j, s * QPS + q);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          f32x4 part[MT];
+#pragma unroll
+          for (int q = 0; q < QPS; ++q) {
+            const bf16x8 wf = decode8<F::CODES>(st.w[i][s * QPS + q]);
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+              part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  xf[j][q], wf, q ? part[j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+          }
+          add_group(acc[i], part, F::scale((uint16_t)(st.s[i] >> (16 * s))));
+        }
       }
-      const float sc = F::scale((uint16_t)(st.s[i] >> (16 * s)));
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(sc, part[j][r], acc[i][j][r]);
-      // the sums are made here: left free, the compiler sinks them past the next branch
-      // and keeps every `part` of the step in registers until then
-#pragma unroll
-      for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[i][j]));
     }
-  }
 }
 
 // Waits for this wave's LDS accesses only, then for the workgroup: loads from global
@@ -181,7 +236,7 @@ __device__ __forceinline__ void lds_barrier() {
 // steps are in registers or on their way.
 template <class F, int MT, int NT>
 __device__ __forceinline__ void multiply_shared(f32x4 (&acc)[NT][MT], const Blocks<NT>& src,
-                                                const uint8_t* x, const uint32_t (&xoff)[MT],
+                                                buffer x, const uint32_t (&xoff)[MT],
                                                 uint8_t* xs, int KT, int tid) {
   constexpr int BUF = MT * 4096;
   const int lane = tid & 63, row = tid >> 4;
@@ -189,53 +244,45 @@ __device__ __forceinline__ void multiply_shared(f32x4 (&acc)[NT][MT], const Bloc
   u32x4 xr[MT];
   Weights<F, NT> st[3];
   auto load_x = [&](int k) {
-    const uint8_t* xk = x + (size_t)k * 256;
 #pragma unroll
-    for (int p = 0; p < MT; ++p) xr[p] = load16(xk + xoff[p]);
+    for (int p = 0; p < MT; ++p) xr[p] = buffer_load16(x, xoff[p], k * 256);
   };
   auto put_x = [&](int k) {
 #pragma unroll
     for (int p = 0; p < MT; ++p)
       *reinterpret_cast<u32x4*>(put + (k & 1) * BUF + p * 4096) = xr[p];
   };
-  // FULL: the loads of the steps ahead are known to be there.  Only then does the
-  // compiler know how many loads came after the ones that it waits for; with a load
-  // under a condition it waits for all of them.
-  auto step = [&](auto full, int k, Weights<F, NT>& w) {
-    constexpr bool FULL = decltype(full)::value;
-    if (FULL || k + 1 < KT) put_x(k + 1);
-    if (FULL || k + 2 < KT) load_x(k + 2);
+  // The loads ahead are unconditional, past the end those of the last step again: with a
+  // load under a condition the compiler does not know how many came after the one
+  // that it waits for, and waits for all.
+  auto step = [&](int k, Weights<F, NT>& w) {
+    put_x(k + 1);
+    load_x(min(k + 2, KT - 1));
     const uint8_t* xb = xs + (k & 1) * BUF + (lane & 15) * 256;
     multiply_step(acc, w, [&](int j, int q) {
       return *reinterpret_cast<const bf16x8*>(xb + j * 4096 +
                                               ((4 * q + (lane >> 4)) ^ (lane & 15)) * 16);
     });
-    if (FULL || k + 3 < KT) load_weights(w, src, k + 3, lane);
+    load_weights(w, src, min(k + 3, KT - 1), lane);
     lds_barrier();
   };
   load_x(0);
 #pragma unroll
-  for (int d = 0; d < 3; ++d)
-    if (d < KT) load_weights(st[d], src, d, lane);
+  for (int d = 0; d < 3; ++d) load_weights(st[d], src, min(d, KT - 1), lane);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   put_x(0);
-  if (KT > 1) load_x(1);
+  load_x(min(1, KT - 1));
   lds_barrier();
-  int k = 0;
-  for (; k + 5 < KT; k += 3) {
-    step(std::true_type{}, k, st[0]);
-    step(std::true_type{}, k + 1, st[1]);
-    step(std::true_type{}, k + 2, st[2]);
-  }
-  // the last three to five steps
-#pragma unroll 1
-  for (; k < KT; k += 3) {
-    step(std::false_type{}, k, st[0]);
-    if (k + 1 < KT) step(std::false_type{}, k + 1, st[1]);
-    if (k + 2 < KT) step(std::false_type{}, k + 2, st[2]);
+  for (int k = 0;;) {
+    step(k, st[0]);
+    if (++k >= KT) break;
+    step(k, st[1]);
+    if (++k >= KT) break;
+    step(k, st[2]);
+    if (++k >= KT) break;
   }
 }
 
@@ -248,33 +295,31 @@ struct ThinStep {
 
 template <class F, int NT>
 __device__ __forceinline__ void multiply_thin(f32x4 (&acc)[NT][1], const Blocks<NT>& src,
-                                              const uint8_t* x, uint32_t xoff, int k0, int k1,
+                                              buffer x, uint32_t xoff, int k0, int k1,
                                               int lane) {
   ThinStep<F, NT> a, b;
   auto load = [&](ThinStep<F, NT>& st, int k) {
     load_weights(st.w, src, k, lane);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      st.x[q] = __builtin_bit_cast(bf16x8, load16(x + (size_t)k * 256 + xoff + q * 64));
+      st.x[q] = __builtin_bit_cast(bf16x8, buffer_load16(x, xoff + q * 64, k * 256));
   };
   auto multiply = [&](const ThinStep<F, NT>& st) {
     multiply_step(acc, st.w, [&](int, int q) { return st.x[q]; });
   };
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (k0 < k1) load(a, k0);
-  if (k0 + 1 < k1) load(b, k0 + 1);
-  int k = k0;
-  for (; k + 3 < k1; k += 2) {
+  if (k0 >= k1) return;
+  load(a, k0);
+  load(b, min(k0 + 1, k1 - 1));
+  for (int k = k0;;) {
     multiply(a);
-    load(a, k + 2);
+    load(a, min(k + 2, k1 - 1));
+    if (++k >= k1) break;
     multiply(b);
-    load(b, k + 3);
+    load(b, min(k + 2, k1 - 1));
+    if (++k >= k1) break;
   }
-  if (k < k1) multiply(a);
-  if (k + 2 < k1) load(a, k + 2);
-  if (k + 1 < k1) multiply(b);
-  if (k + 2 < k1) multiply(a);
 }
 
 // Staged output rows: lane L holds rows 4 (L / 16) + 0..3 of column L % 16 of a block.
@@ -311,22 +356,24 @@ __device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t
   // the wave's first output block of the tile, and its weight blocks
   const int ob = SWIGLU ? first / 2 : first;
   Blocks<NT> src;
+  const size_t first_run = (size_t)t.e * NB * KT;
+  src.w = make_buffer(a.w + first_run * 1024);
+  src.s = make_buffer(wa.scales + first_run * (16 * (128 / F::GROUP)));
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     int nb = SWIGLU ? tile * (PER / 2) + ob + (i % (NT / 2)) + (i / (NT / 2)) * (NB / 2)
                     : tile * PER + ob + i;
     if constexpr (!SWIGLU) nb = min(nb, NB - 1);     // past the last column: not stored
-    const size_t blk = ((size_t)t.e * NB + nb) * KT;
-    src.w[i] = a.w + blk * 1024;
-    src.s[i] = wa.scales + blk * (16 * (128 / F::GROUP));
+    src.run[i] = (uint32_t)nb * KT;
   }
+  const buffer x = make_buffer(a.x);
   // rows past m_end read the group's last row; they are not stored
   auto row_offset = [&](int r) { return (uint32_t)min(t.m_abs + r, t.g1 - 1) * (uint32_t)(a.K * 2); };
   f32x4 acc[NT][MT];
   if constexpr (T::SPLIT > 1) {
     static_assert(T::SPLIT == kW4Waves && NT == kW4Waves && MT == 1, "one block a wave at the end");
     // the wave's share of K
-    multiply_thin<F>(acc, src, a.x, row_offset(lane & 15) + (lane >> 4) * 16,
+    multiply_thin<F>(acc, src, x, row_offset(lane & 15) + (lane >> 4) * 16,
                      wave * KT / T::SPLIT, (wave + 1) * KT / T::SPLIT, lane);
     // wave w adds up block w of all shares, in the order of k
     __shared__ f32x4 s_part[T::SPLIT][NT][64];
@@ -347,7 +394,7 @@ __device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t
     uint32_t xoff[MT];
 #pragma unroll
     for (int p = 0; p < MT; ++p) xoff[p] = row_offset(p * 16 + (tid >> 4)) + (tid & 15) * 16;
-    multiply_shared<F>(acc, src, a.x, xoff, xs, KT, tid);
+    multiply_shared<F>(acc, src, x, xoff, xs, KT, tid);
     if constexpr (SWIGLU) {
 #pragma unroll
       for (int i = 0; i < NT / 2; ++i) {
