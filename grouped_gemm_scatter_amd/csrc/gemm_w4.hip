@@ -33,19 +33,18 @@ constexpr int kW4Threads = 256;
 constexpr int kW4Waves = kW4Threads / 64;
 
 // Tile of a launch: ROWS x COLS GEMM columns, K split over SPLIT waves, BLOCKS
-// 16-column blocks a wave.
+// 16-column blocks a wave, PER_CU workgroups resident on a CU.
 struct DecodeTile {
-  static constexpr int ROWS = 64, COLS = 256, SPLIT = 1, BLOCKS = 4;
+  static constexpr int ROWS = 64, COLS = 256, SPLIT = 1, BLOCKS = 4, PER_CU = 2;
 };
 struct NarrowTile {
-  static constexpr int ROWS = 64, COLS = 128, SPLIT = 1, BLOCKS = 2;
+  static constexpr int ROWS = 64, COLS = 128, SPLIT = 1, BLOCKS = 2, PER_CU = 2;
 };
 struct ThinTile {
-  static constexpr int ROWS = 16, COLS = 64, SPLIT = 4, BLOCKS = 4;
+  static constexpr int ROWS = 16, COLS = 64, SPLIT = 4, BLOCKS = 4, PER_CU = 4;
 };
 
-// 1/16 of the signed integer in the low half of byte B (the compiler itself takes a
-// shift for every code).
+// 1/16 of the signed integer in the low half of byte B.
 template <int B>
 __device__ __forceinline__ float off_i4(uint32_t v) {
   float f;
@@ -64,6 +63,11 @@ __device__ __forceinline__ float off_i4(uint32_t v) {
 }
 
 // The 8 codes of a packed dword as bf16 values: e2m1 values, or (code - 8) / 16.
+// Both are exact: 4 conversions for e2m1, for int4 a shift, 8 conversions (the
+// instruction takes a byte's low half; written out, because the compiler takes a shift
+// for every code instead of selecting the byte) and 4 roundings of exact numbers.
+// (int4 as unsigned codes through the fp8 conversion, 7 instructions, with -8 sum x
+// from one more MFMA for each X fragment: the same time within 2%, and inexact zeros.)
 template <int CODES>
 __device__ __forceinline__ bf16x8 decode8(uint32_t v) {
   if constexpr (CODES == EP_W4_E2M1) {
@@ -73,8 +77,8 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t v) {
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.f, 3);
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
   } else {
-    // packed as two's complement nibbles, codes 0..3 in the low and 4..7 in the high
-    // halves of the bytes; the conversion takes a byte's low half and gives 1/16 of it
+    // packed as two's complement, codes 0..3 in the low and 4..7 in the high halves of
+    // the bytes
     const float l0 = off_i4<0>(v), l1 = off_i4<1>(v), l2 = off_i4<2>(v), l3 = off_i4<3>(v);
     v >>= 4;
     const float h0 = off_i4<0>(v), h1 = off_i4<1>(v), h2 = off_i4<2>(v), h3 = off_i4<3>(v);
@@ -94,10 +98,9 @@ struct Format {
   static constexpr int CODES = CODES_, GROUP = GROUP_;
   typedef typename ScaleWord<128 / GROUP>::type word;
   static __device__ __forceinline__ float scale(uint16_t s) {
-    float v;
-    if constexpr (F16) v = (float)__builtin_bit_cast(_Float16, s);
-    else v = bf16_lo(s);
-    return CODES == EP_W4_INT4 ? 16.f * v : v;
+    constexpr float m = CODES == EP_W4_INT4 ? 16.f : 1.f;    // decode8's 1/16
+    if constexpr (F16) return m * (float)__builtin_bit_cast(_Float16, s);
+    return m * bf16_lo(s);
   }
 };
 
@@ -171,14 +174,16 @@ template <class F, int MT, int NT, class X>
 __device__ __forceinline__ void multiply_step(f32x4 (&acc)[NT][MT], const Weights<F, NT>& st,
                                               X x) {
   constexpr int SPT = 128 / F::GROUP, QPS = 4 / SPT;    // scales of a row per 128 k; quarters a scale
-  // column blocks at a time: all of them against X fragments held for a whole group, or
-  // where those are many, two against fragments read a quarter at a time
-  constexpr int IB = QPS * MT > 8 ? 2 : NT;
+  // X fragments of a whole group for all blocks, or where those are many, of a quarter
+  // at a time for two column blocks
+  constexpr bool BY_QUARTER = QPS > 1 && (NT == 2 || QPS * MT > 8);
+  constexpr int IB = BY_QUARTER ? 2 : NT;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i0 = 0; i0 < NT; i0 += IB)
 #pragma unroll
     for (int s = 0; s < SPT; ++s) {
-      if constexpr (IB < NT) {
+      if constexpr (BY_QUARTER) {
         f32x4 part[IB][MT];
 #pragma unroll
         for (int q = 0; q < QPS; ++q) {
@@ -191,7 +196,7 @@ __device__ __forceinline__ void multiply_step(f32x4 (&acc)[NT][MT], const Weight
 #pragma unroll
             for (int j = 0; j < MT; ++j)
               part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  xf[j], wf, q ? part[i][j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+                  xf[j], wf, q ? part[i][j] : zero, 0, 0, 0);
           }
         }
 #pragma unroll
@@ -211,8 +216,8 @@ __device__ __forceinline__ void multiply_step(f32x4 (&acc)[NT][MT], const Weight
             const bf16x8 wf = decode8<F::CODES>(st.w[i][s * QPS + q]);
 #pragma unroll
             for (int j = 0; j < MT; ++j)
-              part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  xf[j][q], wf, q ? part[j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+              part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j][q], wf, q ? part[j] : zero,
+                                                                0, 0, 0);
           }
           add_group(acc[i], part, F::scale((uint16_t)(st.s[i] >> (16 * s))));
         }
@@ -345,8 +350,11 @@ __device__ __forceinline__ void swiglu(f32x4 (&g)[MT], const f32x4 (&u)[MT]) {
 // The products of one tile with MT 16-row blocks, staged in LDS as bf16 rows.
 template <class T, class F, bool SWIGLU, int MT>
 __device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t, uint8_t* smem,
-                                             int pitch, uint8_t* xs, int tid, int wave) {
+                                             int pitch, int tid, int wave) {
   const GemmArgs& a = wa.g;
+  // opaque, so that what derives from it is computed for each tile, not kept for every
+  // tile shape across the others' K loops
+  asm volatile("" : "+v"(tid));
   const int lane = tid & 63;
   const int KT = a.K / 128, NB = a.N / 16;
   constexpr int PER = T::COLS / 16;                  // blocks of a tile
@@ -394,7 +402,7 @@ __device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t
     uint32_t xoff[MT];
 #pragma unroll
     for (int p = 0; p < MT; ++p) xoff[p] = row_offset(p * 16 + (tid >> 4)) + (tid & 15) * 16;
-    multiply_shared<F>(acc, src, x, xoff, xs, KT, tid);
+    multiply_shared<F>(acc, src, x, xoff, smem, KT, tid);
     if constexpr (SWIGLU) {
 #pragma unroll
       for (int i = 0; i < NT / 2; ++i) {
@@ -409,11 +417,12 @@ __device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t
 }
 
 template <class T, class F, bool SWIGLU>
-__global__ __launch_bounds__(kW4Threads, 2) void gemm_w4_kernel(W4Args wa) {
+__global__ __launch_bounds__(kW4Threads, T::PER_CU) void gemm_w4_kernel(W4Args wa) {
   constexpr int OUT = SWIGLU ? T::COLS / 2 : T::COLS;  // output columns of a tile
   constexpr int PITCH = OUT * 2 + 16;                // bytes per staged output row
-  __shared__ __attribute__((aligned(16))) uint8_t smem[T::ROWS * PITCH];
-  __shared__ __attribute__((aligned(16))) uint8_t s_x[T::SPLIT > 1 ? 16 : 2 * T::ROWS * 256];
+  // the X rows on their way to the MFMAs, and after the K loop the finished tile
+  constexpr int X_BYTES = T::SPLIT > 1 ? 0 : 2 * T::ROWS * 256, C_BYTES = T::ROWS * PITCH;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[X_BYTES > C_BYTES ? X_BYTES : C_BYTES];
   __shared__ uint64_t s_rowdst[T::ROWS];
   __shared__ int s_base[kMaxLocalExperts + 1];
   __shared__ int s_gbeg[kMaxLocalExperts + 1];
@@ -436,19 +445,23 @@ __global__ __launch_bounds__(kW4Threads, 2) void gemm_w4_kernel(W4Args wa) {
                                              &s_bad))
     return;
   const int total = s_base[El];
-  const int G = gridDim.x, per_xcd = G >> 3;         // G is a multiple of 8
+  const int per_xcd = gridDim.x >> 3;                // the grid is a multiple of 8
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   PendingTiles pending;
   pending.done = s_done;
   pending.e = s_pend;
   pending.base = s_base;
 
-  for (int round = 0;; ++round) {
-    const int item = round * G + xcd * per_xcd + slot;
-    if (item >= total) break;
+  // each XCD (workgroups go round-robin over the eight) takes an equal run of the items,
+  // its workgroups in turn
+  const int end = (int)((int64_t)(xcd + 1) * total / 8);
+  for (int item = (int)((int64_t)xcd * total / 8) + slot; item < end; item += per_xcd) {
     TileWork t = tile_of<T::ROWS, T::COLS>(a, s_base, s_gbeg, item);
     t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.g1 = __builtin_amdgcn_readfirstlane(t.g1);
+    t.m_abs = __builtin_amdgcn_readfirstlane(t.m_abs);
     t.n_abs = __builtin_amdgcn_readfirstlane(t.n_abs);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
     if (t.empty) {
       signal_empty_expert(a, t.e, pending);
       continue;
@@ -457,24 +470,21 @@ __global__ __launch_bounds__(kW4Threads, 2) void gemm_w4_kernel(W4Args wa) {
       wait_vm<0>();
       prologue_barrier<true>(a, pending);
     }
-    const RowInfo ri =
-        tid < T::ROWS ? load_row_info(a, t.e, t.g1, t.m_abs + tid) : RowInfo{-1, 0, 0};
-    const int mt = __builtin_amdgcn_readfirstlane((t.rows + 15) / 16);
-    if constexpr (T::ROWS == 16) {
-      tile_product<T, F, SWIGLU, 1>(wa, t, smem, PITCH, s_x, tid, wave);
-    } else {
-      if (mt == 1)
-        tile_product<T, F, SWIGLU, 1>(wa, t, smem, PITCH, s_x, tid, wave);
-      else if (mt == 2)
-        tile_product<T, F, SWIGLU, 2>(wa, t, smem, PITCH, s_x, tid, wave);
-      else if (mt == 3)
-        tile_product<T, F, SWIGLU, 3>(wa, t, smem, PITCH, s_x, tid, wave);
-      else
-        tile_product<T, F, SWIGLU, 4>(wa, t, smem, PITCH, s_x, tid, wave);
-    }
     if constexpr (!SWIGLU) {
-      if (tid < T::ROWS) s_rowdst[tid] = row_destination(a, s_recv, ri, t.m_abs + tid);
+      // ready long before the tile is: kept in LDS, not in registers across the K loop
+      if (tid < T::ROWS)
+        s_rowdst[tid] = row_destination(a, s_recv, load_row_info(a, t.e, t.g1, t.m_abs + tid),
+                                        t.m_abs + tid);
     }
+    const int mt = (t.rows + 15) / 16;
+    if (T::ROWS == 16 || mt == 1)
+      tile_product<T, F, SWIGLU, 1>(wa, t, smem, PITCH, tid, wave);
+    else if (mt == 2)
+      tile_product<T, F, SWIGLU, T::ROWS == 16 ? 1 : 2>(wa, t, smem, PITCH, tid, wave);
+    else if (mt == 3)
+      tile_product<T, F, SWIGLU, T::ROWS == 16 ? 1 : 3>(wa, t, smem, PITCH, tid, wave);
+    else
+      tile_product<T, F, SWIGLU, T::ROWS == 16 ? 1 : 4>(wa, t, smem, PITCH, tid, wave);
     __syncthreads();
     const int col0 = t.n_abs / T::COLS * OUT;
     if (SWIGLU || !a.sink_on) {
@@ -545,7 +555,7 @@ template <class T, class F>
 hipError_t launch_tile(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
   const int64_t nt = (a.g.N + T::COLS - 1) / T::COLS, El = a.g.s.n_experts;
   const int64_t items = (int64_t(a.g.m_total) / T::ROWS + El) * nt + El;   // upper bound
-  const int64_t most = (T::SPLIT > 1 ? 4 : 2) * (int64_t)num_cus;
+  const int64_t most = T::PER_CU * (int64_t)num_cus;
   const int64_t g = items < most ? items : most;
   const dim3 grid((int)((g + 7) / 8 * 8)), block(kW4Threads);
   if (swiglu)
@@ -557,9 +567,6 @@ hipError_t launch_tile(const W4Args& a, bool swiglu, int num_cus, hipStream_t st
 
 template <class F>
 hipError_t launch(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
-  // The decode tile where the experts that can have rows make two of them a CU (what
-  // a CU holds at once), half as wide a one where they do not, and the thin one where
-  // besides most experts fit its 16 rows.
   const int64_t El = a.g.s.n_experts, m = a.g.m_total, active = m < El ? m : El;
   const int64_t tiles = active * ((a.g.N + DecodeTile::COLS - 1) / DecodeTile::COLS);
   if (tiles >= 2 * num_cus) return launch_tile<DecodeTile, F>(a, swiglu, num_cus, st);
