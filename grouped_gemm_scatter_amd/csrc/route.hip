@@ -1,15 +1,19 @@
 // Routing to experts: scores, the group limit, top-k picks and their weights for
 // every token, and the gradient of the weights with respect to the logits.
-// One wave per token; lane L holds VPL consecutive experts from L * VPL, so that the
-// lowest lane holds the lowest index of a tie.
+// LPT lanes per token, 64 or, where there are many tokens, 16 (four tokens a wave; up to
+// 256 experts, 16 groups and 16 picks); lane L of them holds VPL consecutive experts from
+// L * VPL, so that the lowest lane holds the lowest index of a tie.
 //
 // Which experts are picked is exact.  Without a bias the choice is the order of the
 // logits themselves.  Where a score is compared (a bias, a sum of two) it is defined in
 // binary64, but computed in binary32 first with a bound on the error: only a token in
 // which two choices next to each other, or the groups at the limit, lie within that
-// bound is chosen again in binary64, in a few tokens of a thousand.
-// A pick: the largest key of every lane, the largest of the wave by six cross-lane
-// moves, the lowest lane that has it by a ballot.
+// bound is chosen again in binary64, a few tokens of a thousand: in the same kernel
+// where tokens are few, in a second one where they are many, since the registers of
+// the binary64 path would leave the first kernel two waves a SIMD.
+// A pick: the largest key of every lane, the largest of the token by cross-lane moves,
+// the lowest lane that has it from a ballot's lowest bit.  It is bound by its instructions,
+// about 70 a pick whatever LPT is, so four tokens share them where they fit.
 //
 // The weights are binary32.  Renormalised softmax weights are a softmax over the
 // picked logits; renormalised sigmoid weights use
@@ -50,28 +54,22 @@ template <int VPL>
 __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int lane, float (&x)[VPL]) {
   const int E = a.n_experts, first = lane * VPL;
   const int64_t at = t * E + first;
-  if (VPL >= 2 && E % VPL == 0) {
+  if (E % VPL == 0) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) x[j] = -INFINITY;
     if (first >= E) return;
     if (a.dtype == EP_LOGITS_F32) {
       const float* p = reinterpret_cast<const float*>(a.logits) + at;
-      if constexpr (VPL == 2) {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) x[j] = clean(__uint_as_float(v[j]));
-      } else {
+      for (int j = 0; j < VPL / 4; ++j) {
+        const u32x4 v = load16(p + 4 * j);
 #pragma unroll
-        for (int j = 0; j < VPL / 4; ++j) {
-          const u32x4 v = load16(p + 4 * j);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x[4 * j + q] = clean(__uint_as_float(v[q]));
-        }
+        for (int q = 0; q < 4; ++q) x[4 * j + q] = clean(__uint_as_float(v[q]));
       }
     } else {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(
           reinterpret_cast<const uint16_t*>(a.logits) + at);
-      uint32_t v[VPL > 1 ? VPL / 2 : 1];
+      uint32_t v[VPL / 2];
 #pragma unroll
       for (int j = 0; j < VPL / 2; ++j) v[j] = p[j];
 #pragma unroll
@@ -89,20 +87,15 @@ __device__ __forceinline__ void store_row(const RouteArgs& a, int64_t t, int lan
   const int E = a.n_experts, first = lane * VPL;
   const int64_t at = t * E + first;
   if (first >= E) return;
-  if (VPL >= 2 && E % VPL == 0) {
+  if (E % VPL == 0) {
     if (a.dtype == EP_LOGITS_F32) {
       float* p = reinterpret_cast<float*>(a.grad_logits) + at;
-      if constexpr (VPL == 2) {
-        *reinterpret_cast<u32x2*>(p) =
-            u32x2{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1])};
-      } else {
 #pragma unroll
-        for (int j = 0; j < VPL / 4; ++j) {
-          u32x4 o;
+      for (int j = 0; j < VPL / 4; ++j) {
+        u32x4 o;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) o[q] = __builtin_bit_cast(uint32_t, v[4 * j + q]);
-          store16_nt(p + 4 * j, o);
-        }
+        for (int q = 0; q < 4; ++q) o[q] = __float_as_uint(v[4 * j + q]);
+        store16_nt(p + 4 * j, o);
       }
     } else {
       uint32_t* p = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.grad_logits) + at);
@@ -143,369 +136,442 @@ __device__ __forceinline__ float read_lane(float v, int lane) {
                             __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 
-// Over the wave, the same in every lane: within rows of 16 lanes, then rows 0 and 2
-// into 1 and 3, then the lower half into the upper, whose last lane has it all.
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, lane_move<0x111>(v, v));        // row_shr 1, 2, 4, 8
-  v = fmaxf(v, lane_move<0x112>(v, v));
-  v = fmaxf(v, lane_move<0x114>(v, v));
-  v = fmaxf(v, lane_move<0x118>(v, v));
-  v = fmaxf(v, lane_move<0x142, 0xa>(v, v));   // row_bcast 15, 31
-  v = fmaxf(v, lane_move<0x143, 0xc>(v, v));
-  return read_lane(v, 63);
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  v += lane_move<0x111>(0.f, v);
-  v += lane_move<0x112>(0.f, v);
-  v += lane_move<0x114>(0.f, v);
-  v += lane_move<0x118>(0.f, v);
-  v += lane_move<0x142, 0xa>(0.f, v);
-  v += lane_move<0x143, 0xc>(0.f, v);
-  return read_lane(v, 63);
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const double o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
-  return v;
-}
-
-// The largest value over the wave and its lowest index.
-__device__ __forceinline__ void wave_best(double& v, int& i) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const double ov = __shfl_xor(v, d);
-    const int oi = __shfl_xor(i, d);
-    if (ov > v || (ov == v && oi < i)) {
-      v = ov;
-      i = oi;
-    }
+// Reductions over the LPT lanes of a token, the same result in each of them: 16 lanes are
+// a row of the data-parallel moves, reduced by rotations; 64 by shifts within the rows,
+// rows 0 and 2 into 1 and 3, the lower half into the upper, and its last lane.
+template <int LPT>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (LPT == 16) {
+    v = fmaxf(v, lane_move<0x128>(v, v));        // row_ror 8, 4, 2, 1
+    v = fmaxf(v, lane_move<0x124>(v, v));
+    v = fmaxf(v, lane_move<0x122>(v, v));
+    return fmaxf(v, lane_move<0x121>(v, v));
+  } else {
+    v = fmaxf(v, lane_move<0x111>(v, v));        // row_shr 1, 2, 4, 8
+    v = fmaxf(v, lane_move<0x112>(v, v));
+    v = fmaxf(v, lane_move<0x114>(v, v));
+    v = fmaxf(v, lane_move<0x118>(v, v));
+    v = fmaxf(v, lane_move<0x142, 0xa>(v, v));   // row_bcast 15, 31
+    v = fmaxf(v, lane_move<0x143, 0xc>(v, v));
+    return read_lane(v, 63);
   }
 }
+template <int LPT>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (LPT == 16) {
+    v += lane_move<0x128>(0.f, v);
+    v += lane_move<0x124>(0.f, v);
+    v += lane_move<0x122>(0.f, v);
+    return v + lane_move<0x121>(0.f, v);
+  } else {
+    v += lane_move<0x111>(0.f, v);
+    v += lane_move<0x112>(0.f, v);
+    v += lane_move<0x114>(0.f, v);
+    v += lane_move<0x118>(0.f, v);
+    v += lane_move<0x142, 0xa>(0.f, v);
+    v += lane_move<0x143, 0xc>(0.f, v);
+    return read_lane(v, 63);
+  }
+}
+template <int LPT>
+__device__ __forceinline__ double lanes_sum(double v) {
+#pragma unroll
+  for (int d = LPT / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+// Binary64 keys hold no NaN.
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double max_move(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const int lo = (int)u, hi = (int)(u >> 32);
+  const uint32_t l = __builtin_amdgcn_update_dpp(lo, lo, CTRL, ROWS, 0xf, false);
+  const uint32_t h = __builtin_amdgcn_update_dpp(hi, hi, CTRL, ROWS, 0xf, false);
+  return larger(v, __builtin_bit_cast(double, (uint64_t)h << 32 | l));
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t l = __builtin_amdgcn_readlane((int)u, lane);
+  const uint32_t h = __builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+template <int LPT>
+__device__ __forceinline__ double lanes_max(double v) {
+  static_assert(LPT == 64, "binary64 choices take a wave per token");
+  v = max_move<0x111>(v);
+  v = max_move<0x112>(v);
+  v = max_move<0x114>(v);
+  v = max_move<0x118>(v);
+  v = max_move<0x142, 0xa>(v);
+  v = max_move<0x143, 0xc>(v);
+  return read_lane(v, 63);
+}
+// v of lane `from` of the token's lanes.
+template <int LPT, class T>
+__device__ __forceinline__ T of_lane(T v, int from) {
+  if constexpr (LPT == 16) return __shfl(v, (int)(threadIdx.x & 48) + from);
+  else return read_lane(v, from);
+}
+// Whether this is the lowest lane of its token for which `is` holds (it holds for one
+// at least in each token of the wave).
+template <int LPT>
+__device__ __forceinline__ bool lowest_lane(bool is) {
+  const uint64_t m = __ballot(is);
+  // the lowest bit of each 16 (a nonzero field's ~m + 1 does not carry), or of all
+  const uint64_t low = m & (~m + (LPT == 16 ? 0x0001000100010001ull : 1ull));
+  return low >> (threadIdx.x & 63) & 1;
+}
 
-constexpr int kNone = 0x7fffffff;
+// e^x for x <= 88 within 2 * 2^-23 of itself (0 below 2^-126): 2^t for t = x log2(e)
+// rounded, times 1 + the rounding's part.
+__device__ __forceinline__ float exp_near(float x) {
+  x = fmaxf(x, -200.f);
+  const float t = x * 0x1.715476p0f;                       // log2(e) to 24 bits
+  const float r = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p0f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e * r, 0x1.62e43p-1f, e);          // ln 2
+}
 
 // Shares of the picks, lane k holding pick k's logit l (there: lane k has a pick):
 // softmax over the picks, or their sigmoids over the sum.
+template <int LPT>
 __device__ __forceinline__ float pick_share(float l, bool there, int score) {
   const float low = score == EP_SCORE_SIGMOID ? fminf(l, 0.f) : l;
-  const float top = wave_max(there ? low : -FLT_MAX);
+  const float top = lanes_max<LPT>(there ? low : -FLT_MAX);
   float e = there ? expf(low - top) : 0.f;
   if (score == EP_SCORE_SIGMOID) e /= 1.f + expf(-fabsf(l));
-  const float sum = wave_sum(e);
+  const float sum = lanes_sum<LPT>(e);
   return there ? e / sum : 0.f;
 }
 
-// The picks of one token in binary64, lane k's id (or -1) in lane k: the definition,
-// reduced over the wave group by group and pick by pick.
+// Bias of the lane's experts: 0 without one, -infinity for an expert that it keeps out.
 template <int VPL>
-__device__ __forceinline__ int pick_binary64(const RouteArgs& a, int lane, const float (&x)[VPL],
-                                             float top) {
-  const int E = a.n_experts, per = E / a.n_groups;
-  const bool top2 = a.n_groups > 1 && a.group_score == EP_GROUP_TOP2;
-  double c[VPL], s[VPL];           // choice, score (with bias)
-  double sum = 0.;
+__device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&b)[VPL]) {
+  const int first = lane * VPL;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const double l = x[j];
-    s[j] = a.score == EP_SCORE_SOFTMAX ? exp(l - top) : 1. / (1. + exp(-l));
-    sum += s[j];
-  }
-  if (a.score == EP_SCORE_SOFTMAX) {
-    sum = wave_sum(sum);
+  for (int j = 0; j < VPL; ++j) b[j] = 0.f;
+  if (!a.bias) return;
+  if (a.n_experts % VPL == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0) {
+    if (first < a.n_experts) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) s[j] = sum > 0. ? s[j] / sum : 0.;
-  }
+      for (int j = 0; j < VPL / 4; ++j) {
+        const u32x4 v = load16(a.bias + first + 4 * j);
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int i = lane * VPL + j;
-    bool there = x[j] > -INFINITY;
-    if (a.bias) {
-      const float b = i < E ? a.bias[i] : 0.f;
-      there = there && b > -INFINITY;
-      s[j] += b;
-      c[j] = there ? s[j] : -INFINITY;
-    } else {
-      c[j] = x[j];
-    }
-    if (!there) s[j] = -INFINITY;
-  }
-  if (a.n_groups > 1) {
-    double value = -INFINITY;      // lane g: the value of group g
-    for (int g = 0; g < a.n_groups; ++g) {
-      double v = -INFINITY;
-      int best = kNone;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const int i = lane * VPL + j;
-        const double y = top2 ? s[j] : c[j];
-        if (i / per == g && i < E && y > v) {
-          v = y;
-          best = i;
-        }
+        for (int q = 0; q < 4; ++q) b[4 * j + q] = __uint_as_float(v[q]);
       }
-      wave_best(v, best);
-      if (top2) {
-        double w = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-          const int i = lane * VPL + j;
-          if (i / per == g && i < E && i != best && s[j] > w) w = s[j];
-        }
-        w = wave_max(w);
-        if (w > -INFINITY) v += w;
-      }
-      if (lane == g) value = v;
     }
-    uint64_t kept = 0;
-    for (int n = 0; n < a.topk_groups; ++n) {
-      double v = value;
-      int g = v > -INFINITY ? lane : kNone;
-      wave_best(v, g);
-      if (g == kNone) break;
-      kept |= 1ull << g;
-      if (lane == g) value = -INFINITY;
-    }
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int g = (lane * VPL + j) / per;
-      if (g >= a.n_groups || !(kept >> g & 1)) c[j] = -INFINITY;
-    }
-  }
-  int id = -1;
-  for (int k = 0; k < a.top_k; ++k) {
-    double v = -INFINITY;
-    int best = kNone;
+  } else {
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
-      if (c[j] > v) {
-        v = c[j];
-        best = lane * VPL + j;
-      }
-    wave_best(v, best);
-    if (best == kNone) break;
-    if (lane == k) id = best;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (best == lane * VPL + j) c[j] = -INFINITY;
+      if (first + j < a.n_experts) b[j] = a.bias[first + j];
   }
-  return id;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) b[j] = b[j] > -INFINITY ? b[j] : -INFINITY;
 }
 
-// Bound on the error of a binary32 score plus bias, over 1 + the largest such sum of the
-// token: a softmax score is within s (|l - top| + 30) 2^-24 <= 31 * 2^-24 (the argument's
-// rounding, expf, a sum of at most 16 + 6 additions, the division), a sigmoid within
-// 4 * 2^-24, and the bias adds one rounding of the sum.
-constexpr float kChoiceError = 0x1p-19f;
+// Bounds on the error of a binary32 score plus bias, over 1 + the largest such sum of the
+// token.  A softmax score is within s (|l - top| + 30) 2^-24 <= 31 * 2^-24 (the argument's
+// rounding, the exponential, a sum of at most 16 + 6 additions, the division), a sigmoid
+// within s (1 - s) 4 + 3 s <= 4 times 2^-24 (the exponential; the sum, the reciprocal),
+// and the bias adds one rounding of the sum.
+__device__ __forceinline__ float choice_error(int score) {
+  return score == EP_SCORE_SOFTMAX ? 0x1p-19f : 0x1p-21f;
+}
 
-// The picks of one token in binary32.  Returns false where the keys are not exact
-// (`exact`: they are the logits) and two that decide lie within their error.
-// key: the choices, score: scores plus bias, -infinity for what cannot be picked; group:
-// the groups of the lane's experts.  lanes: lanes of a group where that is a power of
-// two of whole lanes, 0: no groups, -1: groups of any other size.
-template <int VPL>
-__device__ __forceinline__ bool pick_binary32(const RouteArgs& a, int lane, float (&key)[VPL],
-                                              const float (&score)[VPL],
-                                              const int (&group)[VPL], bool exact, int lanes,
-                                              int& id) {
-  float error = 0.f;
-  if (!exact) {
-    float most = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (score[j] > -INFINITY) most = fmaxf(most, fabsf(score[j]));
-    error = kChoiceError * (1.f + wave_max(most));
-  }
+// The picks of one token, lane k's id (or -1) in lane k.  key: the choices, score: scores
+// plus bias, -infinity for what cannot be picked, each within `error` (0: exact, or
+// binary64).  Returns whether none that decide lie within their error of each other.
+// lanes: lanes of a group where that is a power of two of whole lanes, 0: no groups,
+// -1: groups of any other size.
+template <int LPT, int VPL, class T>
+__device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL],
+                                     const T (&score)[VPL], float error, int lanes, int& id) {
+  constexpr T none = -INFINITY;
   bool sure = true;
   if (lanes != 0) {
     const bool top2 = a.group_score == EP_GROUP_TOP2;
+    const int per = a.n_experts / a.n_groups;
     // the two largest of this lane's group (lanes > 0), or of group `lane`
-    float v1 = -INFINITY, v2 = -INFINITY;
+    T v1 = none, v2 = none;
     if (lanes > 0) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        const float y = top2 ? score[j] : key[j];
-        v2 = fmaxf(v2, fminf(v1, y));
-        v1 = fmaxf(v1, y);
+        const T y = top2 ? score[j] : key[j];
+        v2 = larger(v2, smaller(v1, y));
+        v1 = larger(v1, y);
       }
       for (int d = 1; d < lanes; d <<= 1) {
-        const float o1 = __shfl_xor(v1, d), o2 = __shfl_xor(v2, d);
-        v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
-        v1 = fmaxf(v1, o1);
+        const T o1 = __shfl_xor(v1, d), o2 = __shfl_xor(v2, d);
+        v2 = larger(smaller(v1, o1), larger(v2, o2));
+        v1 = larger(v1, o1);
       }
     } else {
       for (int g = 0; g < a.n_groups; ++g) {
-        float w1 = -INFINITY, w2 = -INFINITY;
+        T w1 = none, w2 = none;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-          const float y = group[j] != g ? -INFINITY : top2 ? score[j] : key[j];
-          w2 = fmaxf(w2, fminf(w1, y));
-          w1 = fmaxf(w1, y);
+          const int i = lane * VPL + j - g * per;
+          const T y = i < 0 || i >= per ? none : top2 ? score[j] : key[j];
+          w2 = larger(w2, smaller(w1, y));
+          w1 = larger(w1, y);
         }
-        const float m1 = wave_max(w1);
-        float m2 = -INFINITY;
-        if (top2) {
-          // the second: one lane that has the first gives its second, the others their first
-          const int win = (int)__builtin_ctzll(__ballot(w1 == m1));
-          m2 = wave_max(lane == win ? w2 : w1);
-        }
+        const T m1 = lanes_max<LPT>(w1);
+        T m2 = none;
+        // the second: the lane that has the first gives its second, the others their first
+        if (top2) m2 = lanes_max<LPT>(lowest_lane<LPT>(w1 == m1) ? w2 : w1);
         if (lane == g) {
           v1 = m1;
           v2 = m2;
         }
       }
     }
-    float value = v1;
-    if (top2 && v2 > -INFINITY) value += v2;
+    T value = v1;
+    if (top2 && v2 > none) value += v2;
     const int step = lanes > 0 ? lanes : 1, g = lane / step;
     int above = 0;                             // groups that come before this one
     for (int o = 0; o < a.n_groups; ++o) {
-      const float v = read_lane(value, o * step);
+      const T v = of_lane<LPT>(value, o * step);
       above += v > value || (v == value && o < g);
     }
     const bool mine = g < a.n_groups;
     const bool keep = mine && above < a.topk_groups;
-    if (!exact && a.topk_groups < a.n_groups) {
-      const float in = -wave_max(keep ? -value : -INFINITY);     // the last kept
-      const float out = wave_max(mine && !keep ? value : -INFINITY);
+    if (error > 0.f && a.topk_groups < a.n_groups) {
+      const T in = -lanes_max<LPT>(keep ? -value : none);        // the last kept
+      const T out = lanes_max<LPT>(mine && !keep ? value : none);
       // (infinite values: a group without experts, a bias of +infinity)
-      if (!(in - out > 4.f * error)) sure = out == -INFINITY;
+      if (!(in - out > 4.f * error)) sure = out == none;
     }
-    const uint64_t kept = __ballot(keep);      // by lane, or by group
+    if (lanes > 0) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (!(kept >> (lanes > 0 ? lane : group[j]) & 1)) key[j] = -INFINITY;
+      for (int j = 0; j < VPL; ++j)
+        if (!keep) key[j] = none;
+    } else {
+      const uint64_t kept = __ballot(keep) >> (LPT == 16 ? threadIdx.x & 48 : 0);   // by group
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (!(kept >> min((lane * VPL + j) / per, 63) & 1)) key[j] = none;
+    }
   }
-  float before = INFINITY;
+  T before = INFINITY;
   id = -1;
   // one more pick than asked for, to see how near it comes
-  const int picks = a.top_k + (exact ? 0 : 1);
+  const int picks = a.top_k + (error > 0.f ? 1 : 0);
   for (int k = 0; k < picks; ++k) {
-    float best = key[0];
+    T best = key[0];
 #pragma unroll
-    for (int j = 1; j < VPL; ++j) best = fmaxf(best, key[j]);
-    const float m = wave_max(best);
-    if (m == -INFINITY) break;
-    if (!exact && k > 0 && !(before - m > 2.f * error)) sure = false;
+    for (int j = 1; j < VPL; ++j) best = larger(best, key[j]);
+    const T m = lanes_max<LPT>(best);
+    if (error > 0.f && k > 0 && m > none && !(before - m > 2.f * error)) sure = false;
     before = m;
     if (k == a.top_k) break;
-    const int win = (int)__builtin_ctzll(__ballot(best == m));
-    int at = VPL;                              // the first of the lane's keys that is m
+    // the winning lane, and the first of its keys that is m
+    const bool win = lowest_lane<LPT>(best == m);
+    bool open = win;
+    int at = 0;
 #pragma unroll
-    for (int j = VPL - 1; j >= 0; --j)
-      if (key[j] == m) at = j;
-    const int i = win * VPL + __builtin_amdgcn_readlane(at, win);
-    if (lane == k) id = i;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (lane * VPL + j == i) key[j] = -INFINITY;
+    for (int j = 0; j < VPL; ++j) {
+      const bool is = open && key[j] == m;
+      open = open && !is;
+      if (is) {
+        at = lane * VPL + j;
+        key[j] = none;
+      }
+    }
+    // from the one lane that has it to lane k
+    const float picked = lanes_max<LPT>(win ? (float)at : -1.f);
+    if (lane == k && m > none) id = (int)picked;
   }
   return sure;
 }
 
+// Lanes of a group for pick().
 template <int VPL>
+__device__ __forceinline__ int group_lanes(const RouteArgs& a) {
+  const int per = a.n_experts / a.n_groups, span = per / VPL;
+  return a.n_groups == 1 ? 0 : per % VPL == 0 && (span & (span - 1)) == 0 ? span : -1;
+}
+
+// The picks of one token in binary64.
+template <int VPL>
+__device__ __forceinline__ int pick_binary64(const RouteArgs& a, int lane, const float (&x)[VPL],
+                                             float top) {
+  double key[VPL], score[VPL], sum = 0.;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const double l = x[j];
+    score[j] = a.score == EP_SCORE_SOFTMAX ? exp(l - top) : 1. / (1. + exp(-l));
+    sum += score[j];
+    // one at a time: this path is rare, and its registers are every token's
+    asm volatile("" : "+v"(score[j]));
+  }
+  sum = a.score == EP_SCORE_SOFTMAX ? lanes_sum<64>(sum) : 1.;
+  float b[VPL];
+  load_bias<VPL>(a, lane, b);
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const bool there = x[j] > -INFINITY && b[j] > -INFINITY;
+    score[j] = there ? score[j] / sum + b[j] : -INFINITY;
+    key[j] = a.bias ? score[j] : x[j];
+  }
+  int id;
+  pick<64, VPL, double>(a, lane, key, score, 0.f, group_lanes<VPL>(a), id);
+  return id;
+}
+
+// Largest logit of a token, at least the smallest finite number.
+template <int LPT, int VPL>
+__device__ __forceinline__ float largest(const float (&x)[VPL]) {
+  float top = x[0];
+#pragma unroll
+  for (int j = 1; j < VPL; ++j) top = fmaxf(top, x[j]);
+  return fmaxf(lanes_max<LPT>(top), -FLT_MAX);
+}
+
+// Weights and stores of one token, lane k with pick k's id.
+template <int LPT, int VPL>
+__device__ __forceinline__ void finish_token(const RouteArgs& a, int64_t t, bool token, int lane,
+                                             const float (&x)[VPL], float top, int id) {
+  const bool there = token && id >= 0;
+  const float l = there ? load_logit(a, t * a.n_experts + id) : -INFINITY;
+  float w;
+  if (a.renormalize) {
+    w = pick_share<LPT>(l, there, a.score);
+  } else if (a.score == EP_SCORE_SIGMOID) {
+    w = 1.f / (1.f + expf(-l));
+  } else {
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) sum += exp_near(x[j] - top);
+    w = expf(l - top) / lanes_sum<LPT>(sum);
+  }
+  if (token && lane < a.top_k) {
+    a.topk_ids[t * a.top_k + lane] = id;
+    a.topk_w[t * a.top_k + lane] = there ? a.scale * w : 0.f;
+  }
+}
+
+// First id of a token that is to be picked in binary64.
+constexpr int kPickAgain = -0x7fffffff;
+
+// HERE: tokens that binary32 cannot decide are picked in binary64 here; else they are
+// marked for pick_again_kernel.
+template <int LPT, int VPL, bool HERE>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+  constexpr int TPW = 64 / LPT;                // tokens of a wave
+  const int lane = threadIdx.x & (LPT - 1), row = (threadIdx.x & 63) / LPT;
+  const int64_t wave = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
+  const int64_t waves = (int64_t)gridDim.x * kRouteWaves;
+  const int E = a.n_experts, lanes = group_lanes<VPL>(a);
+  const bool exact = !a.bias && !(a.n_groups > 1 && a.group_score == EP_GROUP_TOP2);
+  for (int64_t first = wave * TPW; first < a.tokens; first += waves * TPW) {
+    const int64_t t = first + row;
+    const bool token = t < a.tokens;           // the last wave's may be fewer
+    float x[VPL];
+    load_row<VPL>(a, t, token ? lane : E, x);
+    const float top = largest<LPT>(x);
+    float key[VPL], score[VPL], error = 0.f;
+    if (exact) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) key[j] = x[j];
+    } else {
+      load_bias<VPL>(a, lane, key);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        if (a.score == EP_SCORE_SOFTMAX)
+          score[j] = exp_near(x[j] - top);
+        else
+          score[j] = __builtin_amdgcn_rcpf(1.f + exp_near(fminf(-x[j], 88.f)));
+        sum += score[j];
+      }
+      sum = a.score == EP_SCORE_SOFTMAX ? lanes_sum<LPT>(sum) : 1.f;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        score[j] = x[j] > -INFINITY ? score[j] * inv + key[j] : -INFINITY;
+        key[j] = a.bias ? score[j] : x[j];
+        if (score[j] > -INFINITY) error = fmaxf(error, fabsf(score[j]));
+      }
+      error = choice_error(a.score) * (1.f + lanes_max<LPT>(error));
+    }
+    int id;
+    const bool sure = pick<LPT, VPL, float>(a, lane, key, score, error, lanes, id);
+    if constexpr (HERE) {
+      if (!sure) id = pick_binary64<VPL>(a, lane, x, top);
+    } else if (token && !sure && lane == 0) {
+      a.topk_ids[t * a.top_k] = kPickAgain;
+    }
+    finish_token<LPT, VPL>(a, t, token && (HERE || sure), lane, x, top, id);
+  }
+}
+
+// The marked tokens, a wave each: every wave looks through runs of kRun tokens.
+constexpr int kRun = 16;
+template <int VPL>
+__global__ __launch_bounds__(kRouteThreads) void pick_again_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
   const int64_t waves = (int64_t)gridDim.x * kRouteWaves;
-  const int E = a.n_experts, per = E / a.n_groups;
-  const bool exact = !a.bias && !(a.n_groups > 1 && a.group_score == EP_GROUP_TOP2);
-  // lanes of a group, where that is a power of two of whole lanes
-  const int span = per / VPL;
-  const int lanes = a.n_groups == 1 ? 0 : per % VPL == 0 && (span & (span - 1)) == 0 ? span : -1;
-  float bias[VPL];
-  int group[VPL];
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int i = lane * VPL + j;
-    bias[j] = a.bias && i < E ? a.bias[i] : 0.f;
-    group[j] = min(i / per, 63);     // past the last expert: whatever, its keys are -infinity
-  }
-  for (int64_t t = wave; t < a.tokens; t += waves) {
-    float x[VPL];
-    load_row<VPL>(a, t, lane, x);
-    float top = x[0];
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) top = fmaxf(top, x[j]);
-    top = fmaxf(wave_max(top), -FLT_MAX);
-    const bool dense = a.score == EP_SCORE_SOFTMAX && !a.renormalize;
-    float sum = 0.f, key[VPL], score[VPL];
-    if (!exact || dense) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        score[j] = a.score == EP_SCORE_SOFTMAX ? expf(x[j] - top) : 1.f / (1.f + expf(-x[j]));
-        sum += score[j];
-      }
-      sum = a.score == EP_SCORE_SOFTMAX ? wave_sum(sum) : 1.f;
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      if (exact) {
-        key[j] = x[j];
-        continue;
-      }
-      if (a.score == EP_SCORE_SOFTMAX) score[j] *= inv;
-      score[j] = x[j] > -INFINITY && bias[j] > -INFINITY ? score[j] + bias[j] : -INFINITY;
-      key[j] = a.bias ? score[j] : x[j];
-    }
-    int id;
-    if (!pick_binary32<VPL>(a, lane, key, score, group, exact, lanes, id))
-      id = pick_binary64<VPL>(a, lane, x, top);
-    const bool there = id >= 0;
-    const float l = there ? load_logit(a, t * E + id) : -INFINITY;
-    float w;
-    if (a.renormalize)
-      w = pick_share(l, there, a.score);
-    else if (a.score == EP_SCORE_SIGMOID)
-      w = 1.f / (1.f + expf(-l));
-    else
-      w = expf(l - top) / sum;
-    if (lane < a.top_k) {
-      a.topk_ids[t * a.top_k + lane] = id;
-      a.topk_w[t * a.top_k + lane] = there ? a.scale * w : 0.f;
+  for (int64_t first = wave * kRun; first < a.tokens; first += waves * kRun) {
+    const int64_t mine = first + lane;
+    uint64_t marked = __ballot(lane < kRun && mine < a.tokens && a.topk_ids[mine * a.top_k] == kPickAgain);
+    while (marked) {
+      const int64_t t = first + __builtin_ctzll(marked);
+      marked &= marked - 1;
+      float x[VPL];
+      load_row<VPL>(a, t, lane, x);
+      const float top = largest<64>(x);
+      finish_token<64, VPL>(a, t, true, lane, x, top, pick_binary64<VPL>(a, lane, x, top));
     }
   }
 }
 
+// A wave per token; the next token's picks and their logits are loaded before this
+// one's row is computed and stored.
 template <int VPL>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
   const int64_t waves = (int64_t)gridDim.x * kRouteWaves;
   const int E = a.n_experts;
-  for (int64_t t = wave; t < a.tokens; t += waves) {
-    // lane k: pick k's id, gradient and logit
-    int id = lane < a.top_k ? a.topk_ids[t * a.top_k + lane] : -1;
-    float l = -INFINITY;
+  const bool dense = a.score == EP_SCORE_SOFTMAX && !a.renormalize;
+  // lane k: pick k's id (-1: none), logit and gradient
+  auto load_pick = [&](int64_t t, int& id, float& l, float& g) {
+    id = -1;
+    l = -INFINITY;
+    g = 0.f;
+    if (t >= a.tokens || lane >= a.top_k) return;
+    id = a.topk_ids[t * a.top_k + lane];
+    g = a.grad_w[t * a.top_k + lane];
     if (id >= 0 && id < E) l = load_logit(a, t * E + id);
+  };
+  int id;
+  float l, g;
+  load_pick(wave, id, l, g);
+  for (int64_t t = wave; t < a.tokens; t += waves) {
     const bool there = l > -INFINITY;
-    if (!there) id = -1;
-    const float g = there ? a.scale * a.grad_w[t * a.top_k + lane] : 0.f;
+    const int at = there ? id : -1;
+    const float mine = l, gk = there ? a.scale * g : 0.f;
+    load_pick(t + waves, id, l, g);
     float out[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) out[j] = 0.f;
-    const bool dense = a.score == EP_SCORE_SOFTMAX && !a.renormalize;
-    float d = g;                   // what pick k adds at its expert
+    float d = gk;                  // what pick k adds at its expert
     if (!dense) {
       if (a.renormalize) {
-        const float p = pick_share(l, there, a.score);
-        d = p * (g - wave_sum(g * p));
+        const float p = pick_share<64>(mine, there, a.score);
+        d = p * (gk - lanes_sum<64>(gk * p));
       } else {
-        d = g / (1.f + expf(-l));
+        d = gk / (1.f + expf(-mine));
       }
-      if (a.score == EP_SCORE_SIGMOID) d /= 1.f + expf(l);
+      if (a.score == EP_SCORE_SIGMOID) d /= 1.f + expf(mine);
       if (!there) d = 0.f;
     }
     for (int k = 0; k < a.top_k; ++k) {
-      const int i = __builtin_amdgcn_readlane(id, k) - lane * VPL;
+      const int i = __builtin_amdgcn_readlane(at, k) - lane * VPL;
       const float v = read_lane(d, k);
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
@@ -514,18 +580,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
     if (dense) {
       float x[VPL], sum = 0.f, dot = 0.f;
       load_row<VPL>(a, t, lane, x);
-      float top = x[0];
-#pragma unroll
-      for (int j = 1; j < VPL; ++j) top = fmaxf(top, x[j]);
-      top = fmaxf(wave_max(top), -FLT_MAX);
+      const float top = largest<64>(x);
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        x[j] = expf(x[j] - top);
+        x[j] = exp_near(x[j] - top);
         sum += x[j];
         dot += x[j] * out[j];
       }
-      sum = wave_sum(sum);
-      dot = wave_sum(dot);
+      sum = lanes_sum<64>(sum);
+      dot = lanes_sum<64>(dot);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       dot *= inv;
 #pragma unroll
@@ -537,24 +600,51 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
 
 }  // namespace
 
-#define EP_ROUTE_LAUNCH(KERNEL)                                                              \
-  const int64_t blocks = (a.tokens + kRouteWaves - 1) / kRouteWaves;                          \
-  const int64_t most = 16 * (int64_t)num_cus;                                                 \
-  const dim3 grid((int)(blocks < most ? blocks : most)), block(kRouteThreads);                \
-  const int vpl = (a.n_experts + 63) / 64;                                                    \
-  if (vpl <= 1) hipLaunchKernelGGL(KERNEL<1>, grid, block, 0, st, a);                         \
-  else if (vpl <= 2) hipLaunchKernelGGL(KERNEL<2>, grid, block, 0, st, a);                    \
-  else if (vpl <= 4) hipLaunchKernelGGL(KERNEL<4>, grid, block, 0, st, a);                    \
-  else if (vpl <= 8) hipLaunchKernelGGL(KERNEL<8>, grid, block, 0, st, a);                    \
-  else hipLaunchKernelGGL(KERNEL<16>, grid, block, 0, st, a);                                 \
-  return hipGetLastError();
+// Workgroups for `tokens` tokens, `each` a workgroup at a time, at most `per_cu` a CU.
+static int route_grid(int64_t tokens, int each, int num_cus, int per_cu) {
+  const int64_t blocks = (tokens + each - 1) / each, most = (int64_t)per_cu * num_cus;
+  return (int)(blocks < most ? blocks : most);
+}
 
 hipError_t launch_route(const RouteArgs& a, int num_cus, hipStream_t st) {
-  EP_ROUTE_LAUNCH(route_kernel)
+  const dim3 block(kRouteThreads);
+  // four tokens a wave from 16 tokens a CU on: one token took 5.6 us with 64 lanes and
+  // 10.4 with 16, 8192 tokens of 128 experts 11.5 and 7.9
+  const bool many = a.tokens >= 16 * (int64_t)num_cus && a.n_experts <= 256 && a.n_groups <= 16 &&
+                    a.top_k <= 16;
+  if (many) {
+    const dim3 grid(route_grid(a.tokens, 4 * kRouteWaves, num_cus, 16));
+    const int vpl = (a.n_experts + 15) / 16;
+    if (vpl <= 4)
+      hipLaunchKernelGGL((route_kernel<16, 4, false>), grid, block, 0, st, a);
+    else if (vpl <= 8)
+      hipLaunchKernelGGL((route_kernel<16, 8, false>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((route_kernel<16, 16, false>), grid, block, 0, st, a);
+    const bool exact = !a.bias && !(a.n_groups > 1 && a.group_score == EP_GROUP_TOP2);
+    if (!exact)
+      hipLaunchKernelGGL(pick_again_kernel<4>,
+                         dim3(route_grid(a.tokens, kRun * kRouteWaves, num_cus, 4)), block, 0, st, a);
+  } else {
+    const dim3 grid(route_grid(a.tokens, kRouteWaves, num_cus, 16));
+    const int vpl = (a.n_experts + 63) / 64;
+    if (vpl <= 4)
+      hipLaunchKernelGGL((route_kernel<64, 4, true>), grid, block, 0, st, a);
+    else if (vpl <= 8)
+      hipLaunchKernelGGL((route_kernel<64, 8, true>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((route_kernel<64, 16, true>), grid, block, 0, st, a);
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_route_backward(const RouteArgs& a, int num_cus, hipStream_t st) {
-  EP_ROUTE_LAUNCH(route_backward_kernel)
+  const dim3 grid(route_grid(a.tokens, kRouteWaves, num_cus, 8)), block(kRouteThreads);
+  const int vpl = (a.n_experts + 63) / 64;
+  if (vpl <= 4) hipLaunchKernelGGL(route_backward_kernel<4>, grid, block, 0, st, a);
+  else if (vpl <= 8) hipLaunchKernelGGL(route_backward_kernel<8>, grid, block, 0, st, a);
+  else hipLaunchKernelGGL(route_backward_kernel<16>, grid, block, 0, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace ep
