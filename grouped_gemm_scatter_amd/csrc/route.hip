@@ -44,10 +44,6 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t i) {
   return clean(a.dtype == EP_LOGITS_BF16 ? bf16_lo(h) : f16_value(h));
 }
 
-__device__ __forceinline__ float half_value(const RouteArgs& a, uint32_t h) {
-  return clean(a.dtype == EP_LOGITS_BF16 ? bf16_lo(h & 0xffffu) : f16_value(h));
-}
-
 // Logits of experts lane * VPL + 0..VPL-1 of token t, -infinity past the last.  Rows of
 // a multiple of VPL experts start where a lane's values can be loaded together.
 template <int VPL>
@@ -72,8 +68,13 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int lane
       uint32_t v[VPL / 2];
 #pragma unroll
       for (int j = 0; j < VPL / 2; ++j) v[j] = p[j];
+      if (a.dtype == EP_LOGITS_BF16) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) x[j] = half_value(a, v[j / 2] >> (16 * (j & 1)));
+        for (int j = 0; j < VPL; ++j) x[j] = clean(j & 1 ? bf16_hi(v[j / 2]) : bf16_lo(v[j / 2]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) x[j] = clean(f16_value(v[j / 2] >> (16 * (j & 1)) & 0xffffu));
+      }
     }
     return;
   }
@@ -139,23 +140,30 @@ __device__ __forceinline__ float read_lane(float v, int lane) {
 // Reductions over the LPT lanes of a token, the same result in each of them: 16 lanes are
 // a row of the data-parallel moves, reduced by rotations; 64 by shifts within the rows,
 // rows 0 and 2 into 1 and 3, the lower half into the upper, and its last lane.
+// (The maxima are written out: fmaxf() of a moved value takes a move, a quieting of
+// NaNs, which do not occur here, and the maximum; s_nop covers the wait that such a move
+// needs after its operand is written.)
+#define EP_MAX_MOVE(V, CTRL) \
+  asm("s_nop 1\n\tv_max_f32_dpp %0, %0, %0 " CTRL " bank_mask:0xf" : "+v"(V))
 template <int LPT>
 __device__ __forceinline__ float lanes_max(float v) {
   if constexpr (LPT == 16) {
-    v = fmaxf(v, lane_move<0x128>(v, v));        // row_ror 8, 4, 2, 1
-    v = fmaxf(v, lane_move<0x124>(v, v));
-    v = fmaxf(v, lane_move<0x122>(v, v));
-    return fmaxf(v, lane_move<0x121>(v, v));
+    EP_MAX_MOVE(v, "row_ror:8 row_mask:0xf");
+    EP_MAX_MOVE(v, "row_ror:4 row_mask:0xf");
+    EP_MAX_MOVE(v, "row_ror:2 row_mask:0xf");
+    EP_MAX_MOVE(v, "row_ror:1 row_mask:0xf");
+    return v;
   } else {
-    v = fmaxf(v, lane_move<0x111>(v, v));        // row_shr 1, 2, 4, 8
-    v = fmaxf(v, lane_move<0x112>(v, v));
-    v = fmaxf(v, lane_move<0x114>(v, v));
-    v = fmaxf(v, lane_move<0x118>(v, v));
-    v = fmaxf(v, lane_move<0x142, 0xa>(v, v));   // row_bcast 15, 31
-    v = fmaxf(v, lane_move<0x143, 0xc>(v, v));
+    EP_MAX_MOVE(v, "row_shr:1 row_mask:0xf");
+    EP_MAX_MOVE(v, "row_shr:2 row_mask:0xf");
+    EP_MAX_MOVE(v, "row_shr:4 row_mask:0xf");
+    EP_MAX_MOVE(v, "row_shr:8 row_mask:0xf");
+    EP_MAX_MOVE(v, "row_bcast:15 row_mask:0xa");
+    EP_MAX_MOVE(v, "row_bcast:31 row_mask:0xc");
     return read_lane(v, 63);
   }
 }
+#undef EP_MAX_MOVE
 template <int LPT>
 __device__ __forceinline__ float lanes_sum(float v) {
   if constexpr (LPT == 16) {
@@ -282,26 +290,28 @@ __device__ __forceinline__ float choice_error(int score) {
 }
 
 // The picks of one token, lane k's id (or -1) in lane k.  key: the choices, score: scores
-// plus bias, -infinity for what cannot be picked, each within `error` (0: exact, or
-// binary64).  Returns whether none that decide lie within their error of each other.
+// plus bias, -infinity for what cannot be picked, each within `error` unless `exact`.
+// Returns whether none that decide lie within their error of each other.
 // lanes: lanes of a group where that is a power of two of whole lanes, 0: no groups,
 // -1: groups of any other size.
 template <int LPT, int VPL, class T>
 __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL],
-                                     const T (&score)[VPL], float error, int lanes, int& id) {
+                                     const T (&score)[VPL], bool exact, float error, int lanes,
+                                     int& id) {
   constexpr T none = -INFINITY;
   bool sure = true;
   if (lanes != 0) {
     const bool top2 = a.group_score == EP_GROUP_TOP2;
     const int per = a.n_experts / a.n_groups;
     // the two largest of this lane's group (lanes > 0), or of group `lane`
-    T v1 = none, v2 = none;
+    T v1 = none, v2 = none, by[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) by[j] = top2 ? score[j] : key[j];
     if (lanes > 0) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        const T y = top2 ? score[j] : key[j];
-        v2 = larger(v2, smaller(v1, y));
-        v1 = larger(v1, y);
+        v2 = larger(v2, smaller(v1, by[j]));
+        v1 = larger(v1, by[j]);
       }
       for (int d = 1; d < lanes; d <<= 1) {
         const T o1 = __shfl_xor(v1, d), o2 = __shfl_xor(v2, d);
@@ -314,7 +324,7 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL]
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
           const int i = lane * VPL + j - g * per;
-          const T y = i < 0 || i >= per ? none : top2 ? score[j] : key[j];
+          const T y = i < 0 || i >= per ? none : by[j];
           w2 = larger(w2, smaller(w1, y));
           w1 = larger(w1, y);
         }
@@ -338,7 +348,7 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL]
     }
     const bool mine = g < a.n_groups;
     const bool keep = mine && above < a.topk_groups;
-    if (error > 0.f && a.topk_groups < a.n_groups) {
+    if (!exact && a.topk_groups < a.n_groups) {
       const T in = -lanes_max<LPT>(keep ? -value : none);        // the last kept
       const T out = lanes_max<LPT>(mine && !keep ? value : none);
       // (infinite values: a group without experts, a bias of +infinity)
@@ -346,25 +356,24 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL]
     }
     if (lanes > 0) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (!keep) key[j] = none;
+      for (int j = 0; j < VPL; ++j) key[j] = keep ? key[j] : none;
     } else {
       const uint64_t kept = __ballot(keep) >> (LPT == 16 ? threadIdx.x & 48 : 0);   // by group
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
-        if (!(kept >> min((lane * VPL + j) / per, 63) & 1)) key[j] = none;
+        key[j] = kept >> min((lane * VPL + j) / per, 63) & 1 ? key[j] : none;
     }
   }
   T before = INFINITY;
   id = -1;
   // one more pick than asked for, to see how near it comes
-  const int picks = a.top_k + (error > 0.f ? 1 : 0);
+  const int picks = a.top_k + (exact ? 0 : 1);
   for (int k = 0; k < picks; ++k) {
     T best = key[0];
 #pragma unroll
     for (int j = 1; j < VPL; ++j) best = larger(best, key[j]);
     const T m = lanes_max<LPT>(best);
-    if (error > 0.f && k > 0 && m > none && !(before - m > 2.f * error)) sure = false;
+    if (!exact && k > 0 && m > none && !(before - m > 2.f * error)) sure = false;
     before = m;
     if (k == a.top_k) break;
     // the winning lane, and the first of its keys that is m
@@ -375,13 +384,11 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL]
     for (int j = 0; j < VPL; ++j) {
       const bool is = open && key[j] == m;
       open = open && !is;
-      if (is) {
-        at = lane * VPL + j;
-        key[j] = none;
-      }
+      at = is ? j : at;
+      key[j] = is ? none : key[j];
     }
     // from the one lane that has it to lane k
-    const float picked = lanes_max<LPT>(win ? (float)at : -1.f);
+    const float picked = lanes_max<LPT>(win ? (float)(lane * VPL + at) : -1.f);
     if (lane == k && m > none) id = (int)picked;
   }
   return sure;
@@ -417,7 +424,7 @@ __device__ __forceinline__ int pick_binary64(const RouteArgs& a, int lane, const
     key[j] = a.bias ? score[j] : x[j];
   }
   int id;
-  pick<64, VPL, double>(a, lane, key, score, 0.f, group_lanes<VPL>(a), id);
+  pick<64, VPL, double>(a, lane, key, score, true, 0.f, group_lanes<VPL>(a), id);
   return id;
 }
 
@@ -478,27 +485,32 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
       for (int j = 0; j < VPL; ++j) key[j] = x[j];
     } else {
       load_bias<VPL>(a, lane, key);
-      float sum = 0.f;
+      float inv = 1.f;
+      if (a.score == EP_SCORE_SOFTMAX) {
+        float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        if (a.score == EP_SCORE_SOFTMAX)
+        for (int j = 0; j < VPL; ++j) {
           score[j] = exp_near(x[j] - top);
-        else
+          sum += score[j];
+        }
+        sum = lanes_sum<LPT>(sum);
+        inv = sum > 0.f ? 1.f / sum : 0.f;
+      } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
           score[j] = __builtin_amdgcn_rcpf(1.f + exp_near(fminf(-x[j], 88.f)));
-        sum += score[j];
       }
-      sum = a.score == EP_SCORE_SOFTMAX ? lanes_sum<LPT>(sum) : 1.f;
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const bool biased = a.bias != nullptr;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
         score[j] = x[j] > -INFINITY ? score[j] * inv + key[j] : -INFINITY;
-        key[j] = a.bias ? score[j] : x[j];
-        if (score[j] > -INFINITY) error = fmaxf(error, fabsf(score[j]));
+        key[j] = biased ? score[j] : x[j];
+        error = fmaxf(error, score[j] > -INFINITY ? fabsf(score[j]) : 0.f);
       }
       error = choice_error(a.score) * (1.f + lanes_max<LPT>(error));
     }
     int id;
-    const bool sure = pick<LPT, VPL, float>(a, lane, key, score, error, lanes, id);
+    const bool sure = pick<LPT, VPL, float>(a, lane, key, score, exact, error, lanes, id);
     if constexpr (HERE) {
       if (!sure) id = pick_binary64<VPL>(a, lane, x, top);
     } else if (token && !sure && lane == 0) {
