@@ -249,10 +249,10 @@ template <int LPT>
 __device__ __forceinline__ float pick_share(float l, bool there, int score) {
   const float low = score == EP_SCORE_SIGMOID ? fminf(l, 0.f) : l;
   const float top = lanes_max<LPT>(there ? low : -FLT_MAX);
-  float e = there ? expf(low - top) : 0.f;
-  if (score == EP_SCORE_SIGMOID) e /= 1.f + expf(-fabsf(l));
+  float e = there ? exp_near(low - top) : 0.f;
+  if (score == EP_SCORE_SIGMOID) e *= __builtin_amdgcn_rcpf(1.f + exp_near(-fabsf(l)));
   const float sum = lanes_sum<LPT>(e);
-  return there ? e / sum : 0.f;
+  return there ? e * __builtin_amdgcn_rcpf(sum) : 0.f;
 }
 
 // Bias of the lane's experts: 0 without one, -infinity for an expert that it keeps out.
@@ -577,9 +577,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
         const float p = pick_share<64>(mine, there, a.score);
         d = p * (gk - lanes_sum<64>(gk * p));
       } else {
-        d = gk / (1.f + expf(-mine));
+        d = gk * __builtin_amdgcn_rcpf(1.f + exp_near(fminf(-mine, 88.f)));
       }
-      if (a.score == EP_SCORE_SIGMOID) d /= 1.f + expf(mine);
+      if (a.score == EP_SCORE_SIGMOID)
+        d *= __builtin_amdgcn_rcpf(1.f + exp_near(fminf(mine, 88.f)));
       if (!there) d = 0.f;
     }
     for (int k = 0; k < a.top_k; ++k) {
