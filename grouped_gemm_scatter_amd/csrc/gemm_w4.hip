@@ -347,6 +347,50 @@ __device__ __forceinline__ void swiglu(f32x4 (&g)[MT], const f32x4 (&u)[MT]) {
     for (int r = 0; r < 4; ++r) g[j][r] = g[j][r] / (1.f + expf(-g[j][r])) * u[j][r];
 }
 
+// build_work_table with the prefix over the experts made by a scan of one wave: the
+// launch is short enough for a sequential prefix (1 us for 32 experts, 8 for 256) to count.
+template <int BM>
+__device__ __forceinline__ bool build_table(const GemmArgs& a, int nt, int* s_base, int* s_gbeg,
+                                            int* s_bad) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int R = a.s.n_ranks, El = a.s.n_experts;
+  if (tid == 0) *s_bad = 0;
+  __syncthreads();
+  for (int i = tid; i <= El * R; i += kW4Threads) {
+    const int v = a.offsets[i], before = i > 0 ? a.offsets[i - 1] : 0;
+    if (v < before || v > a.m_total || (i == 0 && v != 0) || (i == El * R && v != a.m_total))
+      *s_bad = 1;
+    if (i % R == 0) s_gbeg[i / R] = v;
+  }
+  __syncthreads();
+  if (*s_bad) {
+    if (tid == 0 && blockIdx.x == 0) latch_error(a.s.err, kErrBadGroup);
+    return false;
+  }
+  if (tid < 64) {
+    int base = 0;
+    for (int e0 = 0; e0 < El; e0 += 64) {
+      const int e = e0 + lane;
+      int n = 0;                     // items of expert e: its tiles, or one to signal
+      if (e < El) {
+        const int me = s_gbeg[e + 1] - s_gbeg[e];
+        n = me ? (me + BM - 1) / BM * nt : 1;
+      }
+      int sum = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(sum, d);
+        if (lane >= d) sum += up;
+      }
+      if (e < El) s_base[e] = base + sum - n;
+      base += __shfl(sum, 63);
+    }
+    if (lane == 0) s_base[El] = base;
+  }
+  __syncthreads();
+  return true;
+}
+
 // The products of one tile with MT 16-row blocks, staged in LDS as bf16 rows.
 template <class T, class F, bool SWIGLU, int MT>
 __device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t, uint8_t* smem,
@@ -441,9 +485,7 @@ __global__ __launch_bounds__(kW4Threads, T::PER_CU) void gemm_w4_kernel(W4Args w
     for (int i = 0; i < kMaxRanks; ++i) s_recv[i] = a.s.recv[i];
   }
   init_done(s_done);
-  if (!build_work_table<T::ROWS, kW4Threads>(a, (a.N + T::COLS - 1) / T::COLS, s_base, s_gbeg,
-                                             &s_bad))
-    return;
+  if (!build_table<T::ROWS>(a, (a.N + T::COLS - 1) / T::COLS, s_base, s_gbeg, &s_bad)) return;
   const int total = s_base[El];
   const int per_xcd = gridDim.x >> 3;                // the grid is a multiple of 8
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
@@ -470,11 +512,14 @@ __global__ __launch_bounds__(kW4Threads, T::PER_CU) void gemm_w4_kernel(W4Args w
       wait_vm<0>();
       prologue_barrier<true>(a, pending);
     }
+    // where the rows go: put into LDS at once, so that no register holds it across the K
+    // loop, but in the thin tile, whose K loop is shorter than these loads
+    RowInfo ri{-1, 0, 0};
     if constexpr (!SWIGLU) {
-      // ready long before the tile is: kept in LDS, not in registers across the K loop
-      if (tid < T::ROWS)
-        s_rowdst[tid] = row_destination(a, s_recv, load_row_info(a, t.e, t.g1, t.m_abs + tid),
-                                        t.m_abs + tid);
+      if (tid < T::ROWS) {
+        ri = load_row_info(a, t.e, t.g1, t.m_abs + tid);
+        if (T::SPLIT == 1) s_rowdst[tid] = row_destination(a, s_recv, ri, t.m_abs + tid);
+      }
     }
     const int mt = (t.rows + 15) / 16;
     if (T::ROWS == 16 || mt == 1)
@@ -485,6 +530,9 @@ __global__ __launch_bounds__(kW4Threads, T::PER_CU) void gemm_w4_kernel(W4Args w
       tile_product<T, F, SWIGLU, T::ROWS == 16 ? 1 : 3>(wa, t, smem, PITCH, tid, wave);
     else
       tile_product<T, F, SWIGLU, T::ROWS == 16 ? 1 : 4>(wa, t, smem, PITCH, tid, wave);
+    if constexpr (!SWIGLU && T::SPLIT > 1) {
+      if (tid < T::ROWS) s_rowdst[tid] = row_destination(a, s_recv, ri, t.m_abs + tid);
+    }
     __syncthreads();
     const int col0 = t.n_abs / T::COLS * OUT;
     if (SWIGLU || !a.sink_on) {

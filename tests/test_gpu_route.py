@@ -62,6 +62,15 @@ CASES = {
     "many_picks": (1, 30, 200, 64, dict(score="sigmoid", bias=True)),
     "largest": (1, 25, 1024, 16, dict(n_groups=64, topk_groups=5, bias=True)),
     "odd": (5, 13, 333, 9, dict(n_groups=3, topk_groups=2, score="sigmoid")),
+    # enough tokens for four of them a wave, with a count that is no multiple of four
+    "many_grouped_sigmoid": (7, 601, 256, 8, dict(n_groups=8, topk_groups=4, score="sigmoid",
+                                                  group_score="top2", bias=True, scale=2.5)),
+    "many_odd_groups": (3, 1501, 130, 5, dict(n_groups=10, topk_groups=3, group_score="top2")),
+    "many_groups_of_one_lane": (1, 4100, 64, 4, dict(n_groups=16, topk_groups=5, bias=True)),
+    "many_plain": (8, 513, 33, 16, dict(renormalize=False, bias=True)),
+    "many_softmax": (5, 900, 250, 11, dict()),
+    "many_too_many_picks": (1, 4200, 96, 17, dict(score="sigmoid")),
+    "many_too_many_experts": (1, 4200, 300, 4, dict(n_groups=4, topk_groups=2, bias=True)),
     "bias_alone_moves_the_picks": (1, 60, 40, 4, dict(bias=True, score="sigmoid", renormalize=False)),
 }
 
@@ -123,6 +132,28 @@ def test_ties_go_to_the_lowest_index():
     ids, w = ctx.route(l.cuda(), n_groups=8, topk_groups=2, group_score="top2")
     assert ids.tolist() == [[[0, 1, 2, 3], [10, 11, 12, 13], [3, 7, 11, 15]]]
     assert torch.all(w == 0.25)
+
+
+@pytest.mark.parametrize("T", [9, 4099])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_choices_that_tie_or_nearly_tie(score, group_score, T):
+    """Logits and biases of few values: most tokens hold choices and groups that are equal,
+    or apart by less than binary32 can tell."""
+    rng = np.random.default_rng(T)
+    E, k = 64, 6
+    steps = 2.0 ** -21 * np.arange(-3, 4)
+    l = rng.choice([-1.0, 0.25, 0.5, 1.5], (1, T, E))
+    l = (l + rng.choice(steps, l.shape) * (rng.random(l.shape) < 0.5)).astype(np.float32)
+    bias = rng.choice([0.0, 0.125, 0.25], E).astype(np.float32)
+    ctx = _ctx(1, T, k)
+    kw = dict(n_groups=8, topk_groups=3, group_score=group_score, score=score)
+    ids, w = ctx.route(torch.from_numpy(l).cuda(), bias=torch.from_numpy(bias).cuda(), **kw)
+    want_ids, want_w = P.route(l.reshape(-1, E).astype(np.float64), k, bias=bias, **kw)
+    # choices closer than binary64 itself can tell are left out: equal logits and biases
+    # give equal choices on both sides, others differ by 2^-21 / 16 or more
+    assert np.array_equal(ids.cpu().numpy().reshape(-1, k), want_ids)
+    np.testing.assert_allclose(_numpy(w), want_w, rtol=60 * U)
 
 
 def test_choices_a_binary32_step_apart_are_told_apart():

@@ -49,11 +49,9 @@ def _ctx(sizes, R, T, k, n, **kw):
 
 
 def _sum_bound(a, k, group):
-    """k products, each addition of the matrix unit within one step (2^-23) of a partial
-    sum that a = sum |x w| bounds; then a product and an addition for every group.  The
-    integers of int4 reach 15/8 of |code - 8| where 8 is taken off afterwards, at most
-    16 times |w| summed over a group: the bound counts 16 a."""
-    return (k + 2 * k // group) * 2.0 ** -23 * 16 * a
+    """k exact products, each addition of the matrix unit within one step (2^-23) of a
+    partial sum that a = sum |x w| bounds; then a product and an addition for every group."""
+    return (k + 2 * k // group) * 2.0 ** -23 * a
 
 
 SIZES = {
@@ -63,6 +61,8 @@ SIZES = {
     "no_rows": [0, 0, 0],
     "large_group": [5, 300, 0, 129],
     "many_experts": [(7 * i) % 5 for i in range(256)],
+    # enough tiles for the 256-column tile, one to two row tiles of 0..70 rows an expert
+    "decode_tile": [(11 * i) % 71 for i in range(256)],
 }
 
 
@@ -76,6 +76,12 @@ def test_down_projection(fmt, k, n):
 @pytest.mark.parametrize("mode", ["flag", "per_expert", "system", "padded"])
 def test_down_projection_groups_and_modes(name, mode):
     _down(name, ("int4", 64, "bf16"), 256, 256, R=8 if name == "edges" else 2, mode=mode)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=lambda f: "-".join(map(str, f)))
+def test_down_projection_of_the_decode_tile(fmt):
+    # 640 columns: the last tile of every expert is half empty
+    _down("decode_tile", fmt, 384, 640, R=2)
 
 
 def _down(name, fmt, k, n, R, mode="flag"):
@@ -131,7 +137,7 @@ def _down(name, fmt, k, n, R, mode="flag"):
 @pytest.mark.parametrize("fmt", FORMATS, ids=lambda f: "-".join(map(str, f)))
 @pytest.mark.parametrize("name,inter,hidden", [
     ("edges", 128, 384), ("empty_and_one", 384, 7168), ("one_row", 2048, 256),
-    ("large_group", 256, 128), ("no_rows", 128, 128)])
+    ("large_group", 256, 128), ("no_rows", 128, 128), ("decode_tile", 256, 256)])
 def test_up_projection(fmt, name, inter, hidden):
     codes_are, group, st = fmt
     sizes, R = SIZES[name], 2
@@ -177,6 +183,21 @@ def test_every_code_at_every_place(codes_are):
     ctx.gemm_scatter_w4(x, w, off, src, k, p3_control=-1, c_local=c)
     want = P.weights_w4(codes, scales.double().numpy(), codes_are)[0].T
     assert np.array_equal(c.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("codes_are,zero", [("int4", 0x88), ("e2m1", 0x00), ("e2m1", 0x88)])
+def test_weights_of_zero_give_zeros(codes_are, zero):
+    k, n = 384, 128
+    ctx, _ = _ctx([5, 40], 1, 45, k, n)
+    codes = torch.full((2, n, k // 2), zero, dtype=torch.uint8, device="cuda")
+    scales = torch.rand(2, n, k // 64, device="cuda").bfloat16()
+    w = ctx.pack_weights_w4(codes, scales, codes=codes_are)
+    off = torch.tensor([0, 5, 45], dtype=torch.int32, device="cuda")
+    src = torch.zeros(45, 2, dtype=torch.int32, device="cuda")
+    x = (100 * torch.randn(45, k, device="cuda")).to(torch.bfloat16)
+    c = torch.full((45, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    ctx.gemm_scatter_w4(x, w, off, src, 45, p3_control=-1, c_local=c)
+    assert torch.all(c == 0)
 
 
 def test_numbers_without_an_end_stay_in_their_row():

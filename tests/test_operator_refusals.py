@@ -1,0 +1,71 @@
+"""Refusals of the routing, 4-bit weight and combine-gradient calls that need no GPU: null
+handles at the C boundary, unknown names and types in the plumbing."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from grouped_gemm_scatter_amd import PackedW4
+from grouped_gemm_scatter_amd import binding as B
+from grouped_gemm_scatter_amd.context import EpCombine, _choice
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(B.LIB_PATH):
+        from grouped_gemm_scatter_amd.build import build
+        build(jobs=4)
+    return B.load_library()
+
+
+def test_null_handles_are_rejected(lib):
+    p = ctypes.byref(B.make_route_params(n_experts=8, logits_dtype=torch.float32))
+    f = ctypes.byref(B.make_w4_format(codes=B.EP_W4_INT4, group=32, scale_dtype=torch.bfloat16))
+    assert lib.ep_route_topk(None, p, None, None, 0, None, None, None) == B.EP_ERR_INVALID_ARG
+    assert lib.ep_route_topk_backward(None, p, None, None, None, 0, None,
+                                      None) == B.EP_ERR_INVALID_ARG
+    assert lib.ep_combine_backward(None, None, None, None, 0, None, None, 0, None, None,
+                                   None) == B.EP_ERR_INVALID_ARG
+    assert lib.ep_pack_weights_w4(None, f, None, None, 16, 128, None, None,
+                                  None) == B.EP_ERR_INVALID_ARG
+    assert lib.ep_grouped_gemm_swiglu_w4(None, f, None, None, None, None, 0, None,
+                                         None) == B.EP_ERR_INVALID_ARG
+    assert lib.ep_grouped_gemm_scatter_w4(None, f, None, None, None, None, None, 0, 0, None, 1,
+                                          None) == B.EP_ERR_INVALID_ARG
+
+
+def test_types_and_names():
+    with pytest.raises(ValueError, match="float32, bfloat16 or float16"):
+        B.make_route_params(n_experts=8, logits_dtype=torch.float64)
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
+        B.make_w4_format(codes=0, group=32, scale_dtype=torch.float32)
+    with pytest.raises(ValueError, match="score must be one of"):
+        _choice({"softmax": 0}, "tanh", "score")
+
+
+def test_shapes_and_devices():
+    t = torch.zeros(2, 3, 4)
+    ctx = EpCombine.__new__(EpCombine)       # no device: the checks come before it is used
+    ctx._device_index = 0
+    for args, message in (((t, "x", (2, 3, 5), torch.float32), "must be"),
+                          ((t, "x", (2, 3, 4), torch.int32), "must be torch.int32"),
+                          ((t, "x", (2, 3, 4), torch.float32), "handle's device")):
+        with pytest.raises(ValueError, match=message):
+            ctx._shape(*args)
+
+
+def test_packed_weights_of_another_shape():
+    ctx = EpCombine.__new__(EpCombine)
+    ctx.n_experts_per_device = 2
+    fmt = B.make_w4_format(codes=0, group=32, scale_dtype=torch.bfloat16)
+    w = PackedW4(torch.zeros(2, 16, 64, dtype=torch.uint8), torch.zeros(2, 16, 4), 16, 128, fmt)
+    ctx._need_w4(w, 16, 128)
+    for rows, k in ((32, 128), (16, 256)):
+        with pytest.raises(ValueError, match="packed weights"):
+            ctx._need_w4(w, rows, k)
+    ctx.n_experts_per_device = 3
+    with pytest.raises(ValueError, match="packed weights"):
+        ctx._need_w4(w, 16, 128)
+    with pytest.raises(ValueError, match="pack_weights_w4"):
+        ctx._need_w4(torch.zeros(4), 16, 128)
