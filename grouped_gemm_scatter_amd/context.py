@@ -144,6 +144,15 @@ class EpCombine:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
+    def _flat(self, t, name: str, elems: int, dtype):
+        """Raises unless `t` is a contiguous tensor of this type on the handle's device with
+        at least `elems` elements."""
+        if t is None or isinstance(t, int):
+            return
+        if t.numel() < elems:
+            raise ValueError(f"{name}: {t.numel()} elements, at least {elems} needed")
+        self._shape(t, name, t.shape, dtype)
+
     def _empty(self, shape, dtype, stream):
         """Memory for what a call returns, allocated on the stream that it runs on."""
         if stream is None:
@@ -216,11 +225,12 @@ class EpCombine:
         self._shape(topk_ids, "topk_ids", shape, torch.int32)
         self._shape(topk_w, "topk_w", shape, torch.float32)
         if rows:
-            self._need(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, 4)
-            self._need(src_info, "src_info", 2 * m, 4)
+            self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1,
+                       torch.int32)
+            self._flat(src_info, "src_info", 2 * m, torch.int32)
             if grad_rows is None:
                 grad_rows = self._empty((m, N), torch.bfloat16, stream)
-            self._need(grad_rows, "grad_rows", m * N, 2)
+            self._flat(grad_rows, "grad_rows", m * N, torch.bfloat16)
         elif grad_rows is not None:
             raise ValueError("grad_rows given with rows=False")
         if grad_w is None:
@@ -261,10 +271,10 @@ class EpCombine:
     def up_swiglu_w4(self, x1, w1: PackedW4, offsets, m_total, h_out, *, stream=None):
         """up_swiglu on 4-bit weights packed from [E_l][2*hidden_k][hidden_n] codes."""
         hid, inter = self.hidden_n, self.hidden_k
-        self._need(x1, "x1", m_total * hid, 2)
+        self._flat(x1, "x1", m_total * hid, torch.bfloat16)
         self._need_w4(w1, 2 * inter, hid)
-        self._need(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, 4)
-        self._need(h_out, "h_out", m_total * inter, 2)
+        self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, torch.int32)
+        self._flat(h_out, "h_out", m_total * inter, torch.bfloat16)
         return B.ep_grouped_gemm_swiglu_w4(self.handle, w1.format, x1, w1.codes, w1.scales, offsets,
                                            m_total, h_out, stream)
 
@@ -272,12 +282,12 @@ class EpCombine:
                         c_local=None, epoch: int | None = None, stream=None):
         """gemm_scatter on 4-bit weights packed from [E_l][hidden_n][hidden_k] codes."""
         K, N = self.hidden_k, self.hidden_n
-        self._need(x, "x", m_total * K, 2)
+        self._flat(x, "x", m_total * K, torch.bfloat16)
         self._need_w4(w, N, K)
-        self._need(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, 4)
-        self._need(src_info, "src_info", 2 * m_total, 4)
+        self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, torch.int32)
+        self._flat(src_info, "src_info", 2 * m_total, torch.int32)
         if p3_control < 0:
-            self._need(c_local, "c_local", m_total * N, 2)
+            self._flat(c_local, "c_local", m_total * N, torch.bfloat16)
         return B.ep_grouped_gemm_scatter_w4(self.handle, w.format, x, w.codes, w.scales, offsets,
                                             src_info, m_total, p3_control, c_local,
                                             self._epoch(epoch), stream)

@@ -594,9 +594,10 @@ bool w4_format_ok(const ep_w4_format* f) {
          (f->scales == EP_W4_SCALE_BF16 || f->scales == EP_W4_SCALE_F16);
 }
 
+// Whether np bytes at p and nq bytes at q meet.
 bool overlap(const void* p, uint64_t np, const void* q, uint64_t nq) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + nq && b < a + np;
+  return np && nq && a < b + nq && b < a + np;
 }
 
 }  // namespace
@@ -611,6 +612,11 @@ int ep_route_topk(ep_combine_t h, const ep_route_params* params, const void* log
   if (rc != EP_OK) return rc;
   if (tokens_per_rank == 0) return EP_OK;
   if (!topk_ids || !topk_w) return EP_ERR_INVALID_ARG;
+  const uint64_t in = uint64_t(a.tokens) * a.n_experts * (a.dtype == EP_LOGITS_F32 ? 4 : 2);
+  const uint64_t out = uint64_t(a.tokens) * a.top_k * 4;
+  if (overlap(logits, in, topk_ids, out) || overlap(logits, in, topk_w, out) ||
+      overlap(topk_ids, out, topk_w, out))
+    return EP_ERR_INVALID_ARG;
   a.bias = bias;
   a.topk_ids = topk_ids;
   a.topk_w = topk_w;
@@ -628,7 +634,10 @@ int ep_route_topk_backward(ep_combine_t h, const ep_route_params* params, const 
   if (!topk_ids || !grad_w || !grad_logits || !aligned16(grad_logits)) return EP_ERR_INVALID_ARG;
   const uint64_t bytes =
       uint64_t(a.tokens) * a.n_experts * (a.dtype == EP_LOGITS_F32 ? 4 : 2);
-  if (overlap(logits, bytes, grad_logits, bytes)) return EP_ERR_INVALID_ARG;
+  const uint64_t picks = uint64_t(a.tokens) * a.top_k * 4;
+  if (overlap(logits, bytes, grad_logits, bytes) || overlap(topk_ids, picks, grad_logits, bytes) ||
+      overlap(grad_w, picks, grad_logits, bytes))
+    return EP_ERR_INVALID_ARG;
   a.topk_ids = const_cast<int32_t*>(topk_ids);
   a.grad_w = grad_w;
   a.grad_logits = static_cast<uint8_t*>(grad_logits);
@@ -647,6 +656,13 @@ int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* top
   if (!grad_out || !aligned16(grad_out) || !topk_ids || !topk_w || !grad_w)
     return EP_ERR_INVALID_ARG;
   if (grad_rows && (!aligned16(grad_rows) || !offsets || (m_total > 0 && !src_info)))
+    return EP_ERR_INVALID_ARG;
+  const uint64_t tokens = uint64_t(h->p.n_ranks) * tokens_per_rank;
+  const uint64_t go_bytes = tokens * h->p.hidden_n * 2, w_bytes = tokens * h->p.top_k * 4;
+  const uint64_t rows_bytes = grad_rows ? uint64_t(m_total) * h->p.hidden_n * 2 : 0;
+  if (overlap(grad_out, go_bytes, grad_rows, rows_bytes) ||
+      overlap(grad_out, go_bytes, grad_w, w_bytes) || overlap(topk_ids, w_bytes, grad_w, w_bytes) ||
+      overlap(topk_w, w_bytes, grad_w, w_bytes))
     return EP_ERR_INVALID_ARG;
   ep::CombineBackwardArgs a{};
   a.grad_out = static_cast<const uint8_t*>(grad_out);
@@ -706,9 +722,8 @@ int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format, const 
   if (h->p.dtype != EP_DTYPE_BF16) return EP_ERR_UNSUPPORTED;
   const int hidden = h->p.hidden_n, inter = h->p.hidden_k;
   if (inter % 128) return EP_ERR_UNSUPPORTED;
-  // 32-bit byte offsets inside X1 and one expert's codes and scales
-  if (uint64_t(m_total) * hidden * 2 >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
-  if (uint64_t(inter) * hidden >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
+  if (overlap(x1, uint64_t(m_total) * hidden * 2, h_out, uint64_t(m_total) * inter * 2))
+    return EP_ERR_INVALID_ARG;
   if (!on_device(h)) return EP_ERR_INVALID_ARG;
 
   ep::W4Args a{};
@@ -742,7 +757,9 @@ int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format, const
   if (h->p.dtype != EP_DTYPE_BF16 || h->p.hidden_k % 128 || h->p.send_waves ||
       (h->p.flags & (EP_FLAG_EPILOGUE_ONLY | EP_FLAG_TRACE | EP_FLAG_SEND_TILE)))
     return EP_ERR_UNSUPPORTED;
-  if (uint64_t(m_total) * h->p.hidden_k * 2 >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
+  if (!sink_on && overlap(x, uint64_t(m_total) * h->p.hidden_k * 2, c_local,
+                          uint64_t(m_total) * h->p.hidden_n * 2))
+    return EP_ERR_INVALID_ARG;
   if (!on_device(h)) return EP_ERR_INVALID_ARG;
 
   ep::W4Args a{};

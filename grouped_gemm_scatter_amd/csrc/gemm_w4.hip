@@ -418,9 +418,10 @@ __device__ __forceinline__ void tile_product(const W4Args& wa, const TileWork& t
     if constexpr (!SWIGLU) nb = min(nb, NB - 1);     // past the last column: not stored
     src.run[i] = (uint32_t)nb * KT;
   }
-  const buffer x = make_buffer(a.x);
+  // from the tile's first row, so that 32-bit offsets reach whatever m_total is
+  const buffer x = make_buffer(a.x + (size_t)t.m_abs * a.K * 2);
   // rows past m_end read the group's last row; they are not stored
-  auto row_offset = [&](int r) { return (uint32_t)min(t.m_abs + r, t.g1 - 1) * (uint32_t)(a.K * 2); };
+  auto row_offset = [&](int r) { return (uint32_t)min(r, t.g1 - 1 - t.m_abs) * (uint32_t)(a.K * 2); };
   f32x4 acc[NT][MT];
   if constexpr (T::SPLIT > 1) {
     static_assert(T::SPLIT == kW4Waves && NT == kW4Waves && MT == 1, "one block a wave at the end");

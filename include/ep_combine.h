@@ -472,9 +472,11 @@ typedef struct ep_route_params {
    topk_ids device, [R][tokens_per_rank][top_k] int32, written.
    topk_w   device, [R][tokens_per_rank][top_k] fp32, written.
    tokens_per_rank  0..max_tokens_per_rank.
-   One launch on `stream`, deterministic; uses the handle's n_ranks and top_k and
-   touches none of its buffers.  EP_ERR_INVALID_ARG for a bad size, flag or
-   pointer, or when the handle's device is not the current one;
+   One launch on `stream`, or two (many tokens, and a computed score compared: the
+   second picks the tokens again that the first left marked in topk_ids);
+   deterministic.  Uses the handle's n_ranks and top_k and touches none of its
+   buffers.  EP_ERR_INVALID_ARG for a bad size, flag or pointer, outputs that overlap
+   each other or the logits, or when the handle's device is not the current one;
    EP_ERR_UNSUPPORTED for more experts or groups than the limits. */
 EP_API int ep_route_topk(ep_combine_t h, const ep_route_params* params, const void* logits,
                          const float* bias, int32_t tokens_per_rank, int32_t* topk_ids,
@@ -494,7 +496,8 @@ EP_API int ep_route_topk(ep_combine_t h, const ep_route_params* params, const vo
    logits, topk_ids, tokens_per_rank  as for ep_route_topk.
    grad_w      device, [R][tokens_per_rank][top_k] fp32.
    grad_logits device, [R][tokens_per_rank][n_experts], the logits' type, 16-byte
-               aligned, every value written.  Not the logits themselves.
+               aligned, every value written.  Overlaps none of the inputs
+               (EP_ERR_INVALID_ARG).
    One launch, deterministic. */
 EP_API int ep_route_topk_backward(ep_combine_t h, const ep_route_params* params,
                                   const void* logits, const int32_t* topk_ids,
@@ -518,7 +521,8 @@ EP_API int ep_route_topk_backward(ep_combine_t h, const ep_route_params* params,
    grad_rows device, [m_total][N] bf16, 16-byte aligned, or NULL (then offsets and
              src_info may be NULL too); rows from m_total on are left as they are.
    grad_w    device, [R][tokens_per_rank][top_k] fp32, every value written.
-   One launch, deterministic. */
+   One launch, deterministic.  EP_ERR_INVALID_ARG where grad_rows overlaps grad_out, or
+   grad_w an input. */
 EP_API int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* topk_ids,
                                const float* topk_w, int32_t tokens_per_rank,
                                const int32_t* offsets, const int32_t* src_info, int32_t m_total,
@@ -557,10 +561,10 @@ EP_API int ep_pack_weights_w4(ep_combine_t h, const ep_w4_format* format, const 
    streaming the weights is all of the time.  h_out = bf16( silu(g) * u ), g and u
    summed in fp32 from exact code values, one scale per group (fp32), over k.
    x1, offsets, m_total, h_out as there (any number of rows is right; many rows per
-   expert are faster in bf16 weights); w1 and w1_scale as packed from
-   [E_l][2I][hidden] codes.  A row of x1 holding an infinity or a NaN gives
-   non-finite outputs in that row only.  bf16 handles only (EP_ERR_UNSUPPORTED), I a
-   multiple of 128. */
+   expert are faster in bf16 weights), but h_out overlaps x1 nowhere
+   (EP_ERR_INVALID_ARG); w1 and w1_scale as packed from [E_l][2I][hidden] codes.  An
+   infinity or a NaN in a row of x1 acts as in a plain product, in that row alone.
+   bf16 handles only (EP_ERR_UNSUPPORTED), I a multiple of 128. */
 EP_API int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format, const void* x1,
                                      const void* w1, const void* w1_scale,
                                      const int32_t* offsets, int32_t m_total, void* h_out,
@@ -570,7 +574,7 @@ EP_API int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format,
    gate, epoch and errors, w and w_scale as packed from [E_l][N][K] codes, K a
    multiple of 128 (EP_ERR_UNSUPPORTED).  bf16 handles without EP_FLAG_EPILOGUE_ONLY,
    EP_FLAG_TRACE, EP_FLAG_SEND_TILE or send waves (EP_ERR_UNSUPPORTED);
-   EP_FLAG_W_SLICE_MAJOR plays no part. */
+   EP_FLAG_W_SLICE_MAJOR plays no part.  c_local overlaps x nowhere. */
 EP_API int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format, const void* x,
                                       const void* w, const void* w_scale,
                                       const int32_t* offsets, const int32_t* src_info,

@@ -220,3 +220,56 @@ def test_refusals():
         with pytest.raises(EpError) as e:
             B.ep_combine_backward(ctx.handle, *bad)
         assert e.value.code == B.EP_ERR_INVALID_ARG
+
+
+def test_rows_past_four_gib():
+    """Tokens, slots and rows whose byte offsets pass 32 bits."""
+    T, N = 262144 + 61, 8192
+    cfg = TINY.replace(n_ranks=1, n_experts_global=2, n_experts_local=2, tokens_per_rank=T, top_k=1,
+                       n=N, k=64)
+    ctx = make_ctx(cfg)
+    slots = ctx.recv[0].view(torch.bfloat16).view(T, N)
+    go = torch.empty(1, T, N, dtype=torch.bfloat16, device="cuda")
+    for t in (slots, go[0]):
+        for piece in t.split(32768):
+            piece.copy_(torch.randn(piece.shape, device="cuda"))
+    ids = torch.randint(0, 2, (1, T, 1), dtype=torch.int32, device="cuda")
+    tw = torch.rand(1, T, 1, device="cuda")
+    off, src = ctx.group(ids)
+    assert int(off[-1]) == T
+    gw, gr = ctx.combine_backward(go, ids, tw, off, src, T)
+    torch.cuda.synchronize()
+    assert ctx.query_error() == 0
+    row_of = torch.empty(T, dtype=torch.int64, device="cuda")
+    row_of[src[:T, 0].long()] = torch.arange(T, device="cuda")
+    for at in (slice(0, 300), slice(T // 2, T // 2 + 300), slice(T - 300, T)):
+        a, s = go[0, at].cpu().double(), slots[at].cpu().double()
+        err = (gw[0, at, 0].cpu().double() - (a * s).sum(1)).abs()
+        assert torch.all(err <= 2 * N * 2.0 ** -24 * (a * s).abs().sum(1))
+        want = (tw[0, at] * go[0, at].float()).bfloat16()
+        assert torch.equal(gr[row_of[at]], want)
+
+
+def test_strides_types_and_overlaps_are_refused():
+    cfg = CASES["tiny"]
+    ids, _ = make_routing(cfg)
+    ctx, args, _ = _case(cfg, ids)
+    go, d_ids, tw, off, src, m = args
+    for bad in ((off.cpu(), src), (off.float(), src), (off, src.cpu()), (off, src.float()),
+                (off, src.t())):
+        with pytest.raises(ValueError):
+            ctx.combine_backward(go, d_ids, tw, *bad, m)
+    for rows in (torch.empty(m, cfg.n, dtype=torch.float16, device="cuda"),
+                 torch.empty(m, cfg.n, dtype=torch.bfloat16),
+                 torch.empty(cfg.n, m, dtype=torch.bfloat16, device="cuda").t()):
+        with pytest.raises(ValueError):
+            ctx.combine_backward(*args, grad_rows=rows)
+    both = torch.zeros(go.numel() // cfg.n + m, cfg.n, dtype=torch.bfloat16, device="cuda")
+    go = both[: go.numel() // cfg.n].view(go.shape)
+    args = (go, *args[1:])
+    for kw in (dict(grad_rows=both[both.shape[0] - m - 1:]), dict(grad_w=tw),
+               dict(grad_w=d_ids.view(torch.float32)),
+               dict(grad_w=go.view(-1)[: 2 * tw.numel()].view(torch.float32).view(tw.shape))):
+        with pytest.raises(EpError) as e:
+            ctx.combine_backward(*args, **kw)
+        assert e.value.code == B.EP_ERR_INVALID_ARG

@@ -333,3 +333,42 @@ def test_refusals():
         B.ep_route_topk(ctx.handle, p, l, None, 8, None, w)
     with pytest.raises(EpError):
         B.ep_route_topk(ctx.handle, p, l, None, -1, ids, w)
+
+
+def test_logits_past_four_gib():
+    """Tokens whose byte offsets in the logits pass 32 bits, forward and backward."""
+    T, E = 2_097_152 + 37, 1024
+    opts = dict(score="sigmoid", renormalize=True)
+    ctx = _ctx(1, T, 2)
+    l = torch.empty(1, T, E, dtype=torch.bfloat16, device="cuda")
+    for piece in l[0].split(262144):
+        piece.copy_(torch.randn(piece.shape, device="cuda"))
+    bias = torch.randn(E, device="cuda")
+    ids, w = ctx.route(l, bias=bias, **opts)
+    gw = torch.randn(1, T, 2, device="cuda")
+    grad = ctx.route_backward(l, ids, gw, **opts)
+    dense = ctx.route_backward(l, ids, gw, renormalize=False)
+    last = l[:, -101:].clone()
+    ids2, w2 = ctx.route(last, bias=bias, **opts)
+    assert torch.equal(ids[:, -101:], ids2) and torch.equal(w[:, -101:], w2)
+    gw2 = gw[:, -101:].clone()
+    assert torch.equal(grad[:, -101:], ctx.route_backward(last, ids2, gw2, **opts))
+    assert torch.equal(dense[:, -101:], ctx.route_backward(last, ids2, gw2, renormalize=False))
+    b = bias.cpu().double().numpy()
+    want_ids, _ = P.route(_numpy(last), 2, bias=b, **opts)
+    assert np.array_equal(ids2.cpu().numpy().reshape(-1, 2), want_ids)
+
+
+def test_overlaps_are_refused():
+    ctx = _ctx(1, 8, 4)
+    l = torch.zeros(1, 8, 32, device="cuda")
+    ids, w = ctx.route(l)
+    as_ids = l.view(-1)[:32].view(1, 8, 4).view(torch.int32)
+    as_w, other = l.view(-1)[:32].view(1, 8, 4), torch.zeros_like(l)
+    for call in (lambda: ctx.route(l, topk_ids=as_ids), lambda: ctx.route(l, topk_w=as_w),
+                 lambda: ctx.route(l, topk_ids=ids, topk_w=ids.view(torch.float32)),
+                 lambda: ctx.route_backward(other, as_ids, w, grad_logits=l),
+                 lambda: ctx.route_backward(other, ids, as_w, grad_logits=l)):
+        with pytest.raises(EpError) as e:
+            call()
+        assert e.value.code == B.EP_ERR_INVALID_ARG

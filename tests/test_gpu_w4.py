@@ -418,3 +418,63 @@ def test_from_router_logits_to_the_gradients(tokens):
                                score="sigmoid", scale=2.5)
     tol = 60 * 2.0 ** -24 * 2 * 2.5 * np.abs(gw64).max(1, keepdims=True)
     assert np.all(np.abs(gl.cpu().double().numpy().reshape(-1, E) - want_gl) <= tol)
+
+
+def test_inputs_past_four_gib():
+    """Rows whose byte offsets in x pass 32 bits."""
+    inter, hidden, M = 128, 8192, 262144 + 81
+    ctx, _ = _ctx([1, 1], 1, 1, inter, hidden)
+    rng = np.random.default_rng(6)
+    codes, scales = _weights(rng, 2, 2 * inter, hidden, 128, "bf16")
+    w1 = ctx.pack_weights_w4(to_dev(codes), scales.cuda())
+    x = torch.empty(M, hidden, dtype=torch.bfloat16, device="cuda")
+    for piece in x.split(32768):
+        piece.copy_(torch.randn(piece.shape, device="cuda"))
+    h = torch.empty(M, inter, dtype=torch.bfloat16, device="cuda")
+    ctx.up_swiglu_w4(x, w1, to_dev(np.array([0, 37, M], np.int32)), M, h)
+    # the same rows by themselves
+    last = x[M - 100:].clone()
+    tail = torch.empty(100, inter, dtype=torch.bfloat16, device="cuda")
+    ctx.up_swiglu_w4(last, w1, to_dev(np.array([0, 0, 100], np.int32)), 100, tail)
+    torch.cuda.synchronize()
+    assert ctx.query_error() == 0
+    y, a = P.grouped_product(O.bf16_to_f64(bits(last)), P.weights_w4(
+        codes, scales.double().numpy(), "int4"), np.array([0, 0, 100]))
+    g, u = y[:, :inter], y[:, inter:]
+    silu, bound = g / (1 + np.exp(-g)), _sum_bound(a, hidden, 128)
+    tol = (1.1 * bound[:, :inter] * (np.abs(u) + bound[:, inter:]) + np.abs(silu) * bound[:, inter:] +
+           (2.0 ** -8 + 2.0 ** -20) * np.abs(silu * u) + 1e-38)
+    for got in (h[M - 100:], tail):
+        assert np.all(np.abs(O.bf16_to_f64(bits(got)) - silu * u) <= tol)
+
+
+def test_strides_types_and_overlaps_are_refused():
+    k, n = 128, 128
+    ctx, _ = _ctx([4, 4], 1, 8, k, n)
+    w = ctx.pack_weights_w4(torch.zeros(2, n, k // 2, dtype=torch.uint8, device="cuda"),
+                            torch.ones(2, n, k // 32, device="cuda").bfloat16())
+    w1 = ctx.pack_weights_w4(torch.zeros(2, 2 * k, n // 2, dtype=torch.uint8, device="cuda"),
+                             torch.ones(2, 2 * k, n // 32, device="cuda").bfloat16())
+    x = torch.zeros(8, k, dtype=torch.bfloat16, device="cuda")
+    h, c = torch.zeros_like(x), torch.zeros_like(x)
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    src = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    for bad in ((x.half(), off, src, c), (x.cpu(), off, src, c), (x, off.cpu(), src, c),
+                (x, off, src.cpu(), c), (x, off, src, c.cpu()), (x, off, src.float(), c),
+                (torch.zeros(k, 8, dtype=torch.bfloat16, device="cuda").t(), off, src, c),
+                (x, off, src, torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda").t())):
+        with pytest.raises(ValueError):
+            ctx.gemm_scatter_w4(bad[0], w, bad[1], bad[2], 8, p3_control=-1, c_local=bad[3])
+    for bad in ((x.half(), off, h), (x, off.cpu(), h), (x, off, h.float()), (x, off, h.t())):
+        with pytest.raises(ValueError):
+            ctx.up_swiglu_w4(bad[0], w1, bad[1], 8, bad[2])
+    with pytest.raises(EpError) as e:
+        ctx.up_swiglu_w4(x, w1, off, 8, x)
+    assert e.value.code == B.EP_ERR_INVALID_ARG
+    with pytest.raises(EpError) as e:
+        ctx.gemm_scatter_w4(x, w, off, src, 8, p3_control=-1, c_local=x)
+    assert e.value.code == B.EP_ERR_INVALID_ARG
+    ctx.up_swiglu_w4(x, w1, off, 8, h)
+    ctx.gemm_scatter_w4(x, w, off, src, 8, p3_control=-1, c_local=c)
+    torch.cuda.synchronize()
+    assert ctx.query_error() == 0
