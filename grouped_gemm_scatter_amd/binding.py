@@ -208,12 +208,13 @@ def _ptr(t, dtype=None, name="tensor", allow_none=False):
 
 # the current stream's handle without the stream object around it (2.5 us less a call)
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _current_raw_stream is not None:
-            return _current_raw_stream(torch.cuda.current_device())
+            return _current_raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -4,6 +4,7 @@ creates the library handle and counts step epochs.  Every computation is a
 call into the HIP library."""
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -19,6 +20,18 @@ def _choice(table: dict, value, name: str) -> int:
     if value not in table:
         raise ValueError(f"{name} must be one of {sorted(table)}, not {value!r}")
     return table[value]
+
+
+@functools.lru_cache(maxsize=64)
+def _route_params(n_experts, logits_dtype, n_groups, topk_groups, score, group_score, renormalize,
+                  scale):
+    """The options of a routing call as the C boundary takes them (never changed, so one
+    object serves every call with the same options)."""
+    return B.make_route_params(
+        n_experts=n_experts, logits_dtype=logits_dtype, n_groups=n_groups,
+        topk_groups=topk_groups, score=_choice(_SCORES, score, "score"),
+        group_score=_choice(_GROUP_SCORES, group_score, "group_score"),
+        renormalize=renormalize, scale=scale)
 
 
 @dataclass(frozen=True)
@@ -133,30 +146,32 @@ class EpCombine:
             raise ValueError(f"{name}: {t.numel()} elements, at least {elems} needed")
 
     def _shape(self, t, name: str, shape: tuple, dtype):
-        """Raises unless `t` is a contiguous tensor of this shape and type on the
-        handle's device."""
+        """Address of `t`; raises unless it is a contiguous tensor of this shape and type
+        on the handle's device."""
+        if (t.dtype is dtype and t.shape == shape and t.is_cuda and
+                t.get_device() == self._device_index and t.is_contiguous()):
+            return t.data_ptr()
         if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         if not t.is_cuda or t.get_device() != self._device_index:
             raise ValueError(f"{name} must be on the handle's device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} must be contiguous")
 
     def _flat(self, t, name: str, elems: int, dtype):
-        """Raises unless `t` is a contiguous tensor of this type on the handle's device with
-        at least `elems` elements."""
+        """Address of `t` (None and addresses as they are); raises unless it is a contiguous
+        tensor of this type on the handle's device with at least `elems` elements."""
         if t is None or isinstance(t, int):
-            return
+            return t
         if t.numel() < elems:
             raise ValueError(f"{name}: {t.numel()} elements, at least {elems} needed")
-        self._shape(t, name, t.shape, dtype)
+        return self._shape(t, name, t.shape, dtype)
 
     def _empty(self, shape, dtype, stream):
         """Memory for what a call returns, allocated on the stream that it runs on."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(*shape, dtype=dtype, device=self.device)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream)
         with torch.cuda.stream(stream):
@@ -172,15 +187,11 @@ class EpCombine:
         topk_groups best groups are picked from, by their largest choice ("max") or the
         sum of their two largest ("top2")."""
         R, T, E = logits.shape
-        params = B.make_route_params(
-            n_experts=E, logits_dtype=logits.dtype, n_groups=n_groups, topk_groups=topk_groups,
-            score=_choice(_SCORES, score, "score"),
-            group_score=_choice(_GROUP_SCORES, group_score, "group_score"),
-            renormalize=renormalize, scale=scale)
+        params = _route_params(E, logits.dtype, n_groups, topk_groups, score, group_score,
+                               renormalize, scale)
         shape = (self.n_ranks, T, self.top_k)
-        self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
-        if bias is not None:
-            self._shape(bias, "bias", (E,), torch.float32)
+        at = self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
+        bias_at = None if bias is None else self._shape(bias, "bias", (E,), torch.float32)
         if topk_ids is None:
             topk_ids = self._empty(shape, torch.int32, stream)
         else:
@@ -189,7 +200,8 @@ class EpCombine:
             topk_w = self._empty(shape, torch.float32, stream)
         else:
             self._shape(topk_w, "topk_w", shape, torch.float32)
-        B.ep_route_topk(self.handle, params, logits, bias, T, topk_ids, topk_w, stream)
+        B.ep_route_topk(self.handle, params, at, bias_at, T, topk_ids.data_ptr(),
+                        topk_w.data_ptr(), stream)
         return topk_ids, topk_w
 
     def route_backward(self, logits, topk_ids, grad_w, *, score: str = "softmax",
@@ -198,19 +210,17 @@ class EpCombine:
         """Gradient of `route`'s topk_w with respect to its logits (in their type), from
         the picks it returned and the gradient grad_w [R][T][top_k] of their weights."""
         R, T, E = logits.shape
-        params = B.make_route_params(n_experts=E, logits_dtype=logits.dtype,
-                                     score=_choice(_SCORES, score, "score"),
-                                     renormalize=renormalize, scale=scale)
+        params = _route_params(E, logits.dtype, 1, 1, score, "max", renormalize, scale)
         shape = (self.n_ranks, T, self.top_k)
-        self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
-        self._shape(topk_ids, "topk_ids", shape, torch.int32)
-        self._shape(grad_w, "grad_w", shape, torch.float32)
+        at = self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
+        ids_at = self._shape(topk_ids, "topk_ids", shape, torch.int32)
+        grad_at = self._shape(grad_w, "grad_w", shape, torch.float32)
         if grad_logits is None:
-            grad_logits = self._empty(logits.shape, logits.dtype, stream)
+            grad_logits = self._empty((R, T, E), logits.dtype, stream)
         else:
-            self._shape(grad_logits, "grad_logits", logits.shape, logits.dtype)
-        B.ep_route_topk_backward(self.handle, params, logits, topk_ids, grad_w, T, grad_logits,
-                                 stream)
+            self._shape(grad_logits, "grad_logits", (R, T, E), logits.dtype)
+        B.ep_route_topk_backward(self.handle, params, at, ids_at, grad_at, T,
+                                 grad_logits.data_ptr(), stream)
         return grad_logits
 
     def combine_backward(self, grad_out, topk_ids, topk_w, offsets, src_info, m_total, *,
@@ -221,26 +231,27 @@ class EpCombine:
         m_total on stay as they are; rows=False leaves it out (None is returned)."""
         T, N, m = grad_out.shape[1], self.hidden_n, int(m_total)
         shape = (self.n_ranks, T, self.top_k)
-        self._shape(grad_out, "grad_out", (self.n_ranks, T, N), torch.bfloat16)
-        self._shape(topk_ids, "topk_ids", shape, torch.int32)
-        self._shape(topk_w, "topk_w", shape, torch.float32)
+        at = self._shape(grad_out, "grad_out", (self.n_ranks, T, N), torch.bfloat16)
+        ids_at = self._shape(topk_ids, "topk_ids", shape, torch.int32)
+        w_at = self._shape(topk_w, "topk_w", shape, torch.float32)
+        offsets_at = src_at = rows_at = None
         if rows:
-            self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1,
-                       torch.int32)
-            self._flat(src_info, "src_info", 2 * m, torch.int32)
+            offsets_at = self._flat(offsets, "offsets",
+                                    self.n_experts_per_device * self.n_ranks + 1, torch.int32)
+            src_at = self._flat(src_info, "src_info", 2 * m, torch.int32)
             if grad_rows is None:
                 grad_rows = self._empty((m, N), torch.bfloat16, stream)
-            self._flat(grad_rows, "grad_rows", m * N, torch.bfloat16)
+            rows_at = self._flat(grad_rows, "grad_rows", m * N, torch.bfloat16)
+            if m == 0:
+                rows_at = None           # an empty tensor has no address: no rows are asked for
         elif grad_rows is not None:
             raise ValueError("grad_rows given with rows=False")
         if grad_w is None:
             grad_w = self._empty(shape, torch.float32, stream)
         else:
             self._shape(grad_w, "grad_w", shape, torch.float32)
-        # an empty tensor has no address: no rows are asked for then
-        out = grad_rows if rows and m > 0 else None
-        B.ep_combine_backward(self.handle, grad_out, topk_ids, topk_w, T, offsets, src_info, m,
-                              out, grad_w, stream)
+        B.ep_combine_backward(self.handle, at, ids_at, w_at, T, offsets_at, src_at, m, rows_at,
+                              grad_w.data_ptr(), stream)
         return grad_w, grad_rows
 
     def pack_weights_w4(self, w, scales, *, codes: str = "int4", stream=None) -> PackedW4:
@@ -271,10 +282,11 @@ class EpCombine:
     def up_swiglu_w4(self, x1, w1: PackedW4, offsets, m_total, h_out, *, stream=None):
         """up_swiglu on 4-bit weights packed from [E_l][2*hidden_k][hidden_n] codes."""
         hid, inter = self.hidden_n, self.hidden_k
-        self._flat(x1, "x1", m_total * hid, torch.bfloat16)
+        x1 = self._flat(x1, "x1", m_total * hid, torch.bfloat16)
         self._need_w4(w1, 2 * inter, hid)
-        self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, torch.int32)
-        self._flat(h_out, "h_out", m_total * inter, torch.bfloat16)
+        offsets = self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1,
+                             torch.int32)
+        h_out = self._flat(h_out, "h_out", m_total * inter, torch.bfloat16)
         return B.ep_grouped_gemm_swiglu_w4(self.handle, w1.format, x1, w1.codes, w1.scales, offsets,
                                            m_total, h_out, stream)
 
@@ -282,12 +294,13 @@ class EpCombine:
                         c_local=None, epoch: int | None = None, stream=None):
         """gemm_scatter on 4-bit weights packed from [E_l][hidden_n][hidden_k] codes."""
         K, N = self.hidden_k, self.hidden_n
-        self._flat(x, "x", m_total * K, torch.bfloat16)
+        x = self._flat(x, "x", m_total * K, torch.bfloat16)
         self._need_w4(w, N, K)
-        self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1, torch.int32)
-        self._flat(src_info, "src_info", 2 * m_total, torch.int32)
+        offsets = self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1,
+                             torch.int32)
+        src_info = self._flat(src_info, "src_info", 2 * m_total, torch.int32)
         if p3_control < 0:
-            self._flat(c_local, "c_local", m_total * N, torch.bfloat16)
+            c_local = self._flat(c_local, "c_local", m_total * N, torch.bfloat16)
         return B.ep_grouped_gemm_scatter_w4(self.handle, w.format, x, w.codes, w.scales, offsets,
                                             src_info, m_total, p3_control, c_local,
                                             self._epoch(epoch), stream)

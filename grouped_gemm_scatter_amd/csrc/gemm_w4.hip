@@ -546,14 +546,14 @@ __global__ __launch_bounds__(kW4Threads, T::PER_CU) void gemm_w4_kernel(W4Args w
     } else {
       // sent rows are written through: a fence per workgroup, each a write-back of its
       // XCD's L2, took 39 of the 62 us of a one-token launch and 20 of a decode step's 95
-      constexpr int TPR = OUT * 2 / 8, RPP = kW4Threads / TPR;
-      const int cc = tid % TPR, col = col0 + cc * 4;
+      constexpr int TPR = OUT * 2 / 16, RPP = kW4Threads / TPR;
+      const int cc = tid % TPR, col = col0 + cc * 8;
       if (col < width)
         for (int r = tid / TPR; r < t.rows; r += RPP) {
           const uint64_t dst = s_rowdst[r];
           if (dst)
-            store8_through(reinterpret_cast<uint8_t*>(dst) + (size_t)col * 2,
-                           *reinterpret_cast<const uint64_t*>(smem + r * PITCH + cc * 8));
+            store16_through(reinterpret_cast<uint8_t*>(dst) + (size_t)col * 2,
+                            *reinterpret_cast<const u32x4*>(smem + r * PITCH + cc * 16));
         }
     }
     if constexpr (!SWIGLU) {
@@ -614,13 +614,30 @@ hipError_t launch_tile(const W4Args& a, bool swiglu, int num_cus, hipStream_t st
   return hipGetLastError();
 }
 
+// The tile by how many of each a launch is likely to have (only the device knows the
+// groups): an expert's last tile is half full on average, and every expert has one.
+// Measured at K 2048, group 64, equal groups, us (decode / narrow / thin tile):
+//   E  4, N 2048, 16 rows each   21.3 / 14.4 /  9.8   128 thin tiles
+//   E 16, N 2048, 16 rows        21.9 / 15.4 / 15.2   512
+//   E  4, N 7168, 24 rows        23.4 / 16.7 / 21.8   896
+//   E 32, N 2048,  1 row         23.7 / 20.6 / 21.1   1024, of one row
+//   E 32, N 2048, 64 rows        32.1 / 29.6 / 72.7   512 narrow tiles
+//   E 16, N 7168,  8 rows        32.4 / 35.2 / 35.9   896
+//   E 32, N 2048, 128 rows       45.7 / 55.7 / 134    1024
+// so: thin tiles up to two a CU, or up to four where they have few rows to repeat the
+// weights for; narrow ones up to two a CU, which is one round of them; else the largest.
 template <class F>
 hipError_t launch(const W4Args& a, bool swiglu, int num_cus, hipStream_t st) {
   const int64_t El = a.g.s.n_experts, m = a.g.m_total, active = m < El ? m : El;
-  const int64_t tiles = active * ((a.g.N + DecodeTile::COLS - 1) / DecodeTile::COLS);
-  if (tiles >= 2 * num_cus) return launch_tile<DecodeTile, F>(a, swiglu, num_cus, st);
-  if (m > 8 * El) return launch_tile<NarrowTile, F>(a, swiglu, num_cus, st);
-  return launch_tile<ThinTile, F>(a, swiglu, num_cus, st);
+  auto tiles = [&](int rows, int cols) {
+    const int64_t by_rows = m / rows + active / 2;
+    return (by_rows > active ? by_rows : active) * ((a.g.N + cols - 1) / cols);
+  };
+  if (tiles(ThinTile::ROWS, ThinTile::COLS) <= (m <= 8 * active ? 4 : 2) * (int64_t)num_cus)
+    return launch_tile<ThinTile, F>(a, swiglu, num_cus, st);
+  if (tiles(NarrowTile::ROWS, NarrowTile::COLS) <= 2 * (int64_t)num_cus)
+    return launch_tile<NarrowTile, F>(a, swiglu, num_cus, st);
+  return launch_tile<DecodeTile, F>(a, swiglu, num_cus, st);
 }
 
 template <int CODES, int GROUP>

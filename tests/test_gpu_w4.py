@@ -478,3 +478,15 @@ def test_strides_types_and_overlaps_are_refused():
     ctx.gemm_scatter_w4(x, w, off, src, 8, p3_control=-1, c_local=c)
     torch.cuda.synchronize()
     assert ctx.query_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=lambda f: "-".join(map(str, f)))
+@pytest.mark.parametrize("name", ["edges", "large_group"])
+def test_down_projection_of_the_narrow_tile(name, fmt):
+    # too many 16-row tiles for the GPU, too few of 256 columns
+    _down(name, fmt, 384, 2048 - 128 if name == "edges" else 4096, R=3)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=lambda f: "-".join(map(str, f)))
+def test_up_projection_of_the_narrow_tile(fmt):
+    test_up_projection(fmt, "edges", 1152, 256)
