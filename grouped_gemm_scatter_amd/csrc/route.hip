@@ -31,8 +31,21 @@ namespace {
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / 64;
 
-// A missing expert (NaN, -infinity) is -infinity; +infinity the largest number.
-__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
+// A missing expert (NaN, -infinity) is -infinity; +infinity the largest number: the median
+// of those two and a logit, which for a quiet NaN is the least of the others (written
+// out, because the compiler drops the -infinity).
+__device__ __forceinline__ float clean(float v) {
+  v = __builtin_canonicalizef(v);
+  asm("v_med3_f32 %0, %0, %1, %2" : "+v"(v) : "s"(-INFINITY), "v"(FLT_MAX));
+  return v;
+}
+
+// A lane's first expert, as a value that the compiler does not follow: bounds and
+// quotients of rare paths would otherwise be computed for every token.
+__device__ __forceinline__ int opaque(int first) {
+  asm volatile("" : "+v"(first));
+  return first;
+}
 
 __device__ __forceinline__ float f16_value(uint32_t v) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
@@ -78,8 +91,9 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int lane
     }
     return;
   }
+  const int i = opaque(first);
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = first + j < E ? load_logit(a, at + j) : -INFINITY;
+  for (int j = 0; j < VPL; ++j) x[j] = i + j < E ? load_logit(a, at + j) : -INFINITY;
 }
 
 template <int VPL>
@@ -255,7 +269,7 @@ __device__ __forceinline__ float pick_share(float l, bool there, int score) {
   return there ? e * __builtin_amdgcn_rcpf(sum) : 0.f;
 }
 
-// Bias of the lane's experts: 0 without one, -infinity for an expert that it keeps out.
+// Bias of the lane's experts, 0 without one (an expert that it keeps out: NaN or -infinity).
 template <int VPL>
 __device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&b)[VPL]) {
   const int first = lane * VPL;
@@ -272,32 +286,32 @@ __device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&
       }
     }
   } else {
+    const int i = opaque(first);
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
-      if (first + j < a.n_experts) b[j] = a.bias[first + j];
+      if (i + j < a.n_experts) b[j] = a.bias[i + j];
   }
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) b[j] = b[j] > -INFINITY ? b[j] : -INFINITY;
 }
 
 // Bounds on the error of a binary32 score plus bias, over 1 + the largest such sum of the
-// token.  A softmax score is within s (|l - top| + 30) 2^-24 <= 31 * 2^-24 (the argument's
-// rounding, the exponential, a sum of at most 16 + 6 additions, the division), a sigmoid
-// within s (1 - s) 4 + 3 s <= 4 times 2^-24 (the exponential; the sum, the reciprocal),
-// and the bias adds one rounding of the sum.
+// token.  The exponential's argument d, within 2.5 |d| 2^-24, is rounded, 2^d is within
+// 2^-23 of itself: in a softmax score s that is within s (2.5 |d| + 2 + 25) 2^-24 <=
+// 28 * 2^-24 (a sum of at most 16 + 6 additions and the division), in a sigmoid within
+// s (1 - s) (2.5 |d| + 2) + 3 s <= 5 times 2^-24 (the addition, the reciprocal); the bias
+// adds one rounding of the sum.
 __device__ __forceinline__ float choice_error(int score) {
   return score == EP_SCORE_SOFTMAX ? 0x1p-19f : 0x1p-21f;
 }
 
-// The picks of one token, lane k's id (or -1) in lane k.  key: the choices, score: scores
-// plus bias, -infinity for what cannot be picked, each within `error` unless `exact`.
-// Returns whether none that decide lie within their error of each other.
+// Takes the experts outside the topk_groups best groups out of a token's choices `key`.
+// score: scores plus bias; both -infinity for what cannot be picked, and each within
+// `error` unless `exact`.  Returns whether the groups at the limit lie further apart than that.
 // lanes: lanes of a group where that is a power of two of whole lanes, 0: no groups,
 // -1: groups of any other size.
 template <int LPT, int VPL, class T>
-__device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL],
-                                     const T (&score)[VPL], bool exact, float error, int lanes,
-                                     int& id) {
+__device__ __forceinline__ bool limit_groups(const RouteArgs& a, int lane, T (&key)[VPL],
+                                             const T (&score)[VPL], bool exact, float error,
+                                             int lanes) {
   constexpr T none = -INFINITY;
   bool sure = true;
   if (lanes != 0) {
@@ -319,11 +333,12 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL]
         v1 = larger(v1, o1);
       }
     } else {
+      const int first = opaque(lane * VPL);
       for (int g = 0; g < a.n_groups; ++g) {
         T w1 = none, w2 = none;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-          const int i = lane * VPL + j - g * per;
+          const int i = first + j - g * per;
           const T y = i < 0 || i >= per ? none : by[j];
           w2 = larger(w2, smaller(w1, y));
           w1 = larger(w1, y);
@@ -359,11 +374,21 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL]
       for (int j = 0; j < VPL; ++j) key[j] = keep ? key[j] : none;
     } else {
       const uint64_t kept = __ballot(keep) >> (LPT == 16 ? threadIdx.x & 48 : 0);   // by group
+      const int first = opaque(lane * VPL);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        key[j] = kept >> min((lane * VPL + j) / per, 63) & 1 ? key[j] : none;
+      for (int j = 0; j < VPL; ++j) key[j] = kept >> min((first + j) / per, 63) & 1 ? key[j] : none;
     }
   }
+  return sure;
+}
+
+// The picks of one token, lane k's id (or -1) in lane k.  key: the choices, within `error`
+// unless `exact`.  Returns whether none that decide lie within their error of each other.
+template <int LPT, int VPL, class T>
+__device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL], bool exact,
+                                     float error, int& id) {
+  constexpr T none = -INFINITY;
+  bool sure = true;
   T before = INFINITY;
   id = -1;
   // one more pick than asked for, to see how near it comes
@@ -394,7 +419,87 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, int lane, T (&key)[VPL]
   return sure;
 }
 
-// Lanes of a group for pick().
+// Batcher's odd-even merge sort of N values as a list of the pairs it compares.
+template <int N>
+struct SortingNetwork {
+  int a[64] = {}, b[64] = {}, size = 0;
+  constexpr SortingNetwork() {
+    for (int p = 1; p < N; p *= 2)
+      for (int k = p; k >= 1; k /= 2)
+        for (int j = k % p; j + k < N; j += 2 * k)
+          for (int i = j; i < j + k && i + k < N; ++i)
+            if (i / (2 * p) == (i + k) / (2 * p)) {
+              a[size] = i;
+              b[size++] = i + k;
+            }
+  }
+};
+
+// pick() for biased scores, 16 lanes a token: choices as integers of 2^-24 with their place
+// among the lane's VPL in the low four bits, sorted within the lane first, so that a
+// pick is the largest head of 16 lists and a step of the list that had it, about 25
+// instructions instead of 130.  The integers hold choices below 8 in magnitude.  Equal ones
+// of two lanes step together, which the count of steps shows.
+// L: entries of a list that matter to so many picks.
+template <int L, int VPL>
+__device__ __forceinline__ bool take_heads(const int (&list)[VPL], int picks, int wanted, int lane,
+                                           uint32_t apart, int* ids, int& found) {
+  constexpr int none = -0x7fffffff - 1 + 16;   // below: no choice
+  int head[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) head[i] = list[i];
+  bool sure = true;
+  int before = 0, steps = 0;
+  found = 0;
+  for (int k = 0; k < picks; ++k) {
+    int m = head[0];
+    asm("s_nop 1\n\tv_max_i32_dpp %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_i32_dpp %0, %0, %0 row_ror:4 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_i32_dpp %0, %0, %0 row_ror:2 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_i32_dpp %0, %0, %0 row_ror:1 row_mask:0xf bank_mask:0xf" : "+v"(m));
+    const bool is = m >= none;
+    if (k > 0 && is && !((uint32_t)before - (uint32_t)m > apart)) sure = false;
+    before = m;
+    found += is;
+    const bool win = is && head[0] == m;
+    if (k < wanted && win) ids[k] = lane * VPL + (m & 15);
+    // by a mask: of a condition the compiler makes a variable index into the list
+    const int step = win ? -1 : 0;
+    steps -= step;
+#pragma unroll
+    for (int i = 0; i + 1 < L; ++i) head[i] = (step & head[i + 1]) | (~step & head[i]);
+    head[L - 1] = (step & (none - 16)) | (~step & head[L - 1]);
+  }
+  return sure && (int)lanes_sum<16>((float)steps) == found;
+}
+template <int VPL>
+__device__ __forceinline__ bool pick_sorted(const RouteArgs& a, int lane, const float (&key)[VPL],
+                                            float largest, float error, int* ids, int& id) {
+  int list[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    list[j] = (int)__builtin_amdgcn_fmed3f(key[j] * 0x1p24f, -0x1p27f, 0x1p27f - 16.f) * 16 + j;
+  constexpr SortingNetwork<VPL> net;
+#pragma unroll
+  for (int c = 0; c < net.size; ++c) {
+    const int x = list[net.a[c]], y = list[net.b[c]];
+    list[net.a[c]] = max(x, y);
+    list[net.b[c]] = min(x, y);
+  }
+  // one more pick than asked for; both conversions cut less than a unit off
+  const int picks = a.top_k + 1;
+  const uint32_t apart = (uint32_t)(2.f * error * 0x1p28f) + 32;
+  bool sure;
+  int found;
+  if (picks <= 9)
+    sure = take_heads<(VPL < 9 ? VPL : 9), VPL>(list, picks, a.top_k, lane, apart, ids, found);
+  else
+    sure = take_heads<VPL, VPL>(list, picks, a.top_k, lane, apart, ids, found);
+  id = lane < min(a.top_k, found) ? ids[lane] : -1;
+  return sure && largest < 7.9f;
+}
+
+// Lanes of a group for limit_groups().
 template <int VPL>
 __device__ __forceinline__ int group_lanes(const RouteArgs& a) {
   const int per = a.n_experts / a.n_groups, span = per / VPL;
@@ -424,7 +529,8 @@ __device__ __forceinline__ int pick_binary64(const RouteArgs& a, int lane, const
     key[j] = a.bias ? score[j] : x[j];
   }
   int id;
-  pick<64, VPL, double>(a, lane, key, score, true, 0.f, group_lanes<VPL>(a), id);
+  limit_groups<64, VPL, double>(a, lane, key, score, true, 0.f, group_lanes<VPL>(a));
+  pick<64, VPL, double>(a, lane, key, true, 0.f, id);
   return id;
 }
 
@@ -473,24 +579,27 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   const int64_t waves = (int64_t)gridDim.x * kRouteWaves;
   const int E = a.n_experts, lanes = group_lanes<VPL>(a);
   const bool exact = !a.bias && !(a.n_groups > 1 && a.group_score == EP_GROUP_TOP2);
+  const bool biased = a.bias != nullptr;
+  __shared__ int s_ids[HERE ? 1 : kRouteThreads / LPT][16];
   for (int64_t first = wave * TPW; first < a.tokens; first += waves * TPW) {
     const int64_t t = first + row;
     const bool token = t < a.tokens;           // the last wave's may be fewer
     float x[VPL];
     load_row<VPL>(a, t, token ? lane : E, x);
     const float top = largest<LPT>(x);
-    float key[VPL], score[VPL], error = 0.f;
+    float key[VPL], score[VPL], error = 0.f, size = 0.f;
     if (exact) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j) key[j] = x[j];
     } else {
       load_bias<VPL>(a, lane, key);
       float inv = 1.f;
+      constexpr float log2e = 0x1.715476p0f;
       if (a.score == EP_SCORE_SOFTMAX) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-          score[j] = exp_near(x[j] - top);
+          score[j] = __builtin_amdgcn_exp2f((x[j] - top) * log2e);
           sum += score[j];
         }
         sum = lanes_sum<LPT>(sum);
@@ -498,19 +607,25 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
       } else {
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
-          score[j] = __builtin_amdgcn_rcpf(1.f + exp_near(fminf(-x[j], 88.f)));
+          score[j] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[j] * -log2e));
       }
-      const bool biased = a.bias != nullptr;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        score[j] = x[j] > -INFINITY ? score[j] * inv + key[j] : -INFINITY;
+        const float v = score[j] * inv + key[j];
+        const bool there = x[j] > -INFINITY && v > -INFINITY;
+        score[j] = there ? v : -INFINITY;
         key[j] = biased ? score[j] : x[j];
-        error = fmaxf(error, score[j] > -INFINITY ? fabsf(score[j]) : 0.f);
+        size = fmaxf(size, there ? fabsf(v) : 0.f);
       }
-      error = choice_error(a.score) * (1.f + lanes_max<LPT>(error));
+      size = lanes_max<LPT>(size);
+      error = choice_error(a.score) * (1.f + size);
     }
     int id;
-    const bool sure = pick<LPT, VPL, float>(a, lane, key, score, exact, error, lanes, id);
+    bool sure = limit_groups<LPT, VPL, float>(a, lane, key, score, exact, error, lanes);
+    if (!HERE && biased)
+      sure &= pick_sorted<VPL>(a, lane, key, size, error, s_ids[HERE ? 0 : threadIdx.x / LPT], id);
+    else
+      sure &= pick<LPT, VPL, float>(a, lane, key, exact, error, id);
     if constexpr (HERE) {
       if (!sure) id = pick_binary64<VPL>(a, lane, x, top);
     } else if (token && !sure && lane == 0) {

@@ -372,3 +372,34 @@ def test_overlaps_are_refused():
         with pytest.raises(EpError) as e:
             call()
         assert e.value.code == B.EP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("T", [5, 4100])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_signaling_nans_are_missing_experts(dtype, T):
+    ctx = _ctx(1, T, 2)
+    l = torch.randn(1, T, 16).to(DTYPES[dtype])
+    bits = l.view(torch.int32 if dtype == "f32" else torch.int16)
+    bits[..., 3] = 0x7f800001 if dtype == "f32" else 0x7f81
+    bits[..., 8] = -0x7fffff if dtype == "f32" else -0x7f     # the same, negative
+    for opts in (dict(), dict(score="sigmoid", n_groups=4, topk_groups=2, group_score="top2")):
+        for bias in (None, torch.zeros(16)):
+            ids, _ = ctx.route(l.cuda(), bias=None if bias is None else bias.cuda(), **opts)
+            want, _ = P.route(_numpy(l), 2, bias=None if bias is None else bias.numpy(), **opts)
+            assert np.array_equal(ids.cpu().numpy()[0], want)
+
+
+@pytest.mark.parametrize("large", [0.0, 6.0, 9.0, 1e6])
+@pytest.mark.parametrize("E,top_k", [(256, 8), (200, 16), (60, 9), (100, 3)])
+def test_biases_of_any_size_over_many_tokens(large, E, top_k):
+    """Biases that leave the range in which choices are compared as integers, on both
+    sides, and groups whose experts are all one lane's."""
+    T = 4099
+    ctx = _ctx(1, T, top_k)
+    l = _logits(E + top_k, 1, T, E, "f32", masked=True)
+    bias = torch.linspace(-1, 1, E) * large + 0.1 * torch.randn(E)
+    for opts in (dict(score="sigmoid"), dict(n_groups=E // 4 if E == 60 else 4, topk_groups=2,
+                                             renormalize=False)):
+        ids, _ = ctx.route(l.cuda(), bias=bias.cuda(), **opts)
+        want, _ = P.route(_numpy(l), top_k, bias=bias.numpy(), **opts)
+        assert np.array_equal(ids.cpu().numpy()[0], want)
