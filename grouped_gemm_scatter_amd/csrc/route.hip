@@ -258,7 +258,8 @@ __device__ __forceinline__ float exp_near(float x) {
 }
 
 // Shares of the picks, lane k holding pick k's logit l (there: lane k has a pick):
-// softmax over the picks, or their sigmoids over the sum.
+// softmax over the picks, or their sigmoids over the sum.  The division is a rounded one, so
+// that the share of a single pick is 1 and its gradient 0.
 template <int LPT>
 __device__ __forceinline__ float pick_share(float l, bool there, int score) {
   const float low = score == EP_SCORE_SIGMOID ? fminf(l, 0.f) : l;
@@ -266,7 +267,7 @@ __device__ __forceinline__ float pick_share(float l, bool there, int score) {
   float e = there ? exp_near(low - top) : 0.f;
   if (score == EP_SCORE_SIGMOID) e *= __builtin_amdgcn_rcpf(1.f + exp_near(-fabsf(l)));
   const float sum = lanes_sum<LPT>(e);
-  return there ? e * __builtin_amdgcn_rcpf(sum) : 0.f;
+  return there ? e / sum : 0.f;
 }
 
 // Bias of the lane's experts, 0 without one (an expert that it keeps out: NaN or -infinity).

@@ -403,3 +403,15 @@ def test_biases_of_any_size_over_many_tokens(large, E, top_k):
         ids, _ = ctx.route(l.cuda(), bias=bias.cuda(), **opts)
         want, _ = P.route(_numpy(l), top_k, bias=bias.numpy(), **opts)
         assert np.array_equal(ids.cpu().numpy()[0], want)
+
+
+@pytest.mark.parametrize("T", [7, 4101])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_single_pick_has_the_whole_weight_and_no_gradient(score, dtype, T):
+    ctx = _ctx(1, T, 1)
+    l = _logits(T, 1, T, 60, dtype, spread=4.0).cuda()
+    ids, w = ctx.route(l, score=score, scale=2.5)
+    assert torch.all(w == 2.5)
+    d = ctx.route_backward(l, ids, torch.randn(1, T, 1, device="cuda"), score=score, scale=2.5)
+    assert torch.all(d == 0)
