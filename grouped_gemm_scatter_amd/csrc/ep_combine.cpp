@@ -661,6 +661,7 @@ int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* top
   const uint64_t go_bytes = tokens * h->p.hidden_n * 2, w_bytes = tokens * h->p.top_k * 4;
   const uint64_t rows_bytes = grad_rows ? uint64_t(m_total) * h->p.hidden_n * 2 : 0;
   if (overlap(grad_out, go_bytes, grad_rows, rows_bytes) ||
+      overlap(grad_w, w_bytes, grad_rows, rows_bytes) ||
       overlap(grad_out, go_bytes, grad_w, w_bytes) || overlap(topk_ids, w_bytes, grad_w, w_bytes) ||
       overlap(topk_w, w_bytes, grad_w, w_bytes))
     return EP_ERR_INVALID_ARG;

@@ -446,9 +446,11 @@ struct SortingNetwork {
 // pick() for biased scores, 16 lanes a token: choices as integers of 2^-24 with their place
 // among the lane's VPL in the low four bits, sorted within the lane first, so that a
 // pick is the largest head of 16 lists and a step of the list that had it, about 25
-// vector instructions instead of 85.  The integers hold choices below 8 in magnitude.  Equal ones
-// of two lanes step together, which the count of steps shows.
+// vector instructions instead of 85.  The integers hold choices below 8 in magnitude,
+// others are left to pick().  Equal ones of two lanes step together, which the count of
+// steps shows.
 // L: entries of a list that matter to so many picks.
+constexpr float kSortedBelow = 7.9f;
 template <int L, int VPL>
 __device__ __forceinline__ bool take_heads(const int (&list)[VPL], int picks, int wanted, int lane,
                                            uint32_t apart, int* ids, int& found) {
@@ -482,7 +484,7 @@ __device__ __forceinline__ bool take_heads(const int (&list)[VPL], int picks, in
 }
 template <int VPL>
 __device__ __forceinline__ bool pick_sorted(const RouteArgs& a, int lane, const float (&key)[VPL],
-                                            float largest, float error, int* ids, int& id) {
+                                            float error, int* ids, int& id) {
   int list[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j)
@@ -504,7 +506,7 @@ __device__ __forceinline__ bool pick_sorted(const RouteArgs& a, int lane, const 
   else
     sure = take_heads<VPL, VPL>(list, picks, a.top_k, lane, apart, ids, found);
   id = lane < min(a.top_k, found) ? ids[lane] : -1;
-  return sure && largest < 7.9f;
+  return sure;
 }
 
 // Lanes of a group for limit_groups().
@@ -630,8 +632,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     }
     int id;
     bool sure = limit_groups<LPT, VPL, float>(a, lane, key, score, exact, error, lanes);
-    if (!HERE && biased)
-      sure &= pick_sorted<VPL>(a, lane, key, size, error, s_ids[HERE ? 0 : threadIdx.x / LPT], id);
+    if (!HERE && biased && __ballot(size < kSortedBelow) == ~0ull)   // in every token of the wave
+      sure &= pick_sorted<VPL>(a, lane, key, error, s_ids[HERE ? 0 : threadIdx.x / LPT], id);
     else
       sure &= pick<LPT, VPL, float>(a, lane, key, exact, error, id);
     if constexpr (HERE) {

@@ -522,7 +522,7 @@ EP_API int ep_route_topk_backward(ep_combine_t h, const ep_route_params* params,
              src_info may be NULL too); rows from m_total on are left as they are.
    grad_w    device, [R][tokens_per_rank][top_k] fp32, every value written.
    One launch, deterministic.  EP_ERR_INVALID_ARG where grad_rows overlaps grad_out, or
-   grad_w an input. */
+   grad_w any of the others. */
 EP_API int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* topk_ids,
                                const float* topk_w, int32_t tokens_per_rank,
                                const int32_t* offsets, const int32_t* src_info, int32_t m_total,

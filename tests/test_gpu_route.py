@@ -415,3 +415,36 @@ def test_a_single_pick_has_the_whole_weight_and_no_gradient(score, dtype, T):
     assert torch.all(w == 2.5)
     d = ctx.route_backward(l, ids, torch.randn(1, T, 1, device="cuda"), score=score, scale=2.5)
     assert torch.all(d == 0)
+
+
+def test_many_tokens_on_another_stream_and_in_a_graph():
+    """The form with a second launch for near ties, captured once and replayed on new logits
+    and biases, and two calls at once."""
+    T, E = 4500, 250
+    opts = dict(score="sigmoid", n_groups=10, topk_groups=4, group_score="top2")
+    ctx = _ctx(1, T, 6)
+    l, bias = _logits(1, 1, T, E, "bf16").cuda(), (0.1 * torch.randn(E)).cuda()
+    l2 = _logits(2, 1, T, E, "bf16").cuda()
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ids1, w1 = ctx.route(l, bias=bias, stream=first, **opts)
+    ids2, w2 = ctx.route(l2, bias=bias, stream=second, **opts)
+    torch.cuda.synchronize()
+    for x, ids, w in ((l, ids1, w1), (l2, ids2, w2)):
+        want = ctx.route(x, bias=bias, **opts)
+        assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+        assert np.array_equal(ids.cpu().numpy()[0], P.route(
+            _numpy(x), 6, bias=bias.cpu().numpy(), **opts)[0])
+    ids, w = torch.empty_like(ids1), torch.empty_like(w1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ctx.route(l, bias=bias, topk_ids=ids, topk_w=w, **opts)
+        grad = ctx.route_backward(l, ids, w, score="sigmoid")
+    for seed in range(3):
+        l.copy_(_logits(10 + seed, 1, T, E, "bf16"))
+        bias.copy_(0.1 * torch.randn(E))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ctx.route(l, bias=bias, **opts)
+        assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+        assert torch.equal(grad, ctx.route_backward(l, ids, w, score="sigmoid"))
