@@ -272,9 +272,11 @@ __device__ __forceinline__ uint64_t row_destination(const GemmArgs& a, uint8_t* 
 
 // 16 bytes of a sent row, written through the XCD's L2 (sc1: agent scope), so that they
 // are visible to every XCD once the store is acknowledged (vmcnt), without the
-// write-back of the L2 that a release fence makes.
+// write-back of the L2 that a release fence makes.  (s_nop: the registers of a store of
+// more than 8 bytes may be written only a wait state later, which the compiler does not
+// see to for written-out stores.)
 __device__ __forceinline__ void store16_through(void* p, u32x4 v) {
-  asm volatile("global_store_dwordx4 %0, %1, off sc1" : : "v"(p), "v"(v) : "memory");
+  asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 1" : : "v"(p), "v"(v) : "memory");
 }
 
 // Tiles whose rows are sent but whose completion is still to be counted.

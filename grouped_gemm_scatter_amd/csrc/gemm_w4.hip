@@ -58,28 +58,17 @@ struct ThinTile {
   static constexpr int ROWS = 16, COLS = 64, SPLIT = 4, BLOCKS = 4, PER_CU = 4;
 };
 
-// 1/16 of the signed integer in the low half of byte B.
+// 1/16 of the signed integer in the low half of byte B.  (The mask makes the compiler select
+// the byte in the conversion; that is left to it, since only then it keeps the conversion's
+// result off registers that a matrix instruction still reads.)
 template <int B>
 __device__ __forceinline__ float off_i4(uint32_t v) {
-  float f;
-  if constexpr (B == 0)
-    asm("v_cvt_off_f32_i4_e32 %0, %1" : "=v"(f) : "v"(v));
-  else if constexpr (B == 1)
-    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1"
-        : "=v"(f) : "v"(v));
-  else if constexpr (B == 2)
-    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2"
-        : "=v"(f) : "v"(v));
-  else
-    asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
-        : "=v"(f) : "v"(v));
-  return f;
+  return __builtin_amdgcn_cvt_off_f32_i4((v >> (8 * B)) & 0xffu);
 }
 
 // The 8 codes of a packed dword as bf16 values: e2m1 values, or (code - 8) / 16.
 // Both are exact: 4 conversions for e2m1, for int4 a shift, 8 conversions (the
-// instruction takes a byte's low half; written out, because the compiler takes a shift
-// for every code instead of selecting the byte) and 4 roundings of exact numbers.
+// instruction takes a byte's low half) and 4 roundings of exact numbers.
 // (int4 as unsigned codes through the fp8 conversion, 7 instructions, with -8 sum x
 // from one more MFMA for each X fragment: the same time within 2%, and inexact zeros.)
 template <int CODES>
@@ -95,6 +84,7 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t v) {
     // the bytes
     const float l0 = off_i4<0>(v), l1 = off_i4<1>(v), l2 = off_i4<2>(v), l3 = off_i4<3>(v);
     v >>= 4;
+    asm("" : "+v"(v));               // one shift for all, not one for each byte
     const float h0 = off_i4<0>(v), h1 = off_i4<1>(v), h2 = off_i4<2>(v), h3 = off_i4<3>(v);
     return bf16x8{(__bf16)l0, (__bf16)l1, (__bf16)l2, (__bf16)l3,
                   (__bf16)h0, (__bf16)h1, (__bf16)h2, (__bf16)h3};
