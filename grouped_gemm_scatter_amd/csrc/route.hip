@@ -362,7 +362,12 @@ __device__ __forceinline__ bool limit_groups(const RouteArgs& a, int lane, T (&k
       }
     }
     T value = v1;
-    if (top2 && v2 > none) value += v2;
+    if (top2 && v2 > none) {
+      value += v2;
+      // a binary32 sum past the range is not that of a group without experts: kept finite, it
+      // lies within the error of the others past the range, which are told apart in binary64
+      if (!exact) value = larger(value, (T)-FLT_MAX);
+    }
     const int step = lanes > 0 ? lanes : 1, g = lane / step;
     int above = 0;                             // groups that come before this one
     for (int o = 0; o < a.n_groups; ++o) {

@@ -448,3 +448,29 @@ def test_many_tokens_on_another_stream_and_in_a_graph():
         want = ctx.route(l, bias=bias, **opts)
         assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
         assert torch.equal(grad, ctx.route_backward(l, ids, w, score="sigmoid"))
+
+
+@pytest.mark.parametrize("T", [7, 4101])
+@pytest.mark.parametrize("E,n_groups", [(8, 2), (12, 2), (64, 4)])
+def test_group_sums_past_the_range_of_binary32(E, n_groups, T):
+    """Finite biases whose sums of two overflow binary32, either way: such a group has experts
+    to pick, unlike one whose logits are all missing, and its sum is compared in binary64."""
+    per = E // n_groups
+    ctx = _ctx(1, T, 2)
+    l = _logits(E, 1, T, E, "f32")
+    missing = l.clone()
+    missing[..., :per] = -float("inf")
+    low = torch.full((E,), -3e38)
+    order = low.clone()
+    order[per:2 * per] = -2e38                     # the second group's sum is the larger one
+    tied = order.clone()
+    tied[:per] = -2e38
+    far = torch.full((E,), torch.finfo(torch.float32).min)
+    for x, bias in ((missing, low), (l, low), (l, order), (l, tied), (missing, tied),
+                    (missing, far), (l, far), (l, -order), (missing, -low)):
+        for score in ("sigmoid", "softmax"):
+            opts = dict(score=score, n_groups=n_groups, topk_groups=1, group_score="top2")
+            ids, w = ctx.route(x.cuda(), bias=bias.cuda(), **opts)
+            want_ids, want_w = P.route(_numpy(x), 2, bias=bias.numpy(), **opts)
+            assert np.array_equal(ids.cpu().numpy()[0], want_ids)
+            assert np.all(np.abs(_numpy(w) - want_w) <= _weight_bound(_numpy(x), E) * want_w)
