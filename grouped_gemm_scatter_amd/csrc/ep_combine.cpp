@@ -660,11 +660,20 @@ int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* top
   const uint64_t tokens = uint64_t(h->p.n_ranks) * tokens_per_rank;
   const uint64_t go_bytes = tokens * h->p.hidden_n * 2, w_bytes = tokens * h->p.top_k * 4;
   const uint64_t rows_bytes = grad_rows ? uint64_t(m_total) * h->p.hidden_n * 2 : 0;
-  if (overlap(grad_out, go_bytes, grad_rows, rows_bytes) ||
-      overlap(grad_w, w_bytes, grad_rows, rows_bytes) ||
-      overlap(grad_out, go_bytes, grad_w, w_bytes) || overlap(topk_ids, w_bytes, grad_w, w_bytes) ||
-      overlap(topk_w, w_bytes, grad_w, w_bytes))
+  if (overlap(grad_w, w_bytes, grad_rows, rows_bytes)) return EP_ERR_INVALID_ARG;
+  // every other workgroup still reads these while rows and weights' gradients are stored
+  auto meets_output = [&](const void* p, uint64_t n) {
+    return overlap(p, n, grad_w, w_bytes) || overlap(p, n, grad_rows, rows_bytes);
+  };
+  if (meets_output(grad_out, go_bytes) || meets_output(topk_ids, w_bytes) ||
+      meets_output(topk_w, w_bytes))
     return EP_ERR_INVALID_ARG;
+  const uint64_t runs = uint64_t(h->p.n_experts_per_device) * h->p.n_ranks + 1;
+  if (grad_rows && (meets_output(offsets, runs * 4) || meets_output(src_info, uint64_t(m_total) * 8)))
+    return EP_ERR_INVALID_ARG;
+  const uint64_t slots = uint64_t(tokens_per_rank) * h->p.top_k * h->p.msg_bytes;
+  for (int i = 0; i < h->p.n_ranks; ++i)
+    if (meets_output(h->b.recv_buf[i], slots)) return EP_ERR_INVALID_ARG;
   ep::CombineBackwardArgs a{};
   a.grad_out = static_cast<const uint8_t*>(grad_out);
   a.topk_ids = topk_ids;

@@ -521,8 +521,10 @@ EP_API int ep_route_topk_backward(ep_combine_t h, const ep_route_params* params,
    grad_rows device, [m_total][N] bf16, 16-byte aligned, or NULL (then offsets and
              src_info may be NULL too); rows from m_total on are left as they are.
    grad_w    device, [R][tokens_per_rank][top_k] fp32, every value written.
-   One launch, deterministic.  EP_ERR_INVALID_ARG where grad_rows overlaps grad_out, or
-   grad_w any of the others. */
+   One launch, deterministic.  EP_ERR_INVALID_ARG where grad_rows and grad_w overlap
+   each other, or one of them what the call reads: grad_out, topk_ids, topk_w, with
+   grad_rows offsets and src_info, the slots of tokens_per_rank tokens in a receive
+   buffer. */
 EP_API int ep_combine_backward(ep_combine_t h, const void* grad_out, const int32_t* topk_ids,
                                const float* topk_w, int32_t tokens_per_rank,
                                const int32_t* offsets, const int32_t* src_info, int32_t m_total,

@@ -273,3 +273,52 @@ def test_strides_types_and_overlaps_are_refused():
         with pytest.raises(EpError) as e:
             ctx.combine_backward(*args, **kw)
         assert e.value.code == B.EP_ERR_INVALID_ARG
+
+
+def test_outputs_over_anything_that_is_read_are_refused():
+    """grad_rows and grad_w over each input and over the slots of a receive buffer, which
+    workgroups read while others store; memory next to them is accepted."""
+    cfg = TINY.replace(n_ranks=2, n_experts_global=16, n_experts_local=4, tokens_per_rank=50,
+                       top_k=5, n=384, seed=8)
+    ids, _ = make_routing(cfg)
+    ctx, args, want = _case(cfg, ids)
+    go, d_ids, tw, off, src, m = args
+    N, slots = cfg.n, cfg.tokens_per_rank * cfg.top_k
+    row = 2 * N
+    # every tensor in one allocation, m rows of room behind its first byte
+    for name in range(5):
+        room = torch.zeros(max(args[name].numel() * 4, 4 * tw.numel()) + (m + 1) * row,
+                           dtype=torch.uint8, device="cuda")
+        t = args[name]
+        moved = room[: t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        moved.copy_(t)
+        call = args[:name] + (moved,) + args[name + 1:]
+        rows = room[: m * row].view(torch.bfloat16).view(m, N)
+        weights = room[: 4 * tw.numel()].view(torch.float32).view(tw.shape)
+        for kw in (dict(grad_rows=rows), dict(grad_w=weights)):
+            with pytest.raises(EpError) as e:
+                ctx.combine_backward(*call, **kw)
+            assert e.value.code == B.EP_ERR_INVALID_ARG
+        if name >= 3:                 # not read without rows
+            gw, _ = ctx.combine_backward(*call, rows=False, grad_w=weights)
+            err = np.abs(gw.cpu().double().numpy() - want[0])
+            assert np.all(err <= 2 * N * 2.0 ** -24 * want[2])
+    for recv in ctx.recv:
+        assert recv.numel() == slots * row and m <= slots
+        for kw in (dict(grad_rows=recv[recv.numel() - m * row:].view(torch.bfloat16).view(m, N)),
+                   dict(grad_w=recv[recv.numel() - 4 * tw.numel():].view(torch.float32).view(tw.shape))):
+            with pytest.raises(EpError) as e:
+                ctx.combine_backward(*args, **kw)
+            assert e.value.code == B.EP_ERR_INVALID_ARG
+    # slots of tokens that the call leaves out are not read
+    T = cfg.tokens_per_rank - 1
+    less = d_ids[:, :T].contiguous()
+    off, src = ctx.group(less)
+    free = ctx.recv[1][T * cfg.top_k * row:].view(torch.float32)
+    n = cfg.n_ranks * T * cfg.top_k
+    assert free.numel() >= n
+    gw, gr = ctx.combine_backward(go[:, :T].contiguous(), less, tw[:, :T].contiguous(), off, src,
+                                  int(off[-1]), grad_w=free[:n].view(cfg.n_ranks, T, cfg.top_k))
+    err = np.abs(gw.cpu().double().numpy() - want[0][:, :T])
+    assert np.all(err <= 2 * N * 2.0 ** -24 * want[2][:, :T])
+    assert ctx.query_error() == 0
