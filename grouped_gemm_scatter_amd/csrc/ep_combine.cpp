@@ -617,6 +617,10 @@ int ep_route_topk(ep_combine_t h, const ep_route_params* params, const void* log
   if (overlap(logits, in, topk_ids, out) || overlap(logits, in, topk_w, out) ||
       overlap(topk_ids, out, topk_w, out))
     return EP_ERR_INVALID_ARG;
+  // every token reads the bias, and a second launch reads it again
+  const uint64_t bias_bytes = bias ? uint64_t(a.n_experts) * 4 : 0;
+  if (overlap(bias, bias_bytes, topk_ids, out) || overlap(bias, bias_bytes, topk_w, out))
+    return EP_ERR_INVALID_ARG;
   a.bias = bias;
   a.topk_ids = topk_ids;
   a.topk_w = topk_w;

@@ -476,7 +476,7 @@ typedef struct ep_route_params {
    second picks the tokens again that the first left marked in topk_ids);
    deterministic.  Uses the handle's n_ranks and top_k and touches none of its
    buffers.  EP_ERR_INVALID_ARG for a bad size, flag or pointer, outputs that overlap
-   each other or the logits, or when the handle's device is not the current one;
+   each other, the logits or the bias, or when the handle's device is not the current one;
    EP_ERR_UNSUPPORTED for more experts or groups than the limits. */
 EP_API int ep_route_topk(ep_combine_t h, const ep_route_params* params, const void* logits,
                          const float* bias, int32_t tokens_per_rank, int32_t* topk_ids,

@@ -474,3 +474,18 @@ def test_group_sums_past_the_range_of_binary32(E, n_groups, T):
             want_ids, want_w = P.route(_numpy(x), 2, bias=bias.numpy(), **opts)
             assert np.array_equal(ids.cpu().numpy()[0], want_ids)
             assert np.all(np.abs(_numpy(w) - want_w) <= _weight_bound(_numpy(x), E) * want_w)
+
+
+def test_outputs_over_the_bias_are_refused():
+    ctx = _ctx(1, 8, 4)
+    l = _logits(5, 1, 8, 32, "f32").cuda()
+    room = torch.zeros(64, device="cuda")          # 32 of bias, then 32 of output
+    for at in (0, 8, 31):
+        out = room[at: at + 32].view(1, 8, 4)
+        for kw in (dict(topk_w=out), dict(topk_ids=out.view(torch.int32))):
+            with pytest.raises(EpError) as e:
+                ctx.route(l, bias=room[:32], **kw)
+            assert e.value.code == B.EP_ERR_INVALID_ARG
+    want_ids, want_w = ctx.route(l, bias=room[:32].clone())
+    ids, w = ctx.route(l, bias=room[:32], topk_w=room[32:].view(1, 8, 4))
+    assert torch.equal(ids, want_ids) and torch.equal(w, want_w)
