@@ -600,6 +600,18 @@ bool overlap(const void* p, uint64_t np, const void* q, uint64_t nq) {
   return np && nq && a < b + nq && b < a + np;
 }
 
+// Whether `out` meets what a product of 4-bit weights (rows x k an expert) reads.
+bool w4_output_overlaps(const ep_combine_handle* h, const ep_w4_format* f, const void* x,
+                        const void* w, const void* scales, uint64_t rows, uint64_t k,
+                        const int32_t* offsets, int32_t m_total, const void* out,
+                        uint64_t out_bytes) {
+  const uint64_t El = h->p.n_experts_per_device;
+  return overlap(x, uint64_t(m_total) * k * 2, out, out_bytes) ||
+         overlap(w, El * rows * k / 2, out, out_bytes) ||
+         overlap(scales, El * rows * (k / f->group) * 2, out, out_bytes) ||
+         overlap(offsets, (El * h->p.n_ranks + 1) * 4, out, out_bytes);
+}
+
 }  // namespace
 
 extern "C" {
@@ -736,7 +748,8 @@ int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format, const 
   if (h->p.dtype != EP_DTYPE_BF16) return EP_ERR_UNSUPPORTED;
   const int hidden = h->p.hidden_n, inter = h->p.hidden_k;
   if (inter % 128) return EP_ERR_UNSUPPORTED;
-  if (overlap(x1, uint64_t(m_total) * hidden * 2, h_out, uint64_t(m_total) * inter * 2))
+  if (w4_output_overlaps(h, format, x1, w1, w1_scale, 2 * uint64_t(inter), hidden, offsets,
+                         m_total, h_out, uint64_t(m_total) * inter * 2))
     return EP_ERR_INVALID_ARG;
   if (!on_device(h)) return EP_ERR_INVALID_ARG;
 
@@ -771,8 +784,9 @@ int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format, const
   if (h->p.dtype != EP_DTYPE_BF16 || h->p.hidden_k % 128 || h->p.send_waves ||
       (h->p.flags & (EP_FLAG_EPILOGUE_ONLY | EP_FLAG_TRACE | EP_FLAG_SEND_TILE)))
     return EP_ERR_UNSUPPORTED;
-  if (!sink_on && overlap(x, uint64_t(m_total) * h->p.hidden_k * 2, c_local,
-                          uint64_t(m_total) * h->p.hidden_n * 2))
+  if (!sink_on &&
+      w4_output_overlaps(h, format, x, w, w_scale, h->p.hidden_n, h->p.hidden_k, offsets,
+                         m_total, c_local, uint64_t(m_total) * h->p.hidden_n * 2))
     return EP_ERR_INVALID_ARG;
   if (!on_device(h)) return EP_ERR_INVALID_ARG;
 

@@ -563,7 +563,7 @@ EP_API int ep_pack_weights_w4(ep_combine_t h, const ep_w4_format* format, const 
    streaming the weights is all of the time.  h_out = bf16( silu(g) * u ), g and u
    summed in fp32 from exact code values, one scale per group (fp32), over k.
    x1, offsets, m_total, h_out as there (any number of rows is right; many rows per
-   expert are faster in bf16 weights), but h_out overlaps x1 nowhere
+   expert are faster in bf16 weights), but h_out overlaps no input
    (EP_ERR_INVALID_ARG); w1 and w1_scale as packed from [E_l][2I][hidden] codes.  An
    infinity or a NaN in a row of x1 acts as in a plain product, in that row alone.
    bf16 handles only (EP_ERR_UNSUPPORTED), I a multiple of 128. */
@@ -576,7 +576,8 @@ EP_API int ep_grouped_gemm_swiglu_w4(ep_combine_t h, const ep_w4_format* format,
    gate, epoch and errors, w and w_scale as packed from [E_l][N][K] codes, K a
    multiple of 128 (EP_ERR_UNSUPPORTED).  bf16 handles without EP_FLAG_EPILOGUE_ONLY,
    EP_FLAG_TRACE, EP_FLAG_SEND_TILE or send waves (EP_ERR_UNSUPPORTED);
-   EP_FLAG_W_SLICE_MAJOR plays no part.  c_local overlaps x nowhere. */
+   EP_FLAG_W_SLICE_MAJOR plays no part.  c_local overlaps neither x, w,
+   w_scale nor offsets (EP_ERR_INVALID_ARG). */
 EP_API int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format, const void* x,
                                       const void* w, const void* w_scale,
                                       const int32_t* offsets, const int32_t* src_info,

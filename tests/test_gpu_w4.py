@@ -490,3 +490,46 @@ def test_down_projection_of_the_narrow_tile(name, fmt):
 @pytest.mark.parametrize("fmt", FORMATS, ids=lambda f: "-".join(map(str, f)))
 def test_up_projection_of_the_narrow_tile(fmt):
     test_up_projection(fmt, "edges", 1152, 256)
+
+
+def test_outputs_over_what_is_read_are_refused():
+    """The rows of both products over each input, in whole or by their last row."""
+    k, n, m = 128, 256, 8
+    ctx, _ = _ctx([4, 4], 1, m, k, n)
+    rng = np.random.default_rng(9)
+    packed = [ctx.pack_weights_w4(to_dev(c), s.cuda())
+              for c, s in (_weights(rng, 2, 2 * k, n, 32, "bf16"),
+                           _weights(rng, 2, n, k, 64, "f16"))]
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    src = torch.tensor([[i, 0] for i in range(m)], dtype=torch.int32, device="cuda")
+
+    def up(x, codes, scales, offsets, out):
+        B.ep_grouped_gemm_swiglu_w4(ctx.handle, packed[0].format, x, codes, scales, offsets, m, out)
+
+    def down(x, codes, scales, offsets, out):
+        B.ep_grouped_gemm_scatter_w4(ctx.handle, packed[1].format, x, codes, scales, offsets, src,
+                                     m, -1, out)
+
+    for call, w, width, out_width in ((up, packed[0], n, k), (down, packed[1], k, n)):
+        x = torch.randn(m, width, device="cuda").bfloat16()
+        inputs = (x, w.codes, w.scales, off)
+        want = torch.empty(m, out_width, dtype=torch.bfloat16, device="cuda")
+        call(*inputs, want)
+        row = 2 * out_width
+        for i, t in enumerate(inputs):
+            size = (t.numel() * t.element_size() + 15) // 16 * 16
+            # rows before the input, the input, rows behind it
+            room = torch.zeros(2 * m * row + size, dtype=torch.uint8, device="cuda")
+            moved = room[m * row:][: t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+            moved.copy_(t)
+            call_inputs = inputs[:i] + (moved,) + inputs[i + 1:]
+            for at in (16, m * row, m * row + (t.numel() * t.element_size() - 1) // 16 * 16):
+                out = room[at: at + m * row].view(torch.bfloat16)
+                with pytest.raises(EpError) as e:
+                    call(*call_inputs, out)
+                assert e.value.code == B.EP_ERR_INVALID_ARG
+            for at in (0, m * row + size):
+                out = room[at: at + m * row].view(torch.bfloat16).view(m, out_width)
+                call(*call_inputs, out)
+                assert torch.equal(out, want)
+    assert ctx.query_error() == 0
