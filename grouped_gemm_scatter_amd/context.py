@@ -279,15 +279,29 @@ class EpCombine:
         if have != want:
             raise ValueError(f"packed weights of (experts, rows, k) {want} expected, got {have}")
 
+    def _packed_w4(self, w: PackedW4, rows: int, k: int):
+        """Addresses of the codes and scales of packed weights; raises unless they are what
+        their format says, on the handle's device."""
+        self._need_w4(w, rows, k)
+        n = self.n_experts_per_device * rows
+        scale_type = torch.float16 if w.format.scales == B.EP_W4_SCALE_F16 else torch.bfloat16
+        scale_elems = n * (k // max(w.format.group, 1))
+        if w.scales.dtype != scale_type:
+            raise ValueError(f"scales must be {scale_type}, got {w.scales.dtype}")
+        if w.scales.numel() < scale_elems:
+            raise ValueError(f"scales: {w.scales.numel()} elements, at least {scale_elems} needed")
+        return (self._flat(w.codes, "codes", n * k // 2, torch.uint8),
+                self._flat(w.scales, "scales", scale_elems, scale_type))
+
     def up_swiglu_w4(self, x1, w1: PackedW4, offsets, m_total, h_out, *, stream=None):
         """up_swiglu on 4-bit weights packed from [E_l][2*hidden_k][hidden_n] codes."""
         hid, inter = self.hidden_n, self.hidden_k
         x1 = self._flat(x1, "x1", m_total * hid, torch.bfloat16)
-        self._need_w4(w1, 2 * inter, hid)
+        codes, scales = self._packed_w4(w1, 2 * inter, hid)
         offsets = self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1,
                              torch.int32)
         h_out = self._flat(h_out, "h_out", m_total * inter, torch.bfloat16)
-        return B.ep_grouped_gemm_swiglu_w4(self.handle, w1.format, x1, w1.codes, w1.scales, offsets,
+        return B.ep_grouped_gemm_swiglu_w4(self.handle, w1.format, x1, codes, scales, offsets,
                                            m_total, h_out, stream)
 
     def gemm_scatter_w4(self, x, w: PackedW4, offsets, src_info, m_total, *, p3_control: int = 0,
@@ -295,13 +309,13 @@ class EpCombine:
         """gemm_scatter on 4-bit weights packed from [E_l][hidden_n][hidden_k] codes."""
         K, N = self.hidden_k, self.hidden_n
         x = self._flat(x, "x", m_total * K, torch.bfloat16)
-        self._need_w4(w, N, K)
+        codes, scales = self._packed_w4(w, N, K)
         offsets = self._flat(offsets, "offsets", self.n_experts_per_device * self.n_ranks + 1,
                              torch.int32)
         src_info = self._flat(src_info, "src_info", 2 * m_total, torch.int32)
         if p3_control < 0:
             c_local = self._flat(c_local, "c_local", m_total * N, torch.bfloat16)
-        return B.ep_grouped_gemm_scatter_w4(self.handle, w.format, x, w.codes, w.scales, offsets,
+        return B.ep_grouped_gemm_scatter_w4(self.handle, w.format, x, codes, scales, offsets,
                                             src_info, m_total, p3_control, c_local,
                                             self._epoch(epoch), stream)
 

@@ -69,3 +69,25 @@ def test_packed_weights_of_another_shape():
         ctx._need_w4(w, 16, 128)
     with pytest.raises(ValueError, match="pack_weights_w4"):
         ctx._need_w4(torch.zeros(4), 16, 128)
+
+
+def test_packed_weights_that_are_not_what_their_format_says():
+    """A stack put together by hand: too few codes or scales, scales of the other type, or on
+    another device, before anything is launched."""
+    ctx = EpCombine.__new__(EpCombine)       # no device: the checks come before it is used
+    ctx._device_index = 0
+    ctx.n_experts_per_device, ctx.n_ranks = 2, 1
+    ctx.hidden_n, ctx.hidden_k = 128, 128
+    fmt = B.make_w4_format(codes=0, group=32, scale_dtype=torch.bfloat16)
+    calls = ((256, lambda w: ctx.up_swiglu_w4(4096, w, 4096, 1, 4096)),
+             (128, lambda w: ctx.gemm_scatter_w4(4096, w, 4096, 4096, 1, epoch=1)))
+    for rows, call in calls:
+        codes = torch.zeros(2, rows, 64, dtype=torch.uint8)
+        scales = torch.zeros(2, rows, 4, dtype=torch.bfloat16)
+        for c, s, message in ((codes[:, :, :63], scales, "codes: .* at least"),
+                              (codes, scales, "codes must be on the handle's device"),
+                              (codes.char(), scales, "codes must be torch.uint8"),
+                              (codes, scales.half(), "scales must be torch.bfloat16"),
+                              (codes, scales[:, :, :2], "scales: .* at least")):
+            with pytest.raises(ValueError, match=message):
+                call(PackedW4(c, s, rows, 128, fmt))
