@@ -74,6 +74,11 @@ constexpr int kDecodeTile = ep::kTileDecode64x128;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Bytes of `experts` down-projections in the handle's dtype.
+uint64_t weight_bytes(const ep_combine_params& p, int experts) {
+  return uint64_t(experts) * p.hidden_n * p.hidden_k * (p.dtype == EP_DTYPE_BF16 ? 2 : 1);
+}
+
 int validate_params(const ep_combine_params* p) {
   if (!p) return EP_ERR_INVALID_ARG;
   if (p->n_ranks < 1 || p->n_ranks > EP_MAX_RANKS) return EP_ERR_INVALID_ARG;
@@ -107,11 +112,15 @@ int validate_params(const ep_combine_params* p) {
     if (p->flags & (EP_FLAG_EPILOGUE_ONLY | EP_FLAG_TRACE)) return EP_ERR_UNSUPPORTED;
   }
   if (p->flag_spin_limit < 0) return EP_ERR_INVALID_ARG;
-  // 32-bit element offsets inside the kernels
-  const uint64_t wbytes = uint64_t(p->n_experts_per_device) * p->hidden_n * p->hidden_k *
-                          (p->dtype == EP_DTYPE_BF16 ? 2 : 1);
-  if (wbytes >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
+  // 32-bit offsets inside one expert's weights
+  if (weight_bytes(*p, 1) >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
   return EP_OK;
+}
+
+// The products of weights in the handle's dtype (not those of 4-bit weights) take a stack
+// below 4 GiB.
+bool stack_ok(const ep_combine_handle* h) {
+  return weight_bytes(h->p, h->p.n_experts_per_device) < (uint64_t(1) << 32);
 }
 
 ep::SinkState sink_state(const ep_combine_handle* h, uint64_t epoch) {
@@ -270,6 +279,7 @@ int gemm_scatter(ep_combine_t h, const void* x, const void* w, const float* x_sc
   if (sink_on && !epoch_ok(h, epoch)) return EP_ERR_INVALID_ARG;
   const bool fp8 = h->p.dtype == EP_DTYPE_FP8_E4M3_B128;
   if (fp8 && ((m_total > 0 && !x_scale) || !w_scale)) return EP_ERR_INVALID_ARG;
+  if (!stack_ok(h)) return EP_ERR_UNSUPPORTED;
   const int elt = fp8 ? 1 : 2;
   if (uint64_t(m_total) * h->p.hidden_k * elt >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
   if ((x && !aligned16(x)) || !aligned16(w)) return EP_ERR_INVALID_ARG;
@@ -424,9 +434,8 @@ int ep_dispatch_rows(ep_combine_t h, const void* tokens_x, int32_t tokens_per_ra
 
 int ep_pack_weights(ep_combine_t h, const void* w, void* w_out, void* stream) {
   if (!h || !w || !w_out || !aligned16(w) || !aligned16(w_out)) return EP_ERR_INVALID_ARG;
-  if (h->p.dtype != EP_DTYPE_BF16) return EP_ERR_UNSUPPORTED;
-  const uint64_t bytes =
-      uint64_t(h->p.n_experts_per_device) * h->p.hidden_n * h->p.hidden_k * 2;
+  if (h->p.dtype != EP_DTYPE_BF16 || !stack_ok(h)) return EP_ERR_UNSUPPORTED;
+  const uint64_t bytes = weight_bytes(h->p, h->p.n_experts_per_device);
   const uintptr_t a = reinterpret_cast<uintptr_t>(w), b = reinterpret_cast<uintptr_t>(w_out);
   if (a < b + bytes && b < a + bytes) return EP_ERR_INVALID_ARG;
   const hipError_t err = ep::launch_pack_slice_major(
@@ -444,7 +453,7 @@ int ep_grouped_gemm_swiglu(ep_combine_t h, const void* x1, const void* w1,
   if (h->p.dtype != EP_DTYPE_BF16) return EP_ERR_UNSUPPORTED;
   const int hidden = h->p.hidden_n, inter = h->p.hidden_k;
   // 2I GEMM columns in whole 256-column tiles; 32-bit offsets inside X1 and W1_e
-  if (inter % 128) return EP_ERR_UNSUPPORTED;
+  if (inter % 128 || !stack_ok(h)) return EP_ERR_UNSUPPORTED;
   if (uint64_t(m_total) * hidden * 2 >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
   if (uint64_t(2) * inter * hidden * 2 >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
 
@@ -480,6 +489,7 @@ int ep_grouped_gemm_swiglu_fp8(ep_combine_t h, const void* x1, const float* x1_s
   const int hidden = h->p.hidden_n, inter = h->p.hidden_k;
   // the handle's fp8 rules give hidden and I multiples of 128: 2I GEMM columns in
   // whole 256-column tiles; 32-bit offsets inside X1 and W1_e
+  if (!stack_ok(h)) return EP_ERR_UNSUPPORTED;
   if (uint64_t(m_total) * hidden >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
   if (uint64_t(2) * inter * hidden >= (uint64_t(1) << 32)) return EP_ERR_UNSUPPORTED;
 

@@ -190,8 +190,13 @@ typedef struct ep_combine_handle* ep_combine_t;
    the current device.  No device work and no device memory: the buffers are
    the caller's and must outlive the handle.  Returns EP_OK and *out, or a
    negative code (EP_ERR_INVALID_ARG for a bad size, null or misaligned
-   buffer; EP_ERR_UNSUPPORTED for p2p_world_size != n_ranks or a shape the
-   kernels do not tile; EP_ERR_HIP when the device cannot be queried). */
+   buffer; EP_ERR_UNSUPPORTED for p2p_world_size != n_ranks, a shape the
+   kernels do not tile or N*K weights of one expert that are 4 GiB or more in
+   the handle's dtype; EP_ERR_HIP when the device cannot be queried).  Where the
+   E_l*N*K weights of all experts are 4 GiB or more, the calls that take them in
+   the handle's dtype (ep_grouped_gemm_scatter and its variants, ep_pack_weights,
+   ep_grouped_gemm_swiglu and its fp8 form) return EP_ERR_UNSUPPORTED; 4-bit
+   weights have no such limit. */
 EP_API int ep_combine_init(const ep_combine_params* params, const ep_combine_buffers* bufs,
                     ep_combine_t* out);
 
@@ -554,7 +559,7 @@ typedef struct ep_w4_format {
    codes_out, scales_out  device, the same sizes, written; 16-byte aligned like the
               inputs, overlapping none of them (EP_ERR_INVALID_ARG otherwise).
    rows a multiple of 16 and k of 128 (EP_ERR_UNSUPPORTED).  bf16 handles only
-   (EP_ERR_UNSUPPORTED for fp8): they give E_l. */
+   (EP_ERR_UNSUPPORTED for fp8): they give E_l, and the stack may be of any size. */
 EP_API int ep_pack_weights_w4(ep_combine_t h, const ep_w4_format* format, const void* codes,
                               const void* scales, int32_t rows, int32_t k, void* codes_out,
                               void* scales_out, void* stream);

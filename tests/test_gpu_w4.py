@@ -533,3 +533,60 @@ def test_outputs_over_what_is_read_are_refused():
                 call(*call_inputs, out)
                 assert torch.equal(out, want)
     assert ctx.query_error() == 0
+
+
+@pytest.mark.parametrize("sizes", [
+    {0: 3, 146: 1, 255: 2}, {e: 40 for e in range(3, 256, 23)},
+    {e: 11 * e % 9 for e in range(256)}], ids=["few_rows", "few_experts", "every_expert"])
+def test_a_whole_layer_of_256_experts(sizes):
+    """Both products of a stack whose 2-byte weights would be 7.5 GB, in each tile; products
+    of such weights are refused."""
+    k, n, E, R = 2048, 7168, 256, 2
+    rng = np.random.default_rng(len(sizes))
+    off, src, T = _layout([sizes.get(e, 0) for e in range(E)], R, rng)
+    M = int(off[-1])
+    ctx, _ = _ctx([0] * E, R, T, k, n)
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    stacks = []
+    for rows, kk, group, st in ((2 * k, n, 128, "bf16"), (n, k, 32, "f16")):
+        codes = torch.randint(0, 256, (E, rows, kk // 2), dtype=torch.uint8, device="cuda",
+                              generator=gen)
+        scales = ((0.5 + torch.rand(E, rows, kk // group, device="cuda", generator=gen)) /
+                  (5 * kk ** 0.5)).to(SCALES[st])
+        stacks.append((codes, scales, ctx.pack_weights_w4(codes, scales), group))
+    x = torch.randn(M, n, device="cuda", generator=gen).bfloat16()
+    h = torch.empty(M, k, dtype=torch.bfloat16, device="cuda")
+    c = torch.empty(M, n, dtype=torch.bfloat16, device="cuda")
+    d_off, d_src = to_dev(off), to_dev(src)
+    ctx.up_swiglu_w4(x, stacks[0][2], d_off, M, h)
+    ctx.gemm_scatter_w4(h, stacks[1][2], d_off, d_src, M, p3_control=-1, c_local=c)
+    ctx.next_epoch()
+    ctx.gemm_scatter_w4(h, stacks[1][2], d_off, d_src, M)
+    torch.cuda.synchronize()
+    assert ctx.query_error() == 0 and torch.all(ctx.flags == 1)
+    rank = (np.searchsorted(off, np.arange(M), side="right") - 1) % R
+    for m in range(M):
+        slot = ctx.recv[rank[m]].view(-1, 2 * n)[int(src[m, 0]) * 2 + int(src[m, 1])]
+        assert torch.equal(slot.view(torch.bfloat16), c[m])
+    busy = [e for e in range(E) if sizes.get(e, 0)]
+    for e in sorted({busy[0], busy[len(busy) // 2], busy[-2], busy[-1]}):
+        at = slice(int(off[e * R]), int(off[(e + 1) * R]))
+        for (codes, scales, _, group), inp, got in ((stacks[0], x, h), (stacks[1], h, c)):
+            w = P.weights_w4(codes[e].cpu().numpy(), scales[e].double().cpu().numpy(), "int4")
+            y, a = P.grouped_product(O.bf16_to_f64(bits(inp[at])), w[None], [0, at.stop - at.start])
+            b = _sum_bound(a, w.shape[1], group)
+            if got is h:
+                (g, u), (bg, bu) = (y[:, :k], y[:, k:]), (b[:, :k], b[:, k:])
+                silu = g / (1 + np.exp(-g))
+                y = silu * u
+                b = 1.1 * bg * (np.abs(u) + bu) + np.abs(silu) * bu + 2.0 ** -20 * np.abs(y)
+            tol = b + 2.0 ** -8 * np.abs(y) + 1e-38
+            assert np.all(np.abs(O.bf16_to_f64(bits(got[at])) - y) <= tol)
+    w = stacks[0][0].data_ptr()
+    for call in (lambda: B.ep_grouped_gemm_scatter(ctx.handle, h, w, None, None, d_off, d_src, M,
+                                                   0, None, 2),
+                 lambda: B.ep_grouped_gemm_swiglu(ctx.handle, x, w, d_off, M, h),
+                 lambda: B.ep_pack_weights(ctx.handle, w, stacks[1][0].data_ptr())):
+        with pytest.raises(EpError) as e:
+            call()
+        assert e.value.code == B.EP_ERR_UNSUPPORTED

@@ -91,3 +91,29 @@ def test_packed_weights_that_are_not_what_their_format_says():
                               (codes, scales[:, :, :2], "scales: .* at least")):
             with pytest.raises(ValueError, match=message):
                 call(PackedW4(c, s, rows, 128, fmt))
+
+
+def _init(lib, **over):
+    kw = dict(n_ranks=1, my_rank=0, top_k=2, max_tokens_per_rank=8, n_experts_per_device=1,
+              hidden_k=64, hidden_n=128)
+    kw.update(over)
+    b = B.EpCombineBuffers()
+    b.recv_buf[0] = 4096
+    b.recv_count = b.rank_counter = b.tile_counter = b.error_word = 1 << 20
+    h = ctypes.c_void_p()
+    rc = lib.ep_combine_init(ctypes.byref(B.make_params(msg_bytes=2 * kw["hidden_n"], **kw)),
+                             ctypes.byref(b), ctypes.byref(h))
+    lib.ep_combine_destroy(h)
+    return rc
+
+
+@pytest.mark.parametrize("over", [dict(n_experts_per_device=256, hidden_k=2048, hidden_n=4096),
+                                  dict(n_experts_per_device=256, hidden_k=2048, hidden_n=7168)])
+def test_handles_of_stacks_that_only_4_bits_hold(lib, over):
+    """4 GiB and more in 2-byte weights (without a GPU the call ends at the device's)."""
+    assert _init(lib, **over) in (B.EP_OK, B.EP_ERR_HIP)
+
+
+def test_one_expert_past_four_gib_is_refused(lib):
+    assert _init(lib, hidden_k=1 << 24) == B.EP_ERR_UNSUPPORTED
+    assert _init(lib, hidden_k=(1 << 24) - 64) in (B.EP_OK, B.EP_ERR_HIP)
