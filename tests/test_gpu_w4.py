@@ -590,3 +590,58 @@ def test_a_whole_layer_of_256_experts(sizes):
         with pytest.raises(EpError) as e:
             call()
         assert e.value.code == B.EP_ERR_UNSUPPORTED
+
+
+def test_on_another_stream_everything_is_written_there():
+    """A step on a stream whose earlier work it needs: the input arrives there, late, and what
+    the step writes held something else before."""
+    k, n, R = 256, 128, 2
+    rng = np.random.default_rng(14)
+    off, src, T = _layout([20, 0, 70, 1], R, rng)
+    M = int(off[-1])
+    ctx, _ = _ctx([20, 0, 70, 1], R, T, k, n)
+    c, s = _weights(rng, 4, n, k, 32, "bf16")
+    c1, s1 = _weights(rng, 4, 2 * k, n, 128, "f16")
+    w = ctx.pack_weights_w4(to_dev(c), s.cuda(), codes="e2m1")
+    w1 = ctx.pack_weights_w4(to_dev(c1), s1.cuda())
+    old, new = (torch.randn(M, n, device="cuda").bfloat16() for _ in range(2))
+    d_off, d_src = to_dev(off), to_dev(src)
+    h = torch.empty(M, k, dtype=torch.bfloat16, device="cuda")
+
+    def step(x, stream=None):
+        ctx.next_epoch(stream)
+        ctx.up_swiglu_w4(x, w1, d_off, M, h, stream=stream)
+        ctx.gemm_scatter_w4(h, w, d_off, d_src, M, stream=stream)
+
+    step(new)
+    torch.cuda.synchronize()
+    want, want_h, want_words = [r.clone() for r in ctx.recv], h.clone(), ctx.words.clone()
+    for r in ctx.recv:
+        r.fill_(SENTINEL)
+    h.fill_(7.0)
+    ctx.words.zero_()
+    x = old.clone()
+    late = torch.cuda.Stream()
+    late.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(late):
+        torch.cuda._sleep(20_000_000)
+        x.copy_(new)
+    step(x, late)
+    late.synchronize()
+    assert ctx.query_error() == 0
+    assert torch.equal(h, want_h)
+    assert all(torch.equal(a, b) for a, b in zip(ctx.recv, want))
+    want_words[-R:] = 2                              # the second step's flags
+    assert torch.equal(ctx.words, want_words)
+    assert torch.all(ctx.rank_counter == 0) and torch.all(ctx.tile_counter == 0)
+    # packed there as well, from codes that arrive late
+    codes, scales = torch.zeros_like(to_dev(c1)), torch.zeros_like(s1).cuda()
+    d_c1, d_s1 = to_dev(c1), s1.cuda()
+    late.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(late):
+        torch.cuda._sleep(20_000_000)
+        codes.copy_(d_c1)
+        scales.copy_(d_s1)
+    there = ctx.pack_weights_w4(codes, scales, stream=late)
+    late.synchronize()
+    assert torch.equal(there.codes, w1.codes) and torch.equal(there.scales, w1.scales)
