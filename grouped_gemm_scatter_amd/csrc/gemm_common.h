@@ -312,37 +312,27 @@ __device__ __forceinline__ int tiles_of(const PendingTiles& p, int e) {
 // expert's last tile marks the expert done.
 // THROUGH: the rows were stored with store16_through, which an acknowledged store
 // has already made visible to the whole device, so at agent scope there is nothing
-// left to write back and no fence.  A run of tiles of one expert is then counted by one
-// RMW: short launches end everywhere at about the same time, and a large expert's
-// hundreds of tiles met at its counter one by one (3416 skewed rows: 94 us with an RMW
-// a tile, 90 with one a run; in the wide fp8 tile, whose registers are full, the same cost
-// 4%).
+// left to write back and no fence.  (One RMW for a run of tiles of one expert instead of one
+// a tile: 73.4 against 75.0 us for 3416 skewed rows of 4-bit products, but 82.5 against 80.1
+// for a decode step and 22.8 against 22.3 for a token; in the wide fp8 tile, whose registers
+// are full, 4% slower.)
 template <bool THROUGH = false>
 __device__ __forceinline__ void complete_pending(const GemmArgs& a, PendingTiles& p) {
   if (p.n == 0) return;
   if (a.sink_on && threadIdx.x == 0) {
     if (!THROUGH || a.s.system_scope) fence_release(a.s.system_scope);
     int old[kPendingMax];
-    int add[kPendingMax];          // tiles of a run, at its last; 0 at the others
-    int run = 0;
-#pragma unroll
-    for (int i = 0; i < kPendingMax; ++i) {
-      add[i] = i < p.n ? 1 : 0;
-      if constexpr (THROUGH) {
-        run += add[i];
-        add[i] = i + 1 < p.n && p.e[i + 1] == p.e[i] ? 0 : run;
-        if (add[i]) run = 0;
-      }
-      if (add[i])
-        old[i] = a.s.system_scope
-                     ? __hip_atomic_fetch_add(a.s.tile_counter + p.e[i], add[i], __ATOMIC_RELAXED,
-                                              __HIP_MEMORY_SCOPE_SYSTEM)
-                     : __hip_atomic_fetch_add(a.s.tile_counter + p.e[i], add[i], __ATOMIC_RELAXED,
-                                              __HIP_MEMORY_SCOPE_AGENT);
-    }
 #pragma unroll
     for (int i = 0; i < kPendingMax; ++i)
-      if (add[i] && old[i] == tiles_of(p, p.e[i]) - add[i])
+      if (i < p.n)
+        old[i] = a.s.system_scope
+                     ? __hip_atomic_fetch_add(a.s.tile_counter + p.e[i], 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_SYSTEM)
+                     : __hip_atomic_fetch_add(a.s.tile_counter + p.e[i], 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int i = 0; i < kPendingMax; ++i)
+      if (i < p.n && old[i] == tiles_of(p, p.e[i]) - 1)
         p.done[p.e[i] >> 5] |= 1u << (p.e[i] & 31);
   }
   p.n = 0;
