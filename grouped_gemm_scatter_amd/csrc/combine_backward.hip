@@ -12,9 +12,9 @@
 // rows, two up to 4096, where a lane's bisection takes seven for 128 rows.
 //
 // What it measured: 32768 tokens of 7168 values, one pick in eight local, 1.25 GB:
-// 266 us, 4.7 TB/s, 97% of the rate of a large copy (293 us with one wave a token and
+// 265 us, 4.7 TB/s, 80% of the rate of a plain copy (293 us with one wave a token and
 // bisection).  308 tokens of 4096 values, 12.4 MB: 9.7 us, of which three dependent reads (ids, run
-// bounds, rows' places) are most; a copy of the bytes would take 2.6.
+// bounds, rows' places) are most; a copy of the bytes would take 2.1.
 #include <algorithm>
 
 #include "ep_kernels.h"

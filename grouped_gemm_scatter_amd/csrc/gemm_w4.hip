@@ -22,13 +22,13 @@
 // columns, every wave a quarter of K, the quarters' sums joined through LDS.
 //
 // What bounds it.  32 experts of about 31 rows, 7168 -> 2 x 2048, int4, groups of 128:
-// 121 us for 503 MB, 4.2 TB/s, 86% of the rate of a large copy.  The loads by themselves
+// 122 us for 503 MB, 4.1 TB/s, 69% of the rate of a plain copy.  The loads by themselves
 // took 79 us and the arithmetic by itself 105: a SIMD's conversions (13 vector
 // instructions for 8 codes of a lane) and MFMAs (one for every 16 rows of them) add up,
-// whatever the number of waves.  The down-projection with groups of 32 (e2m1): 79 us for
+// whatever the number of waves.  The down-projection with groups of 32 (e2m1): 78 us for
 // 283 MB, of which the sink's publication at the end of the launch is 8.  A single token:
-// 31 us for 121 MB up, 24 for 61 MB down, bound by the memory's latency at either end of
-// a tile.  Few large groups (1650 rows over 16 experts, 1536 -> 4096): 57 us, bound by
+// 32 us for 121 MB up, 23 for 61 MB down, bound by the memory's latency at either end of
+// a tile.  Few large groups (1650 rows over 16 experts, 1536 -> 4096): 56 us, bound by
 // the arithmetic and by tiles that do not fill their last round.
 // Measured and left: four workgroups a CU of 48 x 128 tiles (129 us up), three a CU (the
 // registers spill), four steps of weights ahead (no faster up, 3% slower down), a raised

@@ -8,9 +8,14 @@
 // logits themselves.  Where a score is compared (a bias, a sum of two) it is defined in
 // binary64, but computed in binary32 first with a bound on the error: only a token in
 // which two choices next to each other, or the groups at the limit, lie within that
-// bound is chosen again in binary64, a few tokens of a thousand: in the same kernel
-// where tokens are few, in a second one where they are many, since the registers of
-// the binary64 path would leave the first kernel two waves a SIMD.
+// bound is chosen again in binary64: in the same kernel where tokens are few, in a second
+// one where they are many, since the registers of the binary64 path would leave the first
+// kernel two waves a SIMD.  That is a few tokens of a thousand where the biases are of the
+// scores' size.  It is every token where one finite bias is huge, since the bound grows with
+// the largest sum of the token, pickable or not (32768 tokens, one bias of -1e9: 125 us, of
+// -infinity 28), and many where groups are ranked by sums without a bias: then picks, though
+// by logits, must lie a score's bound apart as well (bf16 logits, of which many are equal:
+// 89 us, binary32 32).
 // A pick: the largest key of every lane, the largest of the token by cross-lane moves,
 // the lowest lane that has it from a ballot's lowest bit.  That is about 85 vector
 // instructions whatever LPT is, so four tokens share them where they fit; biased choices
@@ -18,7 +23,7 @@
 //
 // What it measured: 32768 tokens of 256 experts in 8 groups (sigmoid, bias, top-2 group sums,
 // fp32 logits) 22 us and 7 us for the second kernel, where a copy of the same bytes takes
-// 7.4: bound by vector instructions, 1030 a wave of four tokens (1770 and 31 us with
+// 6.0: bound by vector instructions, 1030 a wave of four tokens (1770 and 31 us with
 // pick() alone).  8192 tokens of 128 experts 6.2 us, one token 5.2 us, of which most is
 // the latency of a launch.
 //
@@ -672,7 +677,11 @@ __global__ __launch_bounds__(kRouteThreads) void pick_again_kernel(RouteArgs a) 
 }
 
 // What pick k adds at its expert, lane k of the token's LPT lanes with its logit l and
-// scaled gradient g; not for the plain softmax, whose gradient is dense.
+// scaled gradient g; not for the plain softmax, whose gradient is dense.  The reciprocals are
+// the hardware's, within a step (2^-23) of themselves where a division is within half
+// of one, and the exponentials are exp_near()'s: a share is off by a few steps either way, which
+// the difference g - sum g p multiplies in any form, and the kernel took 17 us instead of
+// 20 with them (32768 tokens of 256 experts).
 template <int LPT>
 __device__ __forceinline__ float pick_gradient(const RouteArgs& a, float l, float g, bool there) {
   float d;
@@ -688,8 +697,9 @@ __device__ __forceinline__ float pick_gradient(const RouteArgs& a, float l, floa
 
 // The gradient at the picks alone, four tokens a wave: their rows, which follow one
 // another, are filled with zeros, and once those stores are acknowledged the lanes that
-// hold picks store theirs.  At 32768 tokens of 256 experts it took 12.4 us, the kernel
-// below, in which every lane looks for its experts among the picks, 16.6.
+// hold picks store theirs.  At 32768 tokens of 256 experts it takes 12.1 us, the kernel
+// below, in which every lane looks for its experts among the picks, took 16.6.  A line that
+// holds a pick goes out twice, with a wait between: 48.7 MB written for a gradient of 33.6.
 __global__ __launch_bounds__(kRouteThreads) void route_backward_picks_kernel(RouteArgs a) {
   const int wl = threadIdx.x & 63, lane = wl & 15, row = wl >> 4;
   const int64_t wave = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);

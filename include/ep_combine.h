@@ -437,7 +437,9 @@ EP_API int ep_grouped_gemm_scatter_combine(ep_combine_t h, const void* x, const 
      scores    s = softmax of the present logits, or s_i = 1 / (1 + e^-l_i); 0
                for an expert that is not present
      choice    c_i = s_i + bias_i, or l_i itself without a bias; an expert whose
-               bias is NaN or -infinity is never picked
+               bias is NaN or -infinity is never picked (a huge finite bias,
+               of whichever expert, makes every token's choice take the binary64
+               path, four times as long for many tokens)
      groups    with n_groups > 1, expert i belongs to group i / (n_experts /
                n_groups); a group's value is the largest choice of its pickable
                experts (EP_GROUP_MAX), or the sum of the two largest s_i + bias_i
