@@ -16,8 +16,11 @@ from .binding import (EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3_B128, EP_ERR_BAD_GROUP,
                       EP_W4_SCALE_BF16, EP_W4_SCALE_F16, ep_combine_backward,
                       ep_grouped_gemm_scatter_w4, ep_grouped_gemm_swiglu_w4, ep_pack_weights_w4,
                       ep_route_topk, ep_route_topk_backward, make_route_params, make_w4_format,
-                      load_library, make_params)
-from .context import EpCombine, PackedW4
+                      load_library, make_params,
+                      EP_MOE_MAX_PICKS, EP_MOE_MAX_TOKENS, EP_ROWS_BF16, EP_ROWS_F16, EP_ROWS_F32,
+                      ep_moe_layer, ep_moe_layer_workspace, ep_rms_norm, ep_rms_norm_backward,
+                      ep_rms_norm_backward_workspace, make_norm_params)
+from .context import EpCombine, PackedW4, RmsNorm, RmsNormGrad
 
 __all__ = [
     "EP_DTYPE_BF16", "EP_DTYPE_FP8_E4M3_B128", "EP_ERR_BAD_GROUP", "EP_ERR_FLAG_TIMEOUT",
@@ -33,4 +36,7 @@ __all__ = [
     "EP_W4_SCALE_F16", "ep_combine_backward", "ep_grouped_gemm_scatter_w4",
     "ep_grouped_gemm_swiglu_w4", "ep_pack_weights_w4", "ep_route_topk", "ep_route_topk_backward",
     "make_route_params", "make_w4_format", "load_library", "make_params", "EpCombine", "PackedW4",
+    "EP_MOE_MAX_PICKS", "EP_MOE_MAX_TOKENS", "EP_ROWS_BF16", "EP_ROWS_F16", "EP_ROWS_F32",
+    "ep_moe_layer", "ep_moe_layer_workspace", "ep_rms_norm", "ep_rms_norm_backward",
+    "ep_rms_norm_backward_workspace", "make_norm_params", "RmsNorm", "RmsNormGrad",
 ]

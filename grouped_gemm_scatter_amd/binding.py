@@ -46,12 +46,19 @@ EP_W4_INT4 = 0
 EP_W4_E2M1 = 1
 EP_W4_SCALE_BF16 = 0
 EP_W4_SCALE_F16 = 1
+EP_ROWS_F32 = 0
+EP_ROWS_BF16 = 1
+EP_ROWS_F16 = 2
+EP_MOE_MAX_TOKENS = 64
+EP_MOE_MAX_PICKS = 1024
 
 EXPORTED = ("ep_combine_init", "ep_combine_destroy", "ep_gemm_tile", "ep_group_local_picks",
             "ep_dispatch_rows", "ep_pack_weights", "ep_advance_epoch",
             "ep_grouped_gemm_scatter", "ep_grouped_gemm_scatter_noalloc", "ep_grouped_gemm_swiglu",
             "ep_grouped_gemm_swiglu_fp8", "ep_grouped_gemm_swiglu_w4", "ep_grouped_gemm_scatter_w4",
             "ep_pack_weights_w4", "ep_route_topk", "ep_route_topk_backward", "ep_combine_backward",
+            "ep_rms_norm", "ep_rms_norm_backward", "ep_rms_norm_backward_workspace",
+            "ep_moe_layer", "ep_moe_layer_workspace",
             "ep_grouped_gemm_scatter_combine", "ep_signal_completion",
             "ep_combine_reduce", "ep_combine_query_error", "ep_combine_strerror",
             "ep_combine_version")
@@ -106,6 +113,15 @@ class EpW4Format(ctypes.Structure):
         ("codes", ctypes.c_int32),
         ("group", ctypes.c_int32),
         ("scales", ctypes.c_int32),
+    ]
+
+
+class EpNormParams(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -175,13 +191,23 @@ def load_library(path: str | None = None):
     lib.ep_grouped_gemm_swiglu_w4.restype = ctypes.c_int
     lib.ep_grouped_gemm_scatter_w4.argtypes = [vp, w4, vp, vp, vp, vp, vp, i32, i32, vp, u64, vp]
     lib.ep_grouped_gemm_scatter_w4.restype = ctypes.c_int
+    norm = ctypes.POINTER(EpNormParams)
+    lib.ep_rms_norm.argtypes = [vp, norm, vp, vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.ep_rms_norm.restype = ctypes.c_int
+    lib.ep_rms_norm_backward.argtypes = [vp, norm, vp, vp, vp, vp, i32, vp, vp, vp, vp, i64, vp]
+    lib.ep_rms_norm_backward.restype = ctypes.c_int
+    lib.ep_rms_norm_backward_workspace.argtypes = [vp, i32]
+    lib.ep_rms_norm_backward_workspace.restype = i64
+    lib.ep_moe_layer.argtypes = [vp, w4, w4, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i64, vp]
+    lib.ep_moe_layer.restype = ctypes.c_int
+    lib.ep_moe_layer_workspace.argtypes = [vp, i32]
+    lib.ep_moe_layer_workspace.restype = i64
     lib.ep_combine_query_error.argtypes = [vp, vp]
     lib.ep_combine_query_error.restype = ctypes.c_int
     lib.ep_combine_strerror.argtypes = [ctypes.c_int]
     lib.ep_combine_strerror.restype = ctypes.c_char_p
     lib.ep_combine_version.argtypes = []
     lib.ep_combine_version.restype = ctypes.c_int
-    del i64
     _lib = lib
     return lib
 
@@ -466,6 +492,77 @@ def ep_grouped_gemm_scatter_w4(h, fmt: EpW4Format, x, w, w_scale, offsets, src_i
         _ptr(src_info, torch.int32, "src_info", allow_none=True), int(m_total), int(p3_control),
         _ptr(c_local, torch.bfloat16, "c_local", allow_none=True), int(epoch), _stream(stream))
     return _check(rc, "ep_grouped_gemm_scatter_w4")
+
+
+_ROWS = {torch.float32: EP_ROWS_F32, torch.bfloat16: EP_ROWS_BF16, torch.float16: EP_ROWS_F16}
+
+
+def make_norm_params(*, dtype, residual_dtype=None, weight_dtype=None, eps=1e-6) -> EpNormParams:
+    kinds = [dtype, dtype if residual_dtype is None else residual_dtype,
+             dtype if weight_dtype is None else weight_dtype]
+    for t in kinds:
+        if t not in _ROWS:
+            raise ValueError(f"rows must be float32, bfloat16 or float16, not {t}")
+    for t, name in zip(kinds[1:], ("residual", "weight")):
+        if t not in (dtype, torch.float32):
+            raise ValueError(f"{name} must be {dtype} or float32, not {t}")
+    return EpNormParams(*(_ROWS[t] for t in kinds), eps)
+
+
+def ep_rms_norm(h, params: EpNormParams, x, residual, weight, tokens_per_rank, residual_out, out,
+                codes, scales, stream=None) -> int:
+    kinds = tuple(_ROWS)
+    rc = load_library().ep_rms_norm(
+        h, ctypes.byref(params), _ptr(x, kinds, "x", allow_none=True),
+        _ptr(residual, kinds, "residual", allow_none=True), _ptr(weight, kinds, "weight"),
+        int(tokens_per_rank), _ptr(residual_out, kinds, "residual_out", allow_none=True),
+        _ptr(out, kinds, "out", allow_none=True),
+        _ptr(codes, torch.uint8, "codes", allow_none=True),
+        _ptr(scales, torch.float32, "scales", allow_none=True), _stream(stream))
+    return _check(rc, "ep_rms_norm")
+
+
+def ep_rms_norm_backward(h, params: EpNormParams, grad_out, grad_residual_out, sums, weight,
+                         tokens_per_rank, grad_x, grad_residual, grad_weight, workspace,
+                         workspace_bytes, stream=None) -> int:
+    kinds = tuple(_ROWS)
+    rc = load_library().ep_rms_norm_backward(
+        h, ctypes.byref(params), _ptr(grad_out, kinds, "grad_out", allow_none=True),
+        _ptr(grad_residual_out, kinds, "grad_residual_out", allow_none=True),
+        _ptr(sums, kinds, "sums", allow_none=True), _ptr(weight, kinds, "weight"),
+        int(tokens_per_rank), _ptr(grad_x, kinds, "grad_x", allow_none=True),
+        _ptr(grad_residual, kinds, "grad_residual", allow_none=True),
+        _ptr(grad_weight, torch.float32, "grad_weight"),
+        _ptr(workspace, None, "workspace", allow_none=True), int(workspace_bytes),
+        _stream(stream))
+    return _check(rc, "ep_rms_norm_backward")
+
+
+def ep_rms_norm_backward_workspace(h, tokens_per_rank) -> int:
+    return _check(load_library().ep_rms_norm_backward_workspace(h, int(tokens_per_rank)),
+                  "ep_rms_norm_backward_workspace")
+
+
+def ep_moe_layer(h, format1, format2, x, x_scale, w1, w1_scale, w2, w2_scale, topk_ids, topk_w,
+                 tokens_per_rank, out, workspace, workspace_bytes, stream=None) -> int:
+    scales = (torch.float32,) + tuple(_W4_SCALES)
+    rc = load_library().ep_moe_layer(
+        h, None if format1 is None else ctypes.byref(format1),
+        None if format2 is None else ctypes.byref(format2), _ptr(x, None, "x", allow_none=True),
+        _ptr(x_scale, torch.float32, "x_scale", allow_none=True),
+        _ptr(w1, None, "w1", allow_none=True), _ptr(w1_scale, scales, "w1_scale", allow_none=True),
+        _ptr(w2, None, "w2", allow_none=True), _ptr(w2_scale, scales, "w2_scale", allow_none=True),
+        _ptr(topk_ids, torch.int32, "topk_ids", allow_none=True),
+        _ptr(topk_w, torch.float32, "topk_w", allow_none=True), int(tokens_per_rank),
+        _ptr(out, torch.bfloat16, "out", allow_none=True),
+        _ptr(workspace, None, "workspace", allow_none=True), int(workspace_bytes),
+        _stream(stream))
+    return _check(rc, "ep_moe_layer")
+
+
+def ep_moe_layer_workspace(h, tokens_per_rank) -> int:
+    return _check(load_library().ep_moe_layer_workspace(h, int(tokens_per_rank)),
+                  "ep_moe_layer_workspace")
 
 
 def ep_combine_query_error(h, stream=None) -> int:

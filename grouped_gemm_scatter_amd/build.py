@@ -24,7 +24,7 @@ ARCH = "gfx950"
 
 SOURCES = ["ep_combine.cpp", "gemm_scatter.hip", "gemm_scatter_fp8.hip", "combine.hip",
            "grouping.hip", "dispatch.hip", "layout.hip", "gemm_send.hip", "route.hip",
-           "combine_backward.hip", "gemm_w4.hip"]
+           "combine_backward.hip", "gemm_w4.hip", "norm.hip", "moe_layer.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import functools
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -32,6 +33,28 @@ def _route_params(n_experts, logits_dtype, n_groups, topk_groups, score, group_s
         topk_groups=topk_groups, score=_choice(_SCORES, score, "score"),
         group_score=_choice(_GROUP_SCORES, group_score, "group_score"),
         renormalize=renormalize, scale=scale)
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_params(dtype, residual_dtype, weight_dtype, eps):
+    """The options of a norm as the C boundary takes them."""
+    return B.make_norm_params(dtype=dtype, residual_dtype=residual_dtype,
+                              weight_dtype=weight_dtype, eps=eps)
+
+
+class RmsNorm(NamedTuple):
+    """What EpCombine.rms_norm makes; None for what was not asked for."""
+    out: torch.Tensor | None        # [R][T][hidden_n], the type of x
+    codes: torch.Tensor | None      # [R][T][hidden_n] uint8 e4m3fn codes
+    scales: torch.Tensor | None     # [R][T][hidden_n/128] float32
+    residual: torch.Tensor | None   # [R][T][hidden_n]: x + residual, the residual's type
+
+
+class RmsNormGrad(NamedTuple):
+    """What EpCombine.rms_norm_backward makes."""
+    x: torch.Tensor                 # gradient of x, in its type
+    residual: torch.Tensor          # the same in the type of the sums (x where that is one)
+    weight: torch.Tensor            # [hidden_n] float32
 
 
 @dataclass(frozen=True)
@@ -253,6 +276,131 @@ class EpCombine:
         B.ep_combine_backward(self.handle, at, ids_at, w_at, T, offsets_at, src_at, m, rows_at,
                               grad_w.data_ptr(), stream)
         return grad_w, grad_rows
+
+    def rms_norm(self, x, weight, *, residual=None, eps: float = 1e-6, rows: bool = True,
+                 fp8: bool = False, out=None, codes=None, scales=None, residual_out=None,
+                 stream=None) -> RmsNorm:
+        """RMS norm of x [R][T][hidden_n] (float32, bfloat16 or float16), or of x + residual
+        (x's type or float32; the sum is returned in that type): rows in x's type, and with
+        `fp8` the e4m3fn codes and 1x128 scales that up_swiglu_fp8 and moe_layer take (one
+        pass for both; rows=False leaves the rows out).  `weight` [hidden_n] in x's type or
+        float32.  Results go into tensors that are given; residual_out may be `residual`
+        itself and out `x` itself."""
+        T, N = x.shape[1], self.hidden_n
+        shape = (self.n_ranks, T, N)
+        kept = x.dtype if residual is None else residual.dtype
+        params = _norm_params(x.dtype, kept, weight.dtype, eps)
+        at = self._shape(x, "x", shape, x.dtype)
+        weight_at = self._shape(weight, "weight", (N,), weight.dtype)
+        res_at = kept_at = out_at = codes_at = scales_at = None
+        if residual is not None:
+            res_at = self._shape(residual, "residual", shape, kept)
+            if residual_out is None:
+                residual_out = self._empty(shape, kept, stream)
+            kept_at = self._shape(residual_out, "residual_out", shape, kept)
+        elif residual_out is not None:
+            raise ValueError("residual_out given without a residual")
+        if rows:
+            if out is None:
+                out = self._empty(shape, x.dtype, stream)
+            out_at = self._shape(out, "out", shape, x.dtype)
+        elif out is not None:
+            raise ValueError("out given with rows=False")
+        if fp8:
+            if codes is None:
+                codes = self._empty(shape, torch.uint8, stream)
+            if scales is None:
+                scales = self._empty((self.n_ranks, T, N // 128), torch.float32, stream)
+            codes_at = self._shape(codes, "codes", shape, torch.uint8)
+            scales_at = self._shape(scales, "scales", (self.n_ranks, T, N // 128), torch.float32)
+        elif codes is not None or scales is not None:
+            raise ValueError("codes or scales given with fp8=False")
+        elif not rows:
+            raise ValueError("rows=False and fp8=False ask for nothing")
+        B.ep_rms_norm(self.handle, params, at, res_at, weight_at, T, kept_at, out_at, codes_at,
+                      scales_at, stream)
+        return RmsNorm(out, codes, scales, residual_out)
+
+    def rms_norm_backward(self, grad_out, sums, weight, *, grad_residual=None, eps: float = 1e-6,
+                          grad_x=None, grad_sums=None, grad_weight=None,
+                          stream=None) -> RmsNormGrad:
+        """Gradient of `rms_norm` from that of its rows, grad_out [R][T][hidden_n] in x's
+        type, and of the sums it returned (grad_residual, None for zeros), whose values
+        `sums` are (x itself without a residual).  The gradient of the sum is that of x and
+        of the residual: in x's type, and where the sums are float32 beside 16-bit rows in
+        float32 too.  grad_x may be grad_out itself, grad_sums grad_residual itself."""
+        T, N = grad_out.shape[1], self.hidden_n
+        shape = (self.n_ranks, T, N)
+        params = _norm_params(grad_out.dtype, sums.dtype, weight.dtype, eps)
+        at = self._shape(grad_out, "grad_out", shape, grad_out.dtype)
+        sums_at = self._shape(sums, "sums", shape, sums.dtype)
+        weight_at = self._shape(weight, "weight", (N,), weight.dtype)
+        res_at = both_at = None
+        if grad_residual is not None:
+            res_at = self._shape(grad_residual, "grad_residual", shape, sums.dtype)
+        if grad_x is None:
+            grad_x = self._empty(shape, grad_out.dtype, stream)
+        x_at = self._shape(grad_x, "grad_x", shape, grad_out.dtype)
+        if sums.dtype != grad_out.dtype:
+            if grad_sums is None:
+                grad_sums = self._empty(shape, sums.dtype, stream)
+            both_at = self._shape(grad_sums, "grad_sums", shape, sums.dtype)
+        elif grad_sums is not None:
+            raise ValueError("grad_sums given where grad_x serves for both")
+        else:
+            grad_sums = grad_x
+        if grad_weight is None:
+            grad_weight = self._empty((N,), torch.float32, stream)
+        grad_w_at = self._shape(grad_weight, "grad_weight", (N,), torch.float32)
+        need = B.ep_rms_norm_backward_workspace(self.handle, T)
+        workspace = self._empty((max(need, 16),), torch.uint8, stream)
+        B.ep_rms_norm_backward(self.handle, params, at, res_at, sums_at, weight_at, T, x_at,
+                               both_at, grad_w_at, workspace.data_ptr(), need, stream)
+        return RmsNormGrad(grad_x, grad_sums, grad_weight)
+
+    def moe_layer(self, x, w1, w2, topk_ids, topk_w, *, x_scale=None, w1_scale=None,
+                  w2_scale=None, out=None, stream=None):
+        """The whole layer for a few tokens (at most 64 of all ranks, 1024 picks) on this GPU's
+        experts, in two launches and without the grouped layout: x [R][T][hidden_n] and the
+        picks and weights of `route` to out [R][T][hidden_n] bfloat16, the weighted sum of
+        the local picks as `combine` gives it.  w1 [E_l][2*hidden_k][hidden_n] and w2
+        [E_l][hidden_n][hidden_k] in bfloat16 (w2 from pack_weights where the handle has
+        w_slice_major), or both from pack_weights_w4; with an fp8 handle uint8 e4m3fn codes
+        with w1_scale and w2_scale, and x uint8 codes with x_scale, as `rms_norm` makes them."""
+        T, N, inter, El = x.shape[1], self.hidden_n, self.hidden_k, self.n_experts_per_device
+        fp8 = self.dtype == "fp8"
+        row_type = torch.uint8 if fp8 else torch.bfloat16
+        shape, picks = (self.n_ranks, T, N), (self.n_ranks, T, self.top_k)
+        at = self._shape(x, "x", shape, row_type)
+        ids_at = self._shape(topk_ids, "topk_ids", picks, torch.int32)
+        w_at = self._shape(topk_w, "topk_w", picks, torch.float32)
+        format1 = format2 = x_scale_at = s1_at = s2_at = None
+        if isinstance(w1, PackedW4) or isinstance(w2, PackedW4):
+            w1_at, s1_at = self._packed_w4(w1, 2 * inter, N)
+            w2_at, s2_at = self._packed_w4(w2, N, inter)
+            format1, format2 = w1.format, w2.format
+        else:
+            w1_at = self._flat(w1, "w1", El * 2 * inter * N, row_type)
+            w2_at = self._flat(w2, "w2", El * N * inter, row_type)
+        if fp8:
+            if x_scale is None or w1_scale is None or w2_scale is None:
+                raise ValueError("an fp8 handle takes x_scale, w1_scale and w2_scale")
+            x_scale_at = self._shape(x_scale, "x_scale", (self.n_ranks, T, N // 128),
+                                     torch.float32)
+            s1_at = self._flat(w1_scale, "w1_scale", El * (2 * inter // 128) * (N // 128),
+                               torch.float32)
+            s2_at = self._flat(w2_scale, "w2_scale", El * (N // 128) * (inter // 128),
+                               torch.float32)
+        elif x_scale is not None or w1_scale is not None or w2_scale is not None:
+            raise ValueError("scales are for fp8 handles (packed weights hold their own)")
+        if out is None:
+            out = self._empty(shape, torch.bfloat16, stream)
+        out_at = self._shape(out, "out", shape, torch.bfloat16)
+        need = B.ep_moe_layer_workspace(self.handle, T)
+        workspace = self._empty((max(need, 16),), torch.uint8, stream)
+        B.ep_moe_layer(self.handle, format1, format2, at, x_scale_at, w1_at, s1_at, w2_at, s2_at,
+                       ids_at, w_at, T, out_at, workspace.data_ptr(), need, stream)
+        return out
 
     def pack_weights_w4(self, w, scales, *, codes: str = "int4", stream=None) -> PackedW4:
         """4-bit expert weights laid out once for up_swiglu_w4 and gemm_scatter_w4: w

@@ -206,7 +206,7 @@ int call_tile(const ep_combine_handle* h, int32_t m_total) {
 
 extern "C" {
 
-int ep_combine_version(void) { return 200; }
+int ep_combine_version(void) { return 300; }
 
 const char* ep_combine_strerror(int code) {
   switch (code) {
@@ -817,6 +817,240 @@ int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format, const
   a.scale_f16 = format->scales == EP_W4_SCALE_F16;
   const hipError_t err =
       ep::launch_gemm_w4(a, false, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+}  // extern "C"
+
+namespace {
+
+struct Range {
+  const void* p;
+  uint64_t bytes;
+};
+
+// Whether an output meets another output or an input, but for the input of the same place
+// in `same` where it is exactly that memory.
+template <size_t O, size_t I>
+bool outputs_meet(const Range (&out)[O], const Range (&in)[I], const Range (&same)[O]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (size_t j = 0; j < O; ++j)
+      if (i != j && overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+    for (const Range& r : in)
+      if (overlap(out[i].p, out[i].bytes, r.p, r.bytes) &&
+          !(same[i].p && r.p == same[i].p && out[i].p == r.p && out[i].bytes == r.bytes))
+        return true;
+  }
+  return false;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+uint64_t row_type_bytes(int dtype) { return dtype == EP_ROWS_F32 ? 4 : 2; }
+
+// Checks what the norm and its gradient share and fills it in.
+int norm_args(const ep_combine_handle* h, const ep_norm_params* p, const void* weight,
+              int32_t tokens_per_rank, ep::NormArgs* a) {
+  if (!h || !p) return EP_ERR_INVALID_ARG;
+  if (tokens_per_rank < 0 || tokens_per_rank > h->p.max_tokens_per_rank) return EP_ERR_INVALID_ARG;
+  if (p->dtype < EP_ROWS_F32 || p->dtype > EP_ROWS_F16) return EP_ERR_INVALID_ARG;
+  if (p->residual_dtype != p->dtype && p->residual_dtype != EP_ROWS_F32) return EP_ERR_INVALID_ARG;
+  if (p->weight_dtype != p->dtype && p->weight_dtype != EP_ROWS_F32) return EP_ERR_INVALID_ARG;
+  if (!std::isfinite(p->eps) || p->eps < 0.f) return EP_ERR_INVALID_ARG;
+  if (!weight || !aligned16(weight) || !on_device(h)) return EP_ERR_INVALID_ARG;
+  *a = ep::NormArgs{};
+  a->weight = static_cast<const uint8_t*>(weight);
+  a->rows = int64_t(h->p.n_ranks) * tokens_per_rank;
+  a->N = h->p.hidden_n;
+  a->dtype = p->dtype;
+  a->sum_dtype = p->residual_dtype;
+  a->weight_f32 = p->weight_dtype == EP_ROWS_F32;
+  a->eps = p->eps;
+  return EP_OK;
+}
+
+bool moe_tokens_ok(const ep_combine_handle* h, int32_t tokens_per_rank) {
+  const int64_t tokens = int64_t(h->p.n_ranks) * tokens_per_rank;
+  return tokens <= EP_MOE_MAX_TOKENS && tokens * h->p.top_k <= EP_MOE_MAX_PICKS;
+}
+
+uint64_t moe_workspace(const ep_combine_handle* h, int32_t tokens_per_rank) {
+  return uint64_t(h->p.n_ranks) * tokens_per_rank * h->p.top_k * h->p.hidden_k * 2;
+}
+
+// One product's weights of `rows` x k an expert: bytes of an expert's weights, of the
+// stack's and of its scales.
+struct MoeStack {
+  uint64_t expert, w, scales;
+};
+
+MoeStack moe_stack(const ep_combine_handle* h, const ep_w4_format* f, uint64_t rows, uint64_t k) {
+  const uint64_t El = h->p.n_experts_per_device;
+  if (f) return {rows * k / 2, El * rows * k / 2, El * rows * (k / f->group) * 2};
+  if (h->p.dtype == EP_DTYPE_BF16) return {rows * k * 2, El * rows * k * 2, 0};
+  return {rows * k, El * rows * k, El * (rows / 128) * (k / 128) * 4};
+}
+
+ep::MoeWeights moe_weights(const ep_w4_format* f, const void* w, const void* scales) {
+  ep::MoeWeights m{};
+  m.w = static_cast<const uint8_t*>(w);
+  m.scales = scales;
+  if (f) {
+    m.codes = f->codes;
+    m.group = f->group;
+    m.scale_f16 = f->scales == EP_W4_SCALE_F16;
+  }
+  return m;
+}
+
+}  // namespace
+
+static_assert(EP_MOE_MAX_TOKENS == ep::kMoeTokens && EP_MOE_MAX_PICKS == ep::kMoePicks,
+              "limits of the kernels");
+
+extern "C" {
+
+int ep_rms_norm(ep_combine_t h, const ep_norm_params* params, const void* x, const void* residual,
+                const void* weight, int32_t tokens_per_rank, void* residual_out, void* out,
+                void* codes, float* scales, void* stream) {
+  ep::NormArgs a{};
+  const int rc = norm_args(h, params, weight, tokens_per_rank, &a);
+  if (rc != EP_OK) return rc;
+  if (tokens_per_rank == 0) return EP_OK;
+  if (!x || !codes != !scales || (!out && !codes)) return EP_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, const_cast<const void*>(residual_out),
+                        const_cast<const void*>(out), const_cast<const void*>(codes)})
+    if (!aligned16(p)) return EP_ERR_INVALID_ARG;
+  if (!aligned4(scales)) return EP_ERR_INVALID_ARG;
+  const uint64_t values = uint64_t(a.rows) * a.N;
+  const uint64_t xb = values * row_type_bytes(a.dtype), rb = values * row_type_bytes(a.sum_dtype);
+  const Range outs[] = {{residual_out, residual_out ? rb : 0}, {out, out ? xb : 0},
+                        {codes, codes ? values : 0}, {scales, scales ? values / 32 : 0}};
+  const Range ins[] = {{x, xb}, {residual, residual ? rb : 0},
+                       {weight, uint64_t(a.N) * row_type_bytes(params->weight_dtype)}};
+  const Range same[] = {{residual, 0}, {x, 0}, {nullptr, 0}, {nullptr, 0}};
+  if (outputs_meet(outs, ins, same)) return EP_ERR_INVALID_ARG;
+  a.x = static_cast<const uint8_t*>(x);
+  a.residual = static_cast<const uint8_t*>(residual);
+  a.residual_out = static_cast<uint8_t*>(residual_out);
+  a.out = static_cast<uint8_t*>(out);
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  const hipError_t err = ep::launch_rms_norm(a, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+int64_t ep_rms_norm_backward_workspace(ep_combine_t h, int32_t tokens_per_rank) {
+  if (!h || tokens_per_rank < 0 || tokens_per_rank > h->p.max_tokens_per_rank)
+    return EP_ERR_INVALID_ARG;
+  const int64_t rows = int64_t(h->p.n_ranks) * tokens_per_rank;
+  return int64_t(ep::norm_backward_parts(rows, h->p.hidden_n, h->num_cus)) * h->p.hidden_n * 4;
+}
+
+int ep_rms_norm_backward(ep_combine_t h, const ep_norm_params* params, const void* grad_out,
+                         const void* grad_residual_out, const void* sums, const void* weight,
+                         int32_t tokens_per_rank, void* grad_x, void* grad_residual,
+                         float* grad_weight, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+  ep::NormArgs a{};
+  const int rc = norm_args(h, params, weight, tokens_per_rank, &a);
+  if (rc != EP_OK) return rc;
+  if (!grad_weight || !aligned16(grad_weight)) return EP_ERR_INVALID_ARG;
+  const int64_t need = ep_rms_norm_backward_workspace(h, tokens_per_rank);
+  if (tokens_per_rank > 0) {
+    if (!grad_out || !sums || (!grad_x && !grad_residual) || !workspace || workspace_bytes < need)
+      return EP_ERR_INVALID_ARG;
+    for (const void* p : {grad_out, grad_residual_out, sums, const_cast<const void*>(grad_x),
+                          const_cast<const void*>(grad_residual),
+                          const_cast<const void*>(workspace)})
+      if (!aligned16(p)) return EP_ERR_INVALID_ARG;
+  }
+  const uint64_t values = uint64_t(a.rows) * a.N;
+  const uint64_t xb = values * row_type_bytes(a.dtype), rb = values * row_type_bytes(a.sum_dtype);
+  const Range outs[] = {{grad_x, grad_x ? xb : 0}, {grad_residual, grad_residual ? rb : 0},
+                        {grad_weight, uint64_t(a.N) * 4}, {workspace, uint64_t(need)}};
+  const Range ins[] = {{grad_out, xb}, {grad_residual_out, grad_residual_out ? rb : 0},
+                       {sums, rb}, {weight, uint64_t(a.N) * row_type_bytes(params->weight_dtype)}};
+  const Range same[] = {{grad_out, 0}, {grad_residual_out, 0}, {nullptr, 0}, {nullptr, 0}};
+  if (outputs_meet(outs, ins, same)) return EP_ERR_INVALID_ARG;
+  a.grad_out = static_cast<const uint8_t*>(grad_out);
+  a.grad_residual = static_cast<const uint8_t*>(grad_residual_out);
+  a.x = static_cast<const uint8_t*>(sums);
+  a.grad_x = static_cast<uint8_t*>(grad_x);
+  a.grad_sum = static_cast<uint8_t*>(grad_residual);
+  a.grad_weight = grad_weight;
+  a.partial = static_cast<float*>(workspace);
+  const hipError_t err =
+      ep::launch_rms_norm_backward(a, h->num_cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+int64_t ep_moe_layer_workspace(ep_combine_t h, int32_t tokens_per_rank) {
+  if (!h || tokens_per_rank < 0 || tokens_per_rank > h->p.max_tokens_per_rank)
+    return EP_ERR_INVALID_ARG;
+  if (!moe_tokens_ok(h, tokens_per_rank)) return EP_ERR_UNSUPPORTED;
+  return int64_t(moe_workspace(h, tokens_per_rank));
+}
+
+int ep_moe_layer(ep_combine_t h, const ep_w4_format* format1, const ep_w4_format* format2,
+                 const void* x, const float* x_scale, const void* w1, const void* w1_scale,
+                 const void* w2, const void* w2_scale, const int32_t* topk_ids,
+                 const float* topk_w, int32_t tokens_per_rank, void* out, void* workspace,
+                 int64_t workspace_bytes, void* stream) {
+  if (!h || !format1 != !format2) return EP_ERR_INVALID_ARG;
+  if (format1 && (!w4_format_ok(format1) || !w4_format_ok(format2))) return EP_ERR_INVALID_ARG;
+  if (tokens_per_rank < 0 || tokens_per_rank > h->p.max_tokens_per_rank) return EP_ERR_INVALID_ARG;
+  const bool fp8 = h->p.dtype == EP_DTYPE_FP8_E4M3_B128;
+  const uint64_t hidden = h->p.hidden_n, inter = h->p.hidden_k;
+  if ((fp8 && format1) || inter % 128 || !moe_tokens_ok(h, tokens_per_rank))
+    return EP_ERR_UNSUPPORTED;
+  const MoeStack s1 = moe_stack(h, format1, 2 * inter, hidden);
+  const MoeStack s2 = moe_stack(h, format2, hidden, inter);
+  const uint64_t tokens = uint64_t(h->p.n_ranks) * tokens_per_rank;
+  const uint64_t x_bytes = tokens * hidden * (fp8 ? 1 : 2), out_bytes = tokens * hidden * 2;
+  const uint64_t need = moe_workspace(h, tokens_per_rank);
+  constexpr uint64_t k4G = uint64_t(1) << 32;      // 32-bit offsets inside each
+  if (s1.expert >= k4G || s2.expert >= k4G || x_bytes >= k4G || need >= k4G)
+    return EP_ERR_UNSUPPORTED;
+  if (!on_device(h)) return EP_ERR_INVALID_ARG;
+  if (tokens_per_rank == 0) return EP_OK;
+  if (!x || !w1 || !w2 || !topk_ids || !topk_w || !out || !workspace ||
+      workspace_bytes < int64_t(need))
+    return EP_ERR_INVALID_ARG;
+  if ((fp8 && !x_scale) || ((fp8 || format1) && (!w1_scale || !w2_scale)))
+    return EP_ERR_INVALID_ARG;
+  for (const void* p : {x, w1, w2, const_cast<const void*>(out),
+                        const_cast<const void*>(workspace)})
+    if (!aligned16(p)) return EP_ERR_INVALID_ARG;
+  if (!aligned4(topk_ids) || !aligned4(topk_w)) return EP_ERR_INVALID_ARG;
+  if (fp8 && (!aligned4(x_scale) || !aligned4(w1_scale) || !aligned4(w2_scale)))
+    return EP_ERR_INVALID_ARG;
+  if (format1 && (!aligned16(w1_scale) || !aligned16(w2_scale))) return EP_ERR_INVALID_ARG;
+  const uint64_t pick_bytes = tokens * h->p.top_k * 4;
+  const Range outs[] = {{out, out_bytes}, {workspace, need}};
+  const Range ins[] = {{x, x_bytes}, {x_scale, fp8 ? tokens * (hidden / 128) * 4 : 0},
+                       {w1, s1.w}, {w1_scale, s1.scales}, {w2, s2.w}, {w2_scale, s2.scales},
+                       {topk_ids, pick_bytes}, {topk_w, pick_bytes}};
+  const Range same[] = {{nullptr, 0}, {nullptr, 0}};
+  if (outputs_meet(outs, ins, same)) return EP_ERR_INVALID_ARG;
+  ep::MoeArgs a{};
+  a.x = static_cast<const uint8_t*>(x);
+  a.x_scale = x_scale;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  a.h = static_cast<uint8_t*>(workspace);
+  a.out = static_cast<uint8_t*>(out);
+  a.w1 = moe_weights(format1, w1, w1_scale);
+  a.w2 = moe_weights(format2, w2, w2_scale);
+  a.w2.slice_major = (h->p.flags & EP_FLAG_W_SLICE_MAJOR) ? 1 : 0;
+  a.fp8 = fp8;
+  a.tokens = int(tokens);
+  a.top_k = h->p.top_k;
+  a.expert_lo = h->p.my_rank * h->p.n_experts_per_device;
+  a.n_experts = h->p.n_experts_per_device;
+  a.hidden = h->p.hidden_n;
+  a.inter = h->p.hidden_k;
+  const hipError_t err = ep::launch_moe(a, h->num_cus, static_cast<hipStream_t>(stream));
   return err == hipSuccess ? EP_OK : EP_ERR_HIP;
 }
 

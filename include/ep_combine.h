@@ -591,6 +591,116 @@ EP_API int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format
                                       int32_t m_total, int32_t p3_control, void* c_local,
                                       uint64_t epoch, void* stream);
 
+/* RMS norm of the rows in front of the layer, with the residual's addition: the rows
+   that the router and the dispatch read, in their own type, as the codes and scales
+   that the fp8 calls take, or both in one pass.  For every row of N = hidden_n values
+     s = x + residual          (binary32; s = x without a residual)
+     y = s * w / sqrt(mean(s^2) + eps)
+     residual_out = s, out = y rounded to their types
+     scales[b] = max |y| / 448 over the 128 values of block b (1 if all are zero, at least
+                 2^-126), codes = e4m3fn(y / scales[b]), rounded to nearest even
+   everything in binary32 until those roundings (the norm is of s before its rounding).
+   The sum of squares is binary32 too: beyond its range it is infinite and y zero, and
+   an infinity or a NaN in a row makes that row's y NaN, and no other's. */
+#define EP_ROWS_F32 0
+#define EP_ROWS_BF16 1
+#define EP_ROWS_F16 2
+
+typedef struct ep_norm_params {
+  int32_t dtype;                 /* EP_ROWS_*: type of x, out and grad_out, grad_x */
+  int32_t residual_dtype;        /* of residual and residual_out and their gradients: dtype
+                                    or EP_ROWS_F32 */
+  int32_t weight_dtype;          /* of w: dtype or EP_ROWS_F32 */
+  float eps;                     /* finite, not negative */
+} ep_norm_params;
+
+/* x        device, [R][tokens_per_rank][N], 16-byte aligned like every array of rows.
+   residual device, the same shape, or NULL.
+   weight   device, [N], 16-byte aligned.
+   tokens_per_rank  0..max_tokens_per_rank.
+   residual_out device, the same shape, or NULL; may be `residual` itself.  Without a
+            residual it receives x in the residual's type.
+   out      device, the same shape, or NULL; may be `x` itself.
+   codes    device, [R][tokens_per_rank][N] e4m3fn codes, with scales device,
+            [R][tokens_per_rank][N/128] fp32: both or neither; at least one of out and
+            codes.
+   One launch; deterministic.  Uses the handle's n_ranks and hidden_n and touches none of
+   its buffers.  EP_ERR_INVALID_ARG for a bad size, type or pointer, for outputs that
+   overlap each other or an input (but for the two pairs above), or when the handle's device
+   is not the current one. */
+EP_API int ep_rms_norm(ep_combine_t h, const ep_norm_params* params, const void* x,
+                       const void* residual, const void* weight, int32_t tokens_per_rank,
+                       void* residual_out, void* out, void* codes, float* scales, void* stream);
+
+/* Gradient of ep_rms_norm.  With r the stored sums (residual_out, or x without a residual),
+   g the gradient of y and q that of residual_out, inv = 1 / sqrt(mean(r^2) + eps):
+     ds = inv * (g * w - r * inv^2 * mean(g * w * r)) + q
+     grad_weight = sum over all rows of g * r * inv
+   in binary32.  x and the residual are the two terms of s, so ds is the gradient of both:
+   grad_x is ds in dtype, grad_residual in residual_dtype (where the types are one, one
+   of the two serves).  The codes' rounding has no gradient: g is that of the values they
+   stand for.
+   grad_out device, [R][tokens_per_rank][N], dtype.
+   grad_residual_out  device, the same shape, residual_dtype, or NULL for zeros.
+   sums     device, the same shape, residual_dtype (without a residual: x, and
+            residual_dtype = dtype).
+   grad_x, grad_residual  device, the same shape, written; either may be NULL, not both.
+            grad_x may be grad_out itself, grad_residual grad_residual_out.
+   grad_weight  device, [N] fp32, written (zeros for no tokens).
+   workspace  device, at least ep_rms_norm_backward_workspace(h, tokens_per_rank) bytes,
+            16-byte aligned, written; calls that may overlap in time need one each.
+   Two launches; deterministic.  Errors as for ep_rms_norm. */
+EP_API int ep_rms_norm_backward(ep_combine_t h, const ep_norm_params* params,
+                                const void* grad_out, const void* grad_residual_out,
+                                const void* sums, const void* weight, int32_t tokens_per_rank,
+                                void* grad_x, void* grad_residual, float* grad_weight,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of that workspace, or EP_ERR_INVALID_ARG. */
+EP_API int64_t ep_rms_norm_backward_workspace(ep_combine_t h, int32_t tokens_per_rank);
+
+/* The whole layer for a few tokens, for decode steps where grouping, dispatch, two
+   products and the combine would be a launch each and the rows' number a wait of the host:
+     out[rk][t][:] = bf16( sum over the local picks k of topk_w[rk][t][k] *
+                           W2_e (silu(g) * u) ),   [g; u] = W1_e x[rk][t]
+   over the experts e of this GPU, as ep_grouped_gemm_swiglu, ep_grouped_gemm_scatter and
+   ep_combine_reduce together give it, with silu(g) * u rounded to bf16 and the second
+   product's rows not rounded.  (On fp8 handles silu(g) * u is not put into 8 bits again.)
+   A token without local picks gets +0; picks of the same expert by one token add up.
+   Neither rows nor weights of one expert change what a token without it gets, not even
+   by infinities or NaN.
+   format1, format2  NULL for weights in the handle's dtype, or the formats of 4-bit
+            weights packed by ep_pack_weights_w4 (bf16 handles; both or neither).
+   x        device, [R][tokens_per_rank][hidden] bf16, or with an fp8 handle e4m3fn codes
+            with x_scale device, [R][tokens_per_rank][hidden/128] fp32 (else ignored).
+   w1       device, [E_l][2I][hidden], gate rows 0..I-1, then up rows, as for the
+            up-projections (hidden = hidden_n, I = hidden_k); packed for 4 bits.
+   w1_scale device, [E_l][2I/128][hidden/128] fp32 (fp8), or the packed 4-bit scales.
+   w2, w2_scale  the down-projection's, [E_l][hidden][I]; in the slice-major layout
+            with EP_FLAG_W_SLICE_MAJOR (bf16 weights).
+   topk_ids, topk_w  as for ep_combine_reduce (what ep_route_topk gives).
+   tokens_per_rank  0..max_tokens_per_rank; R * tokens_per_rank at most EP_MOE_MAX_TOKENS
+            and R * tokens_per_rank * top_k at most EP_MOE_MAX_PICKS (EP_ERR_UNSUPPORTED).
+   out      device, [R][tokens_per_rank][hidden] bf16.
+   workspace  device, at least ep_moe_layer_workspace(h, tokens_per_rank) bytes, written;
+            calls that may overlap in time need one each.
+   I a multiple of 128 (EP_ERR_UNSUPPORTED); arrays 16-byte aligned (topk_ids, topk_w and
+   fp32 scales 4-byte).  Stacks of any size, one expert's w1 below 4 GiB
+   (EP_ERR_UNSUPPORTED).  EP_ERR_INVALID_ARG for outputs or a workspace that overlap
+   each other or an input, or when the handle's device is not the current one.  Two
+   launches; deterministic.  No receive buffer, count word or flag is touched. */
+#define EP_MOE_MAX_TOKENS 64
+#define EP_MOE_MAX_PICKS 1024
+
+EP_API int ep_moe_layer(ep_combine_t h, const ep_w4_format* format1, const ep_w4_format* format2,
+                        const void* x, const float* x_scale, const void* w1, const void* w1_scale,
+                        const void* w2, const void* w2_scale, const int32_t* topk_ids,
+                        const float* topk_w, int32_t tokens_per_rank, void* out, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/* Bytes of that workspace, EP_ERR_INVALID_ARG or EP_ERR_UNSUPPORTED. */
+EP_API int64_t ep_moe_layer_workspace(ep_combine_t h, int32_t tokens_per_rank);
+
 /* Synchronizes the stream, returns the latched device error bits (>= 0) and
    clears them, or a negative code if the read failed. */
 EP_API int ep_combine_query_error(ep_combine_t h, void* stream);

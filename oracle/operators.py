@@ -152,3 +152,65 @@ def combine_backward(grad_out_bits, topk_w, picks, slot_bits, shape):
     grad_w[at] = (g * s).sum(axis=1)
     bound[at] = np.abs(g * s).sum(axis=1)
     return grad_w, np.asarray(topk_w, dtype=np.float64)[at][:, None] * g, bound
+
+
+def rms_norm(x, weight, *, residual=None, eps=1e-6):
+    """(s, y) of rows [n][N]: s = x + residual, y = s w / sqrt(mean(s^2) + eps)."""
+    s = np.asarray(x, dtype=np.float64)
+    if residual is not None:
+        s = s + np.asarray(residual, dtype=np.float64)
+    rms = np.sqrt((s * s).mean(axis=-1, keepdims=True) + eps)
+    return s, s / rms * np.asarray(weight, dtype=np.float64)
+
+
+def rms_norm_backward(grad_out, sums, weight, *, grad_residual=None, eps=1e-6):
+    """(ds [n][N], dw [N], bound_ds, bound_dw): the gradients of the sums and the weight,
+    and the sums of the absolute values of the terms that make them."""
+    g, r = np.asarray(grad_out, dtype=np.float64), np.asarray(sums, dtype=np.float64)
+    w = np.asarray(weight, dtype=np.float64)
+    inv = 1.0 / np.sqrt((r * r).mean(axis=-1, keepdims=True) + eps)
+    gw = g * w
+    ds = inv * (gw - r * inv ** 2 * (gw * r).mean(axis=-1, keepdims=True))
+    bound = inv * (np.abs(gw) + np.abs(r) * inv ** 2 * np.abs(gw * r).mean(axis=-1, keepdims=True))
+    if grad_residual is not None:
+        q = np.asarray(grad_residual, dtype=np.float64)
+        ds, bound = ds + q, bound + np.abs(q)
+    each = g * r * inv
+    return ds, each.sum(axis=0), bound, np.abs(each).sum(axis=0)
+
+
+def moe_layer(x, w1, w2, ids, topk_w, expert_lo=0):
+    """The layer of tokens x [n][hidden] through the experts w1 [E][2I][hidden], w2
+    [E][hidden][I] that their picks ids [n][k] name: out[t] = sum over local picks of
+    topk_w * w2 (silu(g) u).  Returns (out, bound): bound [n][hidden] is what rounding may
+    move it by where the products are summed in binary32 and silu(g) u is rounded to
+    bf16.  Each product of K terms: the matrix unit's additions are within 2^-23 of a
+    partial sum each, and scales and joins add at most K / 16 + 32 operations of 2^-24."""
+    x, topk_w = np.asarray(x, dtype=np.float64), np.asarray(topk_w, dtype=np.float64)
+    out, bound = np.zeros_like(x), np.zeros_like(x)
+
+    def steps(k):
+        return k * 2.0 ** -23 + (k / 16 + 32) * 2.0 ** -24
+
+    for t in range(x.shape[0]):
+        total, size = np.zeros(x.shape[1]), np.zeros(x.shape[1])
+        for k, i in enumerate(np.asarray(ids)[t]):
+            e = int(i) - expert_lo
+            if not 0 <= e < w1.shape[0]:
+                continue
+            I = w1.shape[1] // 2
+            y, a = w1[e] @ x[t], np.abs(w1[e]) @ np.abs(x[t])
+            g, u, b = y[:I], y[I:], steps(x.shape[1]) * a
+            with np.errstate(over="ignore"):
+                silu = g / (1.0 + np.exp(-g))
+            h = silu * u
+            dh = (1.1 * b[:I] * (np.abs(u) + b[I:]) + np.abs(silu) * b[I:] +
+                  (2.0 ** -8 + 2.0 ** -20) * np.abs(h) + 1e-38)
+            z = w2[e] @ h
+            mag = np.abs(w2[e]) @ (np.abs(h) + dh)
+            total += topk_w[t, k] * z
+            size += np.abs(topk_w[t, k]) * mag
+            bound[t] += np.abs(topk_w[t, k]) * (np.abs(w2[e]) @ dh + steps(I) * mag)
+        out[t] = total
+        bound[t] += 128 * 2.0 ** -24 * size
+    return out, bound
