@@ -95,14 +95,23 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s) {
   __syncthreads();
 }
 
+// Loads and uses of the steps stay where they are written: a wait for a step counts the
+// loads behind it, which the compiler can only do where they are in one order on every path.
+#define in_order(...)                    \
+  do {                                   \
+    __VA_ARGS__;                         \
+    __builtin_amdgcn_sched_barrier(0);   \
+  } while (0)
+
 // ---- The three kinds of weights.  Block: 16 rows of them, one step of 128 k, as a wave
 // holds it; Rows: the first operand's 16 rows of the same k.  Wave-uniform: where a
 // block's rows start (`row0`), the step.
 
 struct Bf16 {
-  static constexpr int DEPTH = 2;
+  static constexpr int DEPTH = 2, DEPTH2 = 1;     // steps in flight, with one and two row blocks
+  static constexpr bool PAIR_A_LANE = false;
   struct Source {
-    buffer w;
+    const uint8_t* w;
     uint32_t slice, lane;               // bytes between 64-k slices; of this lane's row
   };
   struct Block { u32x4 v[4]; };
@@ -110,7 +119,7 @@ struct Bf16 {
   static __device__ __forceinline__ Source source(const MoeWeights& w, int e, int rows, int k,
                                                   int lane) {
     Source s;
-    s.w = make_buffer(w.w + (size_t)e * rows * k * 2);
+    s.w = w.w + (size_t)e * rows * k * 2;
     const uint32_t pitch = w.slice_major ? 128 : k * 2;
     s.slice = w.slice_major ? (uint32_t)rows * 128 : 128;
     s.lane = (lane & 15) * pitch + (lane >> 4) * 16;
@@ -119,16 +128,19 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t start(const MoeWeights& w, int row0, int k) {
     return (uint32_t)row0 * (w.slice_major ? 128 : k * 2);
   }
-  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int kt) {
+  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int kt,
+                                              int length) {
+    const buffer w = make_buffer(s.w, length);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      b.v[q] = buffer_load16_nt(s.w, s.lane + (q & 1) * 64, start + (2 * kt + (q >> 1)) * s.slice);
+      in_order(b.v[q] = buffer_load16(w, s.lane + (q & 1) * 64,
+                                      start + (2 * kt + (q >> 1)) * s.slice));
   }
   // lane L: row L % 16 (at byte `row` of it), k = 32 q + 8 (L / 16) + 0..7
   static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 16; }
   static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r.v[q] = buffer_load16(x, row + q * 64, kt * 256);
+    for (int q = 0; q < 4; ++q) in_order(r.v[q] = buffer_load16(x, row + q * 64, kt * 256));
   }
   static __device__ __forceinline__ void multiply(f32x4& acc, const Rows& r, const Block& b) {
 #pragma unroll
@@ -141,9 +153,9 @@ struct Bf16 {
 // e4m3fn codes with a scale for 128 x 128 of them.  A lane's 16 bytes are two operands of 8
 // consecutive k, so MFMA 2 i + j takes k = 64 i + 16 (L / 16) + 8 j + 0..7 of both sides.
 struct Fp8 {
-  static constexpr int DEPTH = 3;
   struct Source {
-    buffer w, s;
+    const uint8_t* w;
+    const float* s;
     uint32_t lane;
     int kb;                             // scale blocks a row
   };
@@ -155,32 +167,37 @@ struct Fp8 {
                                                   int lane) {
     Source s;
     s.kb = k / 128;
-    s.w = make_buffer(w.w + (size_t)e * rows * k);
-    s.s = make_buffer(reinterpret_cast<const float*>(w.scales) + (size_t)e * (rows / 128) * s.kb);
+    s.w = w.w + (size_t)e * rows * k;
+    s.s = reinterpret_cast<const float*>(w.scales) + (size_t)e * (rows / 128) * s.kb;
     s.lane = (lane & 15) * k + (lane >> 4) * 16;
     return s;
   }
   static __device__ __forceinline__ uint32_t start(const MoeWeights&, int row0, int) {
     return row0;
   }
-  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t row0, int kt) {
+  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t row0, int kt,
+                                              int length) {
+    const buffer w = make_buffer(s.w, length);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      b.v[i] = buffer_load16_nt(s.w, s.lane + i * 64, (row0 * s.kb + kt) * 128);
-    buffer_load_to(b.s, s.s, 0, ((row0 >> 7) * s.kb + kt) * 4);
+      in_order(b.v[i] = buffer_load16(w, s.lane + i * 64, (row0 * s.kb + kt) * 128));
+    in_order(buffer_load_to(b.s, make_buffer(s.s, length), 0, ((row0 >> 7) * s.kb + kt) * 4));
   }
 };
 
-// Rows of codes with a scale for 128 of them: the up-projection.
+// Rows of codes with a scale for 128 of them: the up-projection.  The weights are the
+// first operand, so that a lane's results are of one pair, whose scale it has loaded.
 struct Fp8Up : Fp8 {
+  static constexpr int DEPTH = 3, DEPTH2 = 2;
+  static constexpr bool PAIR_A_LANE = true;
   struct Rows {
     u32x4 v[2];
-    uint32_t s[4];                      // of rows 4 (L / 16) + 0..3, as the results have them
+    uint32_t s;
   };
   static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 16; }
   static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) r.v[i] = buffer_load16(x, row + i * 64, kt * 128);
+    for (int i = 0; i < 2; ++i) in_order(r.v[i] = buffer_load16(x, row + i * 64, kt * 128));
   }
   static __device__ __forceinline__ void multiply(f32x4& acc, const Rows& r, const Block& b) {
     f32x4 part = {0.f, 0.f, 0.f, 0.f};
@@ -190,22 +207,23 @@ struct Fp8Up : Fp8 {
       for (int j = 0; j < 2; ++j) {
         const long xr = (long)r.v[i][2 * j] | (long)((uint64_t)r.v[i][2 * j + 1] << 32);
         const long wr = (long)b.v[i][2 * j] | (long)((uint64_t)b.v[i][2 * j + 1] << 32);
-        part = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(xr, wr, part, 0, 0, 0);
+        part = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(wr, xr, part, 0, 0, 0);
       }
-    const float ws = __builtin_bit_cast(float, b.s);
+    const float sc = __builtin_bit_cast(float, r.s) * __builtin_bit_cast(float, b.s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      acc[i] = __builtin_fmaf(part[i], __builtin_bit_cast(float, r.s[i]) * ws, acc[i]);
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(part[i], sc, acc[i]);
   }
 };
 
 // Rows in bf16: the down-projection, the codes converted (exactly).
 struct Fp8Down : Fp8 {
+  static constexpr int DEPTH = 3;
   struct Rows { u32x4 v[4]; };
   static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 32; }
   static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r.v[q] = buffer_load16(x, row + (q >> 1) * 128 + (q & 1) * 16, kt * 256);
+    for (int q = 0; q < 4; ++q)
+      in_order(r.v[q] = buffer_load16(x, row + (q >> 1) * 128 + (q & 1) * 16, kt * 256));
   }
   static __device__ __forceinline__ bf16x8 values(uint32_t lo, uint32_t hi) {
     const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, 0);
@@ -230,10 +248,11 @@ struct Fp8Down : Fp8 {
 // Packed 4-bit codes: 16 rows x 128 k are one run of 1 KB.
 template <class F>
 struct W4 {
-  static constexpr int DEPTH = 3;
+  static constexpr int DEPTH = 3, DEPTH2 = 1;
+  static constexpr bool PAIR_A_LANE = false;
   static constexpr uint32_t SB = 16 * (128 / F::GROUP) * 2;   // scale bytes of a run
   struct Source {
-    buffer w, s;
+    const uint8_t *w, *s;
     uint32_t lane, lane_s;
     int kt;                             // runs of a 16-row block
   };
@@ -247,8 +266,8 @@ struct W4 {
     Source s;
     s.kt = k / 128;
     const size_t run = (size_t)e * (rows / 16) * s.kt;
-    s.w = make_buffer(w.w + run * 1024);
-    s.s = make_buffer(reinterpret_cast<const uint8_t*>(w.scales) + run * SB);
+    s.w = w.w + run * 1024;
+    s.s = reinterpret_cast<const uint8_t*>(w.scales) + run * SB;
     s.lane = lane * 16;
     s.lane_s = (lane & 15) * (SB / 16);
     return s;
@@ -256,15 +275,16 @@ struct W4 {
   static __device__ __forceinline__ uint32_t start(const MoeWeights&, int row0, int) {
     return row0 / 16;
   }
-  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int kt) {
+  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int kt,
+                                              int length) {
     const uint32_t run = start * s.kt + kt;
-    b.v = buffer_load16_nt(s.w, s.lane, run * 1024);
-    buffer_load_to(b.s, s.s, s.lane_s, run * SB);
+    in_order(b.v = buffer_load16(make_buffer(s.w, length), s.lane, run * 1024));
+    in_order(buffer_load_to(b.s, make_buffer(s.s, length), s.lane_s, run * SB));
   }
   static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 16; }
   static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r.v[q] = buffer_load16(x, row + q * 64, kt * 256);
+    for (int q = 0; q < 4; ++q) in_order(r.v[q] = buffer_load16(x, row + q * 64, kt * 256));
   }
   static __device__ __forceinline__ void multiply(f32x4& acc, const Rows& r, const Block& b) {
     constexpr int SPT = 128 / F::GROUP, QPS = 4 / SPT;
@@ -283,101 +303,103 @@ struct W4 {
   }
 };
 
-// Waves a SIMD: 128 registers hold the steps of one row block, two take up to 256.
-template <int MT> constexpr int kPerSimd = MT == 1 ? 4 : 2;
-
-template <class P> constexpr bool kCodedRows = false;
-template <> constexpr bool kCodedRows<Fp8Up> = true;
-
 // ---- Up-projection and SwiGLU.  An item is a segment and 16 outputs: 16 gate rows and the 16
 // up rows of W1, whose K the waves split.
-template <class P, int MT>
-__global__ __launch_bounds__(kThreads, kPerSimd<MT>) void moe_up_kernel(MoeArgs a) {
+template <class P, int MT, int DEPTH>
+__device__ __forceinline__ void up_item(const MoeArgs& a, const Table& s, f32x4 (*s_part)[2][2][64],
+                                        int e, int b, int pair, int n, int wave, int lane) {
+  const int KT = a.hidden / 128;
+  const auto src = P::source(a.w1, e, 2 * a.inter, a.hidden, lane);
+  const uint32_t gate = P::start(a.w1, b * 16, a.hidden);
+  const uint32_t up = P::start(a.w1, a.inter + b * 16, a.hidden);
+  // rows past the segment's last repeat it; their results are not stored
+  uint32_t row[MT], scale_at[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int t = s.token[pair + min(j * 16 + (lane & 15), n - 1)];
+    row[j] = (uint32_t)t * (uint32_t)a.hidden * (P::PAIR_A_LANE ? 1 : 2) + P::row_lane(lane);
+    scale_at[j] = t * KT * 4;
+  }
+  struct Step {
+    typename P::Block g, u;
+    typename P::Rows r[MT];
+  };
+  auto load = [&](Step& st, int k) {
+    const int length = buffer_length(k, KT);
+    P::load(st.g, src, gate, k, length);
+    P::load(st.u, src, up, k, length);
+    const buffer x = make_buffer(a.x, length);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      P::load_rows(st.r[j], x, row[j], k);
+      if constexpr (P::PAIR_A_LANE)
+        in_order(buffer_load_to(st.r[j].s, make_buffer(a.x_scale, length), scale_at[j], k * 4));
+    }
+  };
+  f32x4 ag[MT], au[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) ag[j] = au[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // A wave takes every eighth step, so that the workgroup's reads of a row are one run.
+  // Loads ahead are unconditional, past the end of an empty buffer: with one under a
+  // condition the compiler would wait for all that are in flight.
+  Step st[DEPTH];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) load(st[d], wave + d * kWaves);
+  for (int k = wave; k < KT;) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        P::multiply(ag[j], st[d].r[j], st[d].g);
+        P::multiply(au[j], st[d].r[j], st[d].u);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      load(st[d], k + DEPTH * kWaves);
+      k += kWaves;
+      if (k >= KT) break;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    s_part[wave][0][j][lane] = ag[j];
+    s_part[wave][1][j][lane] = au[j];
+  }
+}
+
+template <class P>
+__global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
   __shared__ Table s;
-  __shared__ f32x4 s_part[kWaves][2][MT][64];
+  __shared__ f32x4 s_part[kWaves][2][2][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  build_table<16 * MT, false>(a, s);
-  const int KT = a.hidden / 128, per = a.inter / 16;
-  const int k0 = wave * KT / kWaves, k1 = (wave + 1) * KT / kWaves;
+  build_table<32, false>(a, s);
+  const int per = a.inter / 16;
   const int items = __builtin_amdgcn_readfirstlane(s.segments) * per;
-  constexpr int XB = kCodedRows<P> ? 1 : 2;           // bytes a value of x
-  const buffer x = make_buffer(a.x), xs = make_buffer(a.x_scale);
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int seg = item / per, b = item % per;
     const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
     const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
     const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
-    const auto src = P::source(a.w1, e, 2 * a.inter, a.hidden, lane);
-    const uint32_t gate = P::start(a.w1, b * 16, a.hidden);
-    const uint32_t up = P::start(a.w1, a.inter + b * 16, a.hidden);
-    // rows past the segment's last repeat it; their results are not stored
-    uint32_t row[MT], scale_at[MT][4];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int t = s.token[pair + min(j * 16 + (lane & 15), n - 1)];
-      row[j] = (uint32_t)t * (uint32_t)a.hidden * XB + P::row_lane(lane);
-      if constexpr (kCodedRows<P>)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          scale_at[j][i] = s.token[pair + min(j * 16 + (lane >> 4) * 4 + i, n - 1)] * KT * 4;
-    }
-    struct Step {
-      typename P::Block g, u;
-      typename P::Rows r[MT];
-    };
-    auto load = [&](Step& st, int k) {
-      P::load(st.g, src, gate, k);
-      P::load(st.u, src, up, k);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        P::load_rows(st.r[j], x, row[j], k);
-        if constexpr (kCodedRows<P>)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) buffer_load_to(st.r[j].s[i], xs, scale_at[j][i], k * 4);
-      }
-    };
-    f32x4 ag[MT], au[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) ag[j] = au[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (k0 < k1) {
-      // Loads ahead are unconditional, past the end those of the last step again: with one
-      // under a condition the compiler would wait for all that are in flight.
-      Step st[P::DEPTH];
-#pragma unroll
-      for (int d = 0; d < P::DEPTH; ++d) load(st[d], min(k0 + d, k1 - 1));
-      for (int k = k0; k < k1;) {
-#pragma unroll
-        for (int d = 0; d < P::DEPTH; ++d) {
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            P::multiply(ag[j], st[d].r[j], st[d].g);
-            P::multiply(au[j], st[d].r[j], st[d].u);
-          }
-          load(st[d], min(k + P::DEPTH, k1 - 1));
-          if (++k >= k1) break;
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      s_part[wave][0][j][lane] = ag[j];
-      s_part[wave][1][j][lane] = au[j];
-    }
+    if (n <= 16)
+      up_item<P, 1, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
+    else
+      up_item<P, 2, P::DEPTH2>(a, s, s_part, e, b, pair, n, wave, lane);
     __syncthreads();
     // one value a thread: a pair's row and an output
-    if (tid < MT * 256) {
+    {
       const int j = tid >> 8, l = (tid >> 2) & 63, i = tid & 3;
-      float g = 0.f, u = 0.f;
+      const int r = j * 16 + (P::PAIR_A_LANE ? l & 15 : (l >> 4) * 4 + i);
+      const int c = P::PAIR_A_LANE ? (l >> 4) * 4 + i : l & 15;
+      if (r < n) {
+        float g = 0.f, u = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        g += s_part[w][0][j][l][i];
-        u += s_part[w][1][j][l][i];
-      }
-      const int r = j * 16 + (l >> 4) * 4 + i;
-      if (r < n)
-        reinterpret_cast<__bf16*>(a.h)[(size_t)(pair + r) * a.inter + b * 16 + (l & 15)] =
+        for (int w = 0; w < kWaves; ++w) {
+          g += s_part[w][0][j][l][i];
+          u += s_part[w][1][j][l][i];
+        }
+        reinterpret_cast<__bf16*>(a.h)[(size_t)(pair + r) * a.inter + b * 16 + c] =
             (__bf16)(g / (1.f + expf(-g)) * u);
+      }
     }
     __syncthreads();
   }
@@ -386,66 +408,79 @@ __global__ __launch_bounds__(kThreads, kPerSimd<MT>) void moe_up_kernel(MoeArgs 
 // ---- Down-projection and the weighted sum.  A workgroup takes 16 columns of the output; the
 // steps of all segments are one run that the waves split evenly.  A wave adds what it has of
 // a segment, times the pairs' weights, to its own sums of the tokens in LDS.
-template <class P, int MT>
-__global__ __launch_bounds__(kThreads, kPerSimd<MT>) void moe_down_kernel(MoeArgs a) {
+// The segments are of 16 pairs: an expert's weights are read again for its next 16, by the
+// same workgroup and at once.
+template <class P>
+__global__ __launch_bounds__(kThreads, 4) void moe_down_kernel(MoeArgs a) {
   __shared__ Table s;
-  __shared__ float s_out[kWaves][MT == 1 ? 16 : kMoeTokens][16];
+  __shared__ float s_out[kWaves][kMoeTokens][16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = lane; i < a.tokens * 16; i += 64) s_out[wave][i >> 4][i & 15] = 0.f;
-  build_table<16 * MT, true>(a, s);
+  build_table<16, true>(a, s);
   const int KT = a.inter / 128;
-  const int steps = __builtin_amdgcn_readfirstlane(s.segments) * KT;
-  const int s0 = wave * steps / kWaves, s1 = (wave + 1) * steps / kWaves;
   const int b = blockIdx.x;
-  const buffer h = make_buffer(a.h);
   const uint32_t start = P::start(a.w2, b * 16, a.inter);
-  if (s0 < s1) {
-    struct Step {
-      typename P::Block w;
-      typename P::Rows r[MT];
-    };
-    auto load = [&](Step& st, int at) {
-      const int seg = at / KT, k = at % KT;
-      const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
-      const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
-      const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
-      const auto src = P::source(a.w2, e, a.hidden, a.inter, lane);
-      P::load(st.w, src, start, k);
+  struct Step {
+    typename P::Block w;
+    typename P::Rows r;
+  };
+  // A step by its segment and its k; a wave takes every eighth.
+  struct Place {
+    int seg, k;
+  };
+  auto next = [&](Place p) {
+    p.k += kWaves;
+    while (p.k >= KT) {
+      p.k -= KT;
+      ++p.seg;
+    }
+    return p;
+  };
+  const int segments = __builtin_amdgcn_readfirstlane(s.segments);
+  auto load = [&](Step& st, Place p) {
+    const int length = buffer_length(p.seg, segments);
+    const int seg = min(p.seg, kMaxSegments - 1);
+    const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
+    const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
+    const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
+    const auto src = P::source(a.w2, e, a.hidden, a.inter, lane);
+    P::load(st.w, src, start, p.k, length);
+    const buffer h = make_buffer(a.h, length);
+    P::load_rows(st.r, h,
+                 (uint32_t)(pair + min(lane & 15, n - 1)) * (uint32_t)a.inter * 2 +
+                     P::row_lane(lane),
+                 p.k);
+  };
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  Step st[P::DEPTH];
+  Place now{0, wave - kWaves}, ahead;
+  now = next(now);
+  ahead = now;
 #pragma unroll
-      for (int j = 0; j < MT; ++j)
-        P::load_rows(st.r[j], h,
-                     (uint32_t)(pair + min(j * 16 + (lane & 15), n - 1)) * (uint32_t)a.inter * 2 +
-                         P::row_lane(lane),
-                     k);
-    };
-    f32x4 acc[MT];
+  for (int d = 0; d < P::DEPTH; ++d) {
+    load(st[d], ahead);
+    ahead = next(ahead);
+  }
+  while (now.seg < segments) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Step st[P::DEPTH];
+    for (int d = 0; d < P::DEPTH; ++d) {
+      P::multiply(acc, st[d].r, st[d].w);
+      __builtin_amdgcn_sched_barrier(0);
+      load(st[d], ahead);
+      ahead = next(ahead);
+      const Place then = next(now);
+      if (then.seg != now.seg) {
+        const int pair = s.seg_pair[now.seg], n = s.seg_pairs[now.seg];
 #pragma unroll
-    for (int d = 0; d < P::DEPTH; ++d) load(st[d], min(s0 + d, s1 - 1));
-    for (int at = s0; at < s1;) {
-#pragma unroll
-      for (int d = 0; d < P::DEPTH; ++d) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j) P::multiply(acc[j], st[d].r[j], st[d].w);
-        load(st[d], min(at + P::DEPTH, s1 - 1));
-        ++at;
-        if (at % KT == 0 || at >= s1) {
-          const int seg = (at - 1) / KT, pair = s.seg_pair[seg], n = s.seg_pairs[seg];
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = j * 16 + (lane >> 4) * 4 + i;
-              if (r < n) s_out[wave][s.token[pair + r]][lane & 15] += s.weight[pair + r] * acc[j][i];
-            }
-            acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int r = (lane >> 4) * 4 + i;
+          if (r < n) s_out[wave][s.token[pair + r]][lane & 15] += s.weight[pair + r] * acc[i];
         }
-        if (at >= s1) break;
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
       }
+      now = then;
+      if (now.seg >= segments) break;
     }
   }
   __syncthreads();
@@ -461,26 +496,23 @@ __global__ __launch_bounds__(kThreads, kPerSimd<MT>) void moe_down_kernel(MoeArg
   }
 }
 
-template <class P, int MT>
+template <class P>
 void launch_up(const MoeArgs& a, int num_cus, hipStream_t st) {
-  // at most one segment a pair, and one an expert and every 16 MT pairs
+  // at most one segment a pair, and one an expert and every 32 pairs
   const int64_t picks = (int64_t)a.tokens * a.top_k;
-  const int64_t segments = std::min<int64_t>(picks, a.n_experts + picks / (16 * MT));
-  const int64_t grid = std::min<int64_t>(segments * (a.inter / 16), kPerSimd<MT> / 2 * (int64_t)num_cus);
-  hipLaunchKernelGGL((moe_up_kernel<P, MT>), dim3((int)grid), dim3(kThreads), 0, st, a);
+  const int64_t segments = std::min<int64_t>(picks, a.n_experts + picks / 32);
+  const int64_t grid = std::min<int64_t>(segments * (a.inter / 16), 2 * (int64_t)num_cus);
+  hipLaunchKernelGGL((moe_up_kernel<P>), dim3((int)grid), dim3(kThreads), 0, st, a);
 }
 
-template <class P, int MT>
+template <class P>
 void launch_down(const MoeArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((moe_down_kernel<P, MT>), dim3(a.hidden / 16), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((moe_down_kernel<P>), dim3(a.hidden / 16), dim3(kThreads), 0, st, a);
 }
 
 template <class P>
 void launch_product(const MoeArgs& a, bool up, int num_cus, hipStream_t st) {
-  if (a.tokens <= 16)
-    up ? launch_up<P, 1>(a, num_cus, st) : launch_down<P, 1>(a, st);
-  else
-    up ? launch_up<P, 2>(a, num_cus, st) : launch_down<P, 2>(a, st);
+  up ? launch_up<P>(a, num_cus, st) : launch_down<P>(a, st);
 }
 
 template <int CODES, int GROUP>
@@ -496,10 +528,8 @@ hipError_t launch_product_of(const MoeArgs& a, const MoeWeights& w, bool up, int
   if (w.group == 0) {
     if (!a.fp8)
       launch_product<Bf16>(a, up, num_cus, st);
-    else if (up)
-      a.tokens <= 16 ? launch_up<Fp8Up, 1>(a, num_cus, st) : launch_up<Fp8Up, 2>(a, num_cus, st);
     else
-      a.tokens <= 16 ? launch_down<Fp8Down, 1>(a, st) : launch_down<Fp8Down, 2>(a, st);
+      up ? launch_up<Fp8Up>(a, num_cus, st) : launch_down<Fp8Down>(a, st);
     return hipGetLastError();
   }
   switch (w.codes * 1000 + w.group) {

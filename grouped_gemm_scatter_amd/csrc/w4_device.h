@@ -67,6 +67,18 @@ typedef __amdgpu_buffer_rsrc_t buffer;
 __device__ __forceinline__ buffer make_buffer(const void* p) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)0xffffffff, 0x00020000);
 }
+// The same for step `at` of `end` (wave-uniform) where at < end, else a buffer that is empty:
+// its loads give zeros and read nothing.  The length is the sign of a difference that the
+// compiler does not see through: of a comparison it makes a vector register and a loop over
+// the lanes around every load.
+__device__ __forceinline__ int buffer_length(int at, int end) {
+  int d = __builtin_amdgcn_readfirstlane(at - end);
+  asm("" : "+s"(d));
+  return d >> 31;
+}
+__device__ __forceinline__ buffer make_buffer(const void* p, int length) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, length, 0x00020000);
+}
 constexpr int kNontemporal = 2;
 __device__ __forceinline__ u32x4 buffer_load16(buffer b, uint32_t voff, uint32_t soff) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, 0));
