@@ -33,7 +33,13 @@ struct Table {
   int16_t pick[kMoePicks];             // local expert of a pick, or -1
   uint8_t token[kMoePicks];            // pair: its token
   int segments;
+  int rows;                            // 4, 8 or 16: what the expert of most pairs needs, at most 16
 };
+
+// Lanes below this one in a mask of lanes.
+__device__ __forceinline__ int lanes_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
 
 template <int ROWS, bool WEIGHTS>
 __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s) {
@@ -49,32 +55,35 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s) {
   }
   __syncthreads();
   if (tid < 64) {
-    // pairs and segments before each expert: scans over the lanes, 64 experts at a time
-    int pair = 0, seg = 0;
+    // pairs and segments before each expert, 64 experts at a time: counts by their bits, each
+    // a ballot (scans through LDS took a microsecond)
+    int pair = 0, seg = 0, rows = 4;
     for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
       const int e = e0 + tid;
       const int n = e < a.n_experts ? __popcll(s.tokens[e]) : 0;
-      const int m = (n + ROWS - 1) / ROWS;
-      int pn = n, pm = m;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int un = __shfl_up(pn, d), um = __shfl_up(pm, d);
-        if (tid >= d) {
-          pn += un;
-          pm += um;
-        }
+      int pairs_before = pair, segs_before = seg;
+      for (int bit = 0; a.tokens >> bit; ++bit) {
+        const uint64_t m = __ballot(n >> bit & 1);
+        pairs_before += lanes_below(m) << bit;
+        pair += __popcll(m) << bit;
       }
-      if (e < a.n_experts) s.first[e] = pair + pn - n;
-      for (int i = 0; i < m; ++i) {
-        const int at = seg + pm - m + i;
-        s.seg_expert[at] = e;
-        s.seg_pair[at] = pair + pn - n + i * ROWS;
-        s.seg_pairs[at] = min(n - i * ROWS, ROWS);
+      for (int i = 0; i * ROWS < a.tokens; ++i) {
+        const uint64_t m = __ballot(n > i * ROWS);
+        segs_before += lanes_below(m);
+        seg += __popcll(m);
       }
-      pair += __shfl(pn, 63);
-      seg += __shfl(pm, 63);
+      rows = __ballot(n > 8) ? 16 : __ballot(n > 4) ? max(rows, 8) : rows;
+      if (e < a.n_experts) s.first[e] = pairs_before;
+      for (int i = 0; i * ROWS < n; ++i) {
+        s.seg_expert[segs_before + i] = e;
+        s.seg_pair[segs_before + i] = pairs_before + i * ROWS;
+        s.seg_pairs[segs_before + i] = min(n - i * ROWS, ROWS);
+      }
     }
-    if (tid == 0) s.segments = seg;
+    if (tid == 0) {
+      s.segments = seg;
+      s.rows = rows;
+    }
   }
   __syncthreads();
   for (int p = tid; p < picks; p += kThreads) {
@@ -103,6 +112,60 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s) {
     __builtin_amdgcn_sched_barrier(0);   \
   } while (0)
 
+// ---- The first operand's rows, RB of them: 4, 8, 16 or 32 pairs of an expert.
+// An MFMA has 16 rows, and in a step's 128 k four of them follow (by quarters of k).
+// Fewer than 16 pairs would leave its lanes loading one row over and over, four loads a
+// step that cost as much of the memory path as the weights (a stream of 4-bit weights by
+// itself 6.1 TB/s, with these loads 4.4).  So lane L % 16 loads pair L % 16 % RB, of a quarter
+// of its own, and every quarter's MFMA takes the same register: its rows with another
+// quarter's values come out wrong and are left out, which 16 / RB accumulators, one a
+// quarter (or two quarters), make possible.
+template <int RB>
+struct RowsOf {
+  static constexpr int BLOCKS = RB > 16 ? RB / 16 : 1;
+  static constexpr int ACCS = RB < 16 ? 16 / RB : BLOCKS;
+};
+
+// The sums of all quarters of a lane's accumulators, RB rows in rows 0..RB - 1 of the result.
+__device__ __forceinline__ float add_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add_quarters(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// Rows of the results by lane: 4 (L / 16) + i.
+template <int RB>
+__device__ __forceinline__ f32x4 add_row_parts(const f32x4 (&acc)[RowsOf<RB>::ACCS], int lane) {
+  static_assert(RB <= 8, "rows in parts");
+  const int g = lane >> 4;
+  f32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (RB == 8) {
+      v[i] = add_halves(g < 2 ? acc[0][i] : acc[1][i]);
+    } else {
+      const float lo = g == 0 ? acc[0][i] : acc[1][i], hi = g == 2 ? acc[2][i] : acc[3][i];
+      v[i] = add_halves(add_quarters(g < 2 ? lo : hi));
+    }
+  }
+  return v;
+}
+
+// Rows in bf16, k = STRIDE q + 8 (L / 16) .. + 7 for quarter q (bytes: see at()).
+template <int RB>
+struct Bf16Rows {
+  u32x4 v[RB < 16 ? RB / 4 : 4 * RowsOf<RB>::BLOCKS];
+  // register of row block j and quarter q, and its accumulator
+  static constexpr int reg(int j, int q) { return RB < 16 ? q & (RB / 4 - 1) : 4 * j + q; }
+  static constexpr int acc(int j, int q) { return RB < 16 ? q / (RB / 4) : j; }
+  // quarter that the lane loads first
+  static __device__ __forceinline__ int quarter(int lane) {
+    return RB < 16 ? (lane & 15) / RB * (RB / 4) : 0;
+  }
+};
+
 // ---- The three kinds of weights.  Block: 16 rows of them, one step of 128 k, as a wave
 // holds it; Rows: the first operand's 16 rows of the same k.  Wave-uniform: where a
 // block's rows start (`row0`), the step.
@@ -115,7 +178,7 @@ struct Bf16 {
     uint32_t slice, lane;               // bytes between 64-k slices; of this lane's row
   };
   struct Block { u32x4 v[4]; };
-  struct Rows { u32x4 v[4]; };
+  template <int RB> using Rows = Bf16Rows<RB>;
   static __device__ __forceinline__ Source source(const MoeWeights& w, int e, int rows, int k,
                                                   int lane) {
     Source s;
@@ -136,19 +199,63 @@ struct Bf16 {
       in_order(b.v[q] = buffer_load16(w, s.lane + (q & 1) * 64,
                                       start + (2 * kt + (q >> 1)) * s.slice));
   }
-  // lane L: row L % 16 (at byte `row` of it), k = 32 q + 8 (L / 16) + 0..7
-  static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 16; }
-  static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) in_order(r.v[q] = buffer_load16(x, row + q * 64, kt * 256));
+  // byte of a lane's first values in its row's 256 of a step, and of the next quarter
+  static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
+    return (lane >> 4) * 16 + quarter * 64;
   }
-  static __device__ __forceinline__ void multiply(f32x4& acc, const Rows& r, const Block& b) {
+  template <int RB>
+  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, buffer x,
+                                                   const uint32_t (&row)[RowsOf<RB>::BLOCKS],
+                                                   int kt) {
+#pragma unroll
+    for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j)
+#pragma unroll
+      for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
+        in_order(r.v[4 * j + q] = buffer_load16(x, row[j] + q * 64, kt * 256));
+  }
+  template <int RB>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
+                                                  const Bf16Rows<RB>& r, const Block& b) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r.v[q]),
-                                                    __builtin_bit_cast(bf16x8, b.v[q]), acc, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j) {
+        f32x4& to = acc[r.acc(j, q)];
+        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r.v[r.reg(j, q)]),
+                                                     __builtin_bit_cast(bf16x8, b.v[q]), to, 0, 0, 0);
+      }
   }
 };
+
+// One step of weights whose scale holds for QPS quarters: w(q) the values of quarter q,
+// scale(q) its scale.
+template <int RB, int QPS, class W, class S>
+__device__ __forceinline__ void scaled_multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
+                                                const Bf16Rows<RB>& r, W w, S scale) {
+  constexpr int BLOCKS = RowsOf<RB>::BLOCKS;
+  // quarters of one sum: of one scale and one accumulator
+  constexpr int RUN = RB < 16 && RB / 4 < QPS ? RB / 4 : QPS;
+#pragma unroll
+  for (int q0 = 0; q0 < 4; q0 += RUN) {
+    f32x4 part[BLOCKS] = {};
+#pragma unroll
+    for (int q = q0; q < q0 + RUN; ++q) {
+      const bf16x8 wq = w(q);
+#pragma unroll
+      for (int j = 0; j < BLOCKS; ++j)
+        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, r.v[r.reg(j, q)]), wq, part[j], 0, 0, 0);
+    }
+    const float sc = scale(q0);
+#pragma unroll
+    for (int j = 0; j < BLOCKS; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x4& to = acc[r.acc(j, q0)];
+        to[i] = __builtin_fmaf(sc, part[j][i], to[i]);
+      }
+  }
+}
 
 // e4m3fn codes with a scale for 128 x 128 of them.  A lane's 16 bytes are two operands of 8
 // consecutive k, so MFMA 2 i + j takes k = 64 i + 16 (L / 16) + 8 j + 0..7 of both sides.
@@ -190,40 +297,73 @@ struct Fp8 {
 struct Fp8Up : Fp8 {
   static constexpr int DEPTH = 3, DEPTH2 = 2;
   static constexpr bool PAIR_A_LANE = true;
+  // a row's 128 bytes of a step are two halves of k; with 8 rows a lane loads one of them
+  template <int RB>
   struct Rows {
-    u32x4 v[2];
-    uint32_t s;
+    static_assert(RB >= 8, "halves of k");
+    u32x4 v[RB < 16 ? 1 : 2 * RowsOf<RB>::BLOCKS];
+    uint32_t s[RowsOf<RB>::BLOCKS];
+    static constexpr int reg(int j, int h) { return RB < 16 ? 0 : 2 * j + h; }
+    static constexpr int acc(int j, int h) { return RB < 16 ? h : j; }
+    static __device__ __forceinline__ int quarter(int lane) { return RB < 16 ? (lane & 15) / 8 : 0; }
   };
-  static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 16; }
-  static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) in_order(r.v[i] = buffer_load16(x, row + i * 64, kt * 128));
+  static __device__ __forceinline__ uint32_t at(int lane, int half) {
+    return (lane >> 4) * 16 + half * 64;
   }
-  static __device__ __forceinline__ void multiply(f32x4& acc, const Rows& r, const Block& b) {
-    f32x4 part = {0.f, 0.f, 0.f, 0.f};
+  template <int RB>
+  static __device__ __forceinline__ void load_rows(Rows<RB>& r, buffer x,
+                                                   const uint32_t (&row)[RowsOf<RB>::BLOCKS],
+                                                   int kt) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const long xr = (long)r.v[i][2 * j] | (long)((uint64_t)r.v[i][2 * j + 1] << 32);
-        const long wr = (long)b.v[i][2 * j] | (long)((uint64_t)b.v[i][2 * j + 1] << 32);
-        part = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(wr, xr, part, 0, 0, 0);
-      }
-    const float sc = __builtin_bit_cast(float, r.s) * __builtin_bit_cast(float, b.s);
+      for (int h = 0; h < (RB < 16 ? 1 : 2); ++h)
+        in_order(r.v[2 * j + h] = buffer_load16(x, row[j] + h * 64, kt * 128));
+  }
+  template <int RB>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
+                                                  const Rows<RB>& r, const Block& b) {
+    const float ws = __builtin_bit_cast(float, b.s);
+    constexpr int PARTS = RB < 16 ? 2 : 1;           // accumulators a step's halves go to
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(part[i], sc, acc[i]);
+    for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j) {
+      const float sc = __builtin_bit_cast(float, r.s[j]) * ws;
+      f32x4 part[PARTS] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const u32x4 x = r.v[r.reg(j, h)], w = b.v[h];
+          const long xr = (long)x[2 * o] | (long)((uint64_t)x[2 * o + 1] << 32);
+          const long wr = (long)w[2 * o] | (long)((uint64_t)w[2 * o + 1] << 32);
+          f32x4& to = part[PARTS == 2 ? h : 0];
+          to = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(wr, xr, to, 0, 0, 0);
+        }
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f32x4& to = acc[r.acc(j, h)];
+          to[i] = __builtin_fmaf(part[h][i], sc, to[i]);
+        }
+    }
   }
 };
 
 // Rows in bf16: the down-projection, the codes converted (exactly).
 struct Fp8Down : Fp8 {
   static constexpr int DEPTH = 3;
-  struct Rows { u32x4 v[4]; };
-  static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 32; }
-  static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
+  template <int RB> using Rows = Bf16Rows<RB>;
+  static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
+    return (lane >> 4) * 32 + (quarter >> 1) * 128 + (quarter & 1) * 16;
+  }
+  template <int RB>
+  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, buffer x,
+                                                   const uint32_t (&row)[RowsOf<RB>::BLOCKS],
+                                                   int kt) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      in_order(r.v[q] = buffer_load16(x, row + (q >> 1) * 128 + (q & 1) * 16, kt * 256));
+    for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
+      in_order(r.v[q] = buffer_load16(x, row[0] + (q >> 1) * 128 + (q & 1) * 16, kt * 256));
   }
   static __device__ __forceinline__ bf16x8 values(uint32_t lo, uint32_t hi) {
     const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, 0);
@@ -232,20 +372,20 @@ struct Fp8Down : Fp8 {
     const bf16x2 s = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, 1);
     return bf16x8{p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
   }
-  static __device__ __forceinline__ void multiply(f32x4& acc, const Rows& r, const Block& b) {
-    f32x4 part = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          __builtin_bit_cast(bf16x8, r.v[q]),
-          values(b.v[q >> 1][2 * (q & 1)], b.v[q >> 1][2 * (q & 1) + 1]), part, 0, 0, 0);
+  template <int RB>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
+                                                  const Bf16Rows<RB>& r, const Block& b) {
     const float ws = __builtin_bit_cast(float, b.s);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(part[i], ws, acc[i]);
+    scaled_multiply<RB, 4>(
+        acc, r, [&](int q) { return values(b.v[q >> 1][2 * (q & 1)], b.v[q >> 1][2 * (q & 1) + 1]); },
+        [&](int) { return ws; });
   }
 };
 
-// Packed 4-bit codes: 16 rows x 128 k are one run of 1 KB.
+// Packed 4-bit codes: 16 rows x 128 k are one run of 1 KB.  A wave's load is whole lines
+// that no other takes, so it goes past the caches' replacement (6.7 TB/s against 6.1; where a
+// line is two loads of 64 bytes a row, as with the other weights, it is the other way
+// around, 4.3 and 5.5).
 template <class F>
 struct W4 {
   static constexpr int DEPTH = 3, DEPTH2 = 1;
@@ -260,7 +400,7 @@ struct W4 {
     u32x4 v;
     typename F::word s;
   };
-  struct Rows { u32x4 v[4]; };
+  template <int RB> using Rows = Bf16Rows<RB>;
   static __device__ __forceinline__ Source source(const MoeWeights& w, int e, int rows, int k,
                                                   int lane) {
     Source s;
@@ -278,67 +418,63 @@ struct W4 {
   static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int kt,
                                               int length) {
     const uint32_t run = start * s.kt + kt;
-    in_order(b.v = buffer_load16(make_buffer(s.w, length), s.lane, run * 1024));
+    in_order(b.v = buffer_load16_nt(make_buffer(s.w, length), s.lane, run * 1024));
     in_order(buffer_load_to(b.s, make_buffer(s.s, length), s.lane_s, run * SB));
   }
-  static __device__ __forceinline__ uint32_t row_lane(int lane) { return (lane >> 4) * 16; }
-  static __device__ __forceinline__ void load_rows(Rows& r, buffer x, uint32_t row, int kt) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) in_order(r.v[q] = buffer_load16(x, row + q * 64, kt * 256));
+  static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
+    return Bf16::at(lane, quarter);
   }
-  static __device__ __forceinline__ void multiply(f32x4& acc, const Rows& r, const Block& b) {
-    constexpr int SPT = 128 / F::GROUP, QPS = 4 / SPT;
-#pragma unroll
-    for (int s = 0; s < SPT; ++s) {
-      f32x4 part = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int q = 0; q < QPS; ++q)
-        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, r.v[s * QPS + q]), decode8<F::CODES>(b.v[s * QPS + q]), part,
-            0, 0, 0);
-      const float sc = F::scale((uint16_t)(b.s >> (16 * s)));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(sc, part[i], acc[i]);
-    }
+  template <int RB>
+  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, buffer x,
+                                                   const uint32_t (&row)[RowsOf<RB>::BLOCKS],
+                                                   int kt) {
+    Bf16::load_rows<RB>(r, x, row, kt);
+  }
+  template <int RB>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
+                                                  const Bf16Rows<RB>& r, const Block& b) {
+    constexpr int QPS = F::GROUP / 32;
+    scaled_multiply<RB, QPS>(
+        acc, r, [&](int q) { return decode8<F::CODES>(b.v[q]); },
+        [&](int q) { return F::scale((uint16_t)(b.s >> (16 * (q / QPS)))); });
   }
 };
 
 // ---- Up-projection and SwiGLU.  An item is a segment and 16 outputs: 16 gate rows and the 16
 // up rows of W1, whose K the waves split.
-template <class P, int MT, int DEPTH>
+template <class P, int RB, int DEPTH>
 __device__ __forceinline__ void up_item(const MoeArgs& a, const Table& s, f32x4 (*s_part)[2][2][64],
                                         int e, int b, int pair, int n, int wave, int lane) {
+  constexpr int BLOCKS = RowsOf<RB>::BLOCKS, ACCS = RowsOf<RB>::ACCS;
+  typedef typename P::template Rows<RB> Rows;
   const int KT = a.hidden / 128;
   const auto src = P::source(a.w1, e, 2 * a.inter, a.hidden, lane);
   const uint32_t gate = P::start(a.w1, b * 16, a.hidden);
   const uint32_t up = P::start(a.w1, a.inter + b * 16, a.hidden);
   // rows past the segment's last repeat it; their results are not stored
-  uint32_t row[MT], scale_at[MT];
+  uint32_t row[BLOCKS], scale_at[BLOCKS];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int t = s.token[pair + min(j * 16 + (lane & 15), n - 1)];
-    row[j] = (uint32_t)t * (uint32_t)a.hidden * (P::PAIR_A_LANE ? 1 : 2) + P::row_lane(lane);
+  for (int j = 0; j < BLOCKS; ++j) {
+    const int t = s.token[pair + min(j * 16 + (lane & 15) % RB, n - 1)];
+    row[j] = (uint32_t)t * (uint32_t)a.hidden * (P::PAIR_A_LANE ? 1 : 2) +
+             P::at(lane, Rows::quarter(lane));
     scale_at[j] = t * KT * 4;
   }
   struct Step {
     typename P::Block g, u;
-    typename P::Rows r[MT];
+    Rows r;
   };
   auto load = [&](Step& st, int k) {
     const int length = buffer_length(k, KT);
     P::load(st.g, src, gate, k, length);
     P::load(st.u, src, up, k, length);
-    const buffer x = make_buffer(a.x, length);
+    P::template load_rows<RB>(st.r, make_buffer(a.x, length), row, k);
+    if constexpr (P::PAIR_A_LANE)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      P::load_rows(st.r[j], x, row[j], k);
-      if constexpr (P::PAIR_A_LANE)
-        in_order(buffer_load_to(st.r[j].s, make_buffer(a.x_scale, length), scale_at[j], k * 4));
-    }
+      for (int j = 0; j < BLOCKS; ++j)
+        in_order(buffer_load_to(st.r.s[j], make_buffer(a.x_scale, length), scale_at[j], k * 4));
   };
-  f32x4 ag[MT], au[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) ag[j] = au[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 ag[ACCS] = {}, au[ACCS] = {};
   // A wave takes every eighth step, so that the workgroup's reads of a row are one run.
   // Loads ahead are unconditional, past the end of an empty buffer: with one under a
   // condition the compiler would wait for all that are in flight.
@@ -348,21 +484,34 @@ __device__ __forceinline__ void up_item(const MoeArgs& a, const Table& s, f32x4 
   for (int k = wave; k < KT;) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        P::multiply(ag[j], st[d].r[j], st[d].g);
-        P::multiply(au[j], st[d].r[j], st[d].u);
-      }
+      P::template multiply<RB>(ag, st[d].r, st[d].g);
+      P::template multiply<RB>(au, st[d].r, st[d].u);
       __builtin_amdgcn_sched_barrier(0);
       load(st[d], k + DEPTH * kWaves);
       k += kWaves;
       if (k >= KT) break;
     }
   }
+  if constexpr (RB >= 16) {
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    s_part[wave][0][j][lane] = ag[j];
-    s_part[wave][1][j][lane] = au[j];
+    for (int j = 0; j < BLOCKS; ++j) {
+      s_part[wave][0][j][lane] = ag[j];
+      s_part[wave][1][j][lane] = au[j];
+    }
+  } else if constexpr (P::PAIR_A_LANE) {
+    // a pair's two halves of k lie eight lanes apart
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ag[0][i] = (lane & 8) ? ag[1][i] : ag[0][i];
+      au[0][i] = (lane & 8) ? au[1][i] : au[0][i];
+      ag[0][i] += __shfl_xor(ag[0][i], 8);
+      au[0][i] += __shfl_xor(au[0][i], 8);
+    }
+    s_part[wave][0][0][lane] = ag[0];
+    s_part[wave][1][0][lane] = au[0];
+  } else {
+    s_part[wave][0][0][lane] = add_row_parts<RB>(ag, lane);
+    s_part[wave][1][0][lane] = add_row_parts<RB>(au, lane);
   }
 }
 
@@ -380,10 +529,14 @@ __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
     const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
     const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
     const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
-    if (n <= 16)
-      up_item<P, 1, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
+    if (!P::PAIR_A_LANE && n <= 4)
+      up_item<P, P::PAIR_A_LANE ? 8 : 4, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
+    else if (n <= 8)
+      up_item<P, 8, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
+    else if (n <= 16)
+      up_item<P, 16, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
     else
-      up_item<P, 2, P::DEPTH2>(a, s, s_part, e, b, pair, n, wave, lane);
+      up_item<P, 32, P::DEPTH2>(a, s, s_part, e, b, pair, n, wave, lane);
     __syncthreads();
     // one value a thread: a pair's row and an output
     {
@@ -408,8 +561,85 @@ __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
 // ---- Down-projection and the weighted sum.  A workgroup takes 16 columns of the output; the
 // steps of all segments are one run that the waves split evenly.  A wave adds what it has of
 // a segment, times the pairs' weights, to its own sums of the tokens in LDS.
-// The segments are of 16 pairs: an expert's weights are read again for its next 16, by the
-// same workgroup and at once.
+// The segments are of at most 16 pairs: an expert's weights are read again for its next 16,
+// by the same workgroup and at once.  RB: the rows that the largest segment needs.
+template <class P, int RB>
+__device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, float (*s_out)[16],
+                                           int b, int wave, int lane) {
+  typedef typename P::template Rows<RB> Rows;
+  const int KT = a.inter / 128;
+  const int segments = __builtin_amdgcn_readfirstlane(s.segments);
+  const uint32_t start = P::start(a.w2, b * 16, a.inter);
+  struct Step {
+    typename P::Block w;
+    Rows r;
+  };
+  // Where a wave's loads are: a segment and a step of its k; a wave takes every eighth
+  // step of all.  What belongs to the segment is looked up when it is entered.
+  struct Place {
+    int seg, k;
+    decltype(P::source(a.w2, 0, 0, 0, 0)) src;
+    uint32_t row[1];
+  };
+  auto enter = [&](Place& p) {
+    const int seg = min(p.seg, segments - 1);
+    const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
+    const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
+    const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
+    p.src = P::source(a.w2, e, a.hidden, a.inter, lane);
+    p.row[0] = (uint32_t)(pair + min((lane & 15) % RB, n - 1)) * (uint32_t)a.inter * 2 +
+               P::at(lane, Rows::quarter(lane));
+  };
+  // moves on by eight steps; true if that left the segment
+  const int whole = kWaves / KT, rest = kWaves % KT;
+  auto move = [&](int& seg, int& k) {
+    const int was = seg, over = k + rest >= KT;
+    seg += whole + over;
+    k += rest - over * KT;
+    return seg != was;
+  };
+  auto load = [&](Step& st, Place& p) {
+    const int length = buffer_length(p.seg, segments);
+    P::load(st.w, p.src, start, p.k, length);
+    P::template load_rows<RB>(st.r, make_buffer(a.h, length), p.row, p.k);
+    if (move(p.seg, p.k)) enter(p);
+  };
+  f32x4 acc[RowsOf<RB>::ACCS] = {};
+  Step st[P::DEPTH];
+  int seg = wave / KT, k = wave % KT;
+  Place ahead;
+  ahead.seg = seg;
+  ahead.k = k;
+  enter(ahead);
+#pragma unroll
+  for (int d = 0; d < P::DEPTH; ++d) load(st[d], ahead);
+  while (seg < segments) {
+#pragma unroll
+    for (int d = 0; d < P::DEPTH; ++d) {
+      P::template multiply<RB>(acc, st[d].r, st[d].w);
+      __builtin_amdgcn_sched_barrier(0);
+      load(st[d], ahead);
+      const int was = seg;
+      if (move(seg, k)) {
+        const int pair = s.seg_pair[was], n = s.seg_pairs[was];
+        f32x4 v;
+        if constexpr (RB < 16)
+          v = add_row_parts<RB>(acc, lane);
+        else
+          v = acc[0];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (lane >> 4) * 4 + i;
+          if (r < n) s_out[s.token[pair + r]][lane & 15] += s.weight[pair + r] * v[i];
+        }
+#pragma unroll
+        for (int j = 0; j < RowsOf<RB>::ACCS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      if (seg >= segments) break;
+    }
+  }
+}
+
 template <class P>
 __global__ __launch_bounds__(kThreads, 4) void moe_down_kernel(MoeArgs a) {
   __shared__ Table s;
@@ -418,70 +648,14 @@ __global__ __launch_bounds__(kThreads, 4) void moe_down_kernel(MoeArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = lane; i < a.tokens * 16; i += 64) s_out[wave][i >> 4][i & 15] = 0.f;
   build_table<16, true>(a, s);
-  const int KT = a.inter / 128;
-  const int b = blockIdx.x;
-  const uint32_t start = P::start(a.w2, b * 16, a.inter);
-  struct Step {
-    typename P::Block w;
-    typename P::Rows r;
-  };
-  // A step by its segment and its k; a wave takes every eighth.
-  struct Place {
-    int seg, k;
-  };
-  auto next = [&](Place p) {
-    p.k += kWaves;
-    while (p.k >= KT) {
-      p.k -= KT;
-      ++p.seg;
-    }
-    return p;
-  };
-  const int segments = __builtin_amdgcn_readfirstlane(s.segments);
-  auto load = [&](Step& st, Place p) {
-    const int length = buffer_length(p.seg, segments);
-    const int seg = min(p.seg, kMaxSegments - 1);
-    const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
-    const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
-    const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
-    const auto src = P::source(a.w2, e, a.hidden, a.inter, lane);
-    P::load(st.w, src, start, p.k, length);
-    const buffer h = make_buffer(a.h, length);
-    P::load_rows(st.r, h,
-                 (uint32_t)(pair + min(lane & 15, n - 1)) * (uint32_t)a.inter * 2 +
-                     P::row_lane(lane),
-                 p.k);
-  };
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  Step st[P::DEPTH];
-  Place now{0, wave - kWaves}, ahead;
-  now = next(now);
-  ahead = now;
-#pragma unroll
-  for (int d = 0; d < P::DEPTH; ++d) {
-    load(st[d], ahead);
-    ahead = next(ahead);
-  }
-  while (now.seg < segments) {
-#pragma unroll
-    for (int d = 0; d < P::DEPTH; ++d) {
-      P::multiply(acc, st[d].r, st[d].w);
-      __builtin_amdgcn_sched_barrier(0);
-      load(st[d], ahead);
-      ahead = next(ahead);
-      const Place then = next(now);
-      if (then.seg != now.seg) {
-        const int pair = s.seg_pair[now.seg], n = s.seg_pairs[now.seg];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = (lane >> 4) * 4 + i;
-          if (r < n) s_out[wave][s.token[pair + r]][lane & 15] += s.weight[pair + r] * acc[i];
-        }
-        acc = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-      now = then;
-      if (now.seg >= segments) break;
-    }
+  const int b = blockIdx.x, rows = __builtin_amdgcn_readfirstlane(s.rows);
+  if (__builtin_amdgcn_readfirstlane(s.segments) > 0) {
+    if (rows == 4)
+      down_steps<P, 4>(a, s, s_out[wave], b, wave, lane);
+    else if (rows == 8)
+      down_steps<P, 8>(a, s, s_out[wave], b, wave, lane);
+    else
+      down_steps<P, 16>(a, s, s_out[wave], b, wave, lane);
   }
   __syncthreads();
   for (int i = tid; i < a.tokens * 8; i += kThreads) {
