@@ -29,11 +29,10 @@ struct Table {
   uint64_t tokens[kMaxLocalExperts];   // expert e: its tokens
   int first[kMaxLocalExperts];         // its first pair
   int seg_expert[kMaxSegments], seg_pair[kMaxSegments], seg_pairs[kMaxSegments];
-  float weight[kMoePicks];             // pair: the sum of the token's weights of this expert
   int16_t pick[kMoePicks];             // local expert of a pick, or -1
   uint8_t token[kMoePicks];            // pair: its token
   int segments;
-  int rows;                            // 4, 8 or 16: what the expert of most pairs needs, at most 16
+  int rows;                            // 4, 8, 16 or 32: what the largest segment needs
 };
 
 // Lanes below this one in a mask of lanes.
@@ -41,13 +40,19 @@ __device__ __forceinline__ int lanes_below(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
 }
 
-template <int ROWS, bool WEIGHTS>
-__device__ __forceinline__ void build_table(const MoeArgs& a, Table& s) {
+// The picks' weights, and by pairs: the sum of the token's weights of this expert.
+struct Weights {
+  float pick[kMoePicks], pair[kMoePicks];
+};
+
+template <int ROWS>
+__device__ __forceinline__ void build_table(const MoeArgs& a, Table& s, Weights* w = nullptr) {
   const int tid = threadIdx.x, picks = a.tokens * a.top_k;
   for (int e = tid; e < a.n_experts; e += kThreads) s.tokens[e] = 0;
   __syncthreads();
   for (int p = tid; p < picks; p += kThreads) {
     const int e = a.topk_ids[p] - a.expert_lo;
+    if (w) w->pick[p] = a.topk_w[p];
     const bool local = e >= 0 && e < a.n_experts;
     s.pick[p] = (int16_t)(local ? e : -1);
     if (local)
@@ -72,7 +77,9 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s) {
         segs_before += lanes_below(m);
         seg += __popcll(m);
       }
-      rows = __ballot(n > 8) ? 16 : __ballot(n > 4) ? max(rows, 8) : rows;
+      if (ROWS > 16 && __ballot(n > 16)) rows = 32;
+      if (__ballot(n > 8)) rows = max(rows, 16);
+      if (__ballot(n > 4)) rows = max(rows, 8);
       if (e < a.n_experts) s.first[e] = pairs_before;
       for (int i = 0; i * ROWS < n; ++i) {
         s.seg_expert[segs_before + i] = e;
@@ -94,11 +101,11 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s) {
     if (again) continue;
     const int pair = s.first[e] + __popcll(s.tokens[e] & ((1ull << t) - 1));
     s.token[pair] = (uint8_t)t;
-    if constexpr (WEIGHTS) {
-      float w = a.topk_w[p];
+    if (w) {
+      float sum = w->pick[p];
       for (int q = p + 1; q < (t + 1) * a.top_k; ++q)
-        if (s.pick[q] == e) w += a.topk_w[q];
-      s.weight[pair] = w;
+        if (s.pick[q] == e) sum += w->pick[q];
+      w->pair[pair] = sum;
     }
   }
   __syncthreads();
@@ -171,7 +178,8 @@ struct Bf16Rows {
 // block's rows start (`row0`), the step.
 
 struct Bf16 {
-  static constexpr int DEPTH = 2, DEPTH2 = 1;     // steps in flight, with one and two row blocks
+  // steps in flight, as many as 128 registers hold
+  static constexpr int depth(int rows) { return rows > 16 ? 1 : 2; }
   static constexpr bool PAIR_A_LANE = false;
   struct Source {
     const uint8_t* w;
@@ -295,7 +303,7 @@ struct Fp8 {
 // Rows of codes with a scale for 128 of them: the up-projection.  The weights are the
 // first operand, so that a lane's results are of one pair, whose scale it has loaded.
 struct Fp8Up : Fp8 {
-  static constexpr int DEPTH = 3, DEPTH2 = 2;
+  static constexpr int depth(int rows) { return rows > 16 ? 2 : 3; }
   static constexpr bool PAIR_A_LANE = true;
   // a row's 128 bytes of a step are two halves of k; with 8 rows a lane loads one of them
   template <int RB>
@@ -352,7 +360,7 @@ struct Fp8Up : Fp8 {
 
 // Rows in bf16: the down-projection, the codes converted (exactly).
 struct Fp8Down : Fp8 {
-  static constexpr int DEPTH = 3;
+  static constexpr int depth(int) { return 3; }
   template <int RB> using Rows = Bf16Rows<RB>;
   static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
     return (lane >> 4) * 32 + (quarter >> 1) * 128 + (quarter & 1) * 16;
@@ -388,7 +396,7 @@ struct Fp8Down : Fp8 {
 // around, 4.3 and 5.5).
 template <class F>
 struct W4 {
-  static constexpr int DEPTH = 3, DEPTH2 = 1;
+  static constexpr int depth(int rows) { return rows > 16 ? 1 : rows > 8 || F::GROUP == 32 ? 2 : 3; }
   static constexpr bool PAIR_A_LANE = false;
   static constexpr uint32_t SB = 16 * (128 / F::GROUP) * 2;   // scale bytes of a run
   struct Source {
@@ -440,122 +448,160 @@ struct W4 {
   }
 };
 
+// Waits for this wave's LDS accesses, then for the workgroup; loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);                // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // ---- Up-projection and SwiGLU.  An item is a segment and 16 outputs: 16 gate rows and the 16
-// up rows of W1, whose K the waves split.
-template <class P, int RB, int DEPTH>
-__device__ __forceinline__ void up_item(const MoeArgs& a, const Table& s, f32x4 (*s_part)[2][2][64],
-                                        int e, int b, int pair, int n, int wave, int lane) {
-  constexpr int BLOCKS = RowsOf<RB>::BLOCKS, ACCS = RowsOf<RB>::ACCS;
+// up rows of W1, whose K the waves split: a wave takes every eighth step, so that the
+// workgroup's reads of a row are one run.  The loads of the next item's first steps are
+// on their way while an item's sums are joined.
+template <class P, int RB>
+__device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
+                                         f32x4 (*s_part)[kWaves][2][RowsOf<RB>::BLOCKS][64]) {
+  constexpr int BLOCKS = RowsOf<RB>::BLOCKS, ACCS = RowsOf<RB>::ACCS, BUFS = 2 / BLOCKS;
+  constexpr int DEPTH = P::depth(RB);
   typedef typename P::template Rows<RB> Rows;
-  const int KT = a.hidden / 128;
-  const auto src = P::source(a.w1, e, 2 * a.inter, a.hidden, lane);
-  const uint32_t gate = P::start(a.w1, b * 16, a.hidden);
-  const uint32_t up = P::start(a.w1, a.inter + b * 16, a.hidden);
-  // rows past the segment's last repeat it; their results are not stored
-  uint32_t row[BLOCKS], scale_at[BLOCKS];
-#pragma unroll
-  for (int j = 0; j < BLOCKS; ++j) {
-    const int t = s.token[pair + min(j * 16 + (lane & 15) % RB, n - 1)];
-    row[j] = (uint32_t)t * (uint32_t)a.hidden * (P::PAIR_A_LANE ? 1 : 2) +
-             P::at(lane, Rows::quarter(lane));
-    scale_at[j] = t * KT * 4;
-  }
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int KT = a.hidden / 128, per = a.inter / 16;
+  const int items = __builtin_amdgcn_readfirstlane(s.segments) * per;
   struct Step {
     typename P::Block g, u;
     Rows r;
   };
-  auto load = [&](Step& st, int k) {
-    const int length = buffer_length(k, KT);
-    P::load(st.g, src, gate, k, length);
-    P::load(st.u, src, up, k, length);
-    P::template load_rows<RB>(st.r, make_buffer(a.x, length), row, k);
+  struct Place {
+    int item, k;
+    decltype(P::source(a.w1, 0, 0, 0, 0)) src;
+    uint32_t gate, up, row[BLOCKS], scale_at[BLOCKS];
+  };
+  auto enter = [&](Place& p) {
+    const int item = min(p.item, items - 1), seg = item / per, b = item % per;
+    const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
+    const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
+    const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
+    p.src = P::source(a.w1, e, 2 * a.inter, a.hidden, lane);
+    p.gate = P::start(a.w1, b * 16, a.hidden);
+    p.up = P::start(a.w1, a.inter + b * 16, a.hidden);
+    // rows past the segment's last repeat it; their results are not stored
+#pragma unroll
+    for (int j = 0; j < BLOCKS; ++j) {
+      const int t = s.token[pair + min(j * 16 + (lane & 15) % RB, n - 1)];
+      p.row[j] = (uint32_t)t * (uint32_t)a.hidden * (P::PAIR_A_LANE ? 1 : 2) +
+                 P::at(lane, Rows::quarter(lane));
+      p.scale_at[j] = t * KT * 4;
+    }
+  };
+  // Loads ahead are unconditional, past the end of an empty buffer: with one under a
+  // condition the compiler would wait for all that are in flight.
+  auto load = [&](Step& st, Place& p) {
+    const int length = buffer_length(p.item, items) & buffer_length(p.k, KT);
+    P::load(st.g, p.src, p.gate, p.k, length);
+    P::load(st.u, p.src, p.up, p.k, length);
+    P::template load_rows<RB>(st.r, make_buffer(a.x, length), p.row, p.k);
     if constexpr (P::PAIR_A_LANE)
 #pragma unroll
       for (int j = 0; j < BLOCKS; ++j)
-        in_order(buffer_load_to(st.r.s[j], make_buffer(a.x_scale, length), scale_at[j], k * 4));
+        in_order(buffer_load_to(st.r.s[j], make_buffer(a.x_scale, length), p.scale_at[j], p.k * 4));
+    p.k += kWaves;
+    if (p.k >= KT) {
+      p.k = wave;
+      p.item += gridDim.x;
+      enter(p);
+    }
   };
+  int item = blockIdx.x, k = wave, buf = 0;
+  if (item >= items) return;
   f32x4 ag[ACCS] = {}, au[ACCS] = {};
-  // A wave takes every eighth step, so that the workgroup's reads of a row are one run.
-  // Loads ahead are unconditional, past the end of an empty buffer: with one under a
-  // condition the compiler would wait for all that are in flight.
+  Place ahead;
+  ahead.item = item;
+  ahead.k = k;
+  enter(ahead);
   Step st[DEPTH];
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) load(st[d], wave + d * kWaves);
-  for (int k = wave; k < KT;) {
+  for (int d = 0; d < DEPTH; ++d) load(st[d], ahead);
+  while (item < items) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
+      // (a wave without a step of its own multiplies the empty buffer's zeros)
       P::template multiply<RB>(ag, st[d].r, st[d].g);
       P::template multiply<RB>(au, st[d].r, st[d].u);
       __builtin_amdgcn_sched_barrier(0);
-      load(st[d], k + DEPTH * kWaves);
+      load(st[d], ahead);
       k += kWaves;
-      if (k >= KT) break;
-    }
-  }
-  if constexpr (RB >= 16) {
+      if (k >= KT) {
+        auto& part = s_part[buf];
+        if constexpr (RB >= 16) {
 #pragma unroll
-    for (int j = 0; j < BLOCKS; ++j) {
-      s_part[wave][0][j][lane] = ag[j];
-      s_part[wave][1][j][lane] = au[j];
-    }
-  } else if constexpr (P::PAIR_A_LANE) {
-    // a pair's two halves of k lie eight lanes apart
+          for (int j = 0; j < BLOCKS; ++j) {
+            part[wave][0][j][lane] = ag[j];
+            part[wave][1][j][lane] = au[j];
+          }
+        } else if constexpr (P::PAIR_A_LANE) {
+          // a pair's two halves of k lie eight lanes apart
+          f32x4 g, u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ag[0][i] = (lane & 8) ? ag[1][i] : ag[0][i];
-      au[0][i] = (lane & 8) ? au[1][i] : au[0][i];
-      ag[0][i] += __shfl_xor(ag[0][i], 8);
-      au[0][i] += __shfl_xor(au[0][i], 8);
+          for (int i = 0; i < 4; ++i) {
+            g[i] = (lane & 8) ? ag[1][i] : ag[0][i];
+            u[i] = (lane & 8) ? au[1][i] : au[0][i];
+            g[i] += __shfl_xor(g[i], 8);
+            u[i] += __shfl_xor(u[i], 8);
+          }
+          part[wave][0][0][lane] = g;
+          part[wave][1][0][lane] = u;
+        } else {
+          part[wave][0][0][lane] = add_row_parts<RB>(ag, lane);
+          part[wave][1][0][lane] = add_row_parts<RB>(au, lane);
+        }
+#pragma unroll
+        for (int j = 0; j < ACCS; ++j) ag[j] = au[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        lds_barrier();
+        const int seg = item / per, b = item % per;
+        const int pair = s.seg_pair[seg], n = s.seg_pairs[seg];
+        // one value a thread: a pair's row and an output
+        const int j = tid >> 8, l = (tid >> 2) & 63, i = tid & 3;
+        const int r = j * 16 + (P::PAIR_A_LANE ? l & 15 : (l >> 4) * 4 + i);
+        const int c = P::PAIR_A_LANE ? (l >> 4) * 4 + i : l & 15;
+        if (j < BLOCKS && r < n) {
+          float g = 0.f, u = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            g += part[w][0][j][l][i];
+            u += part[w][1][j][l][i];
+          }
+          reinterpret_cast<__bf16*>(a.h)[(size_t)(pair + r) * a.inter + b * 16 + c] =
+              (__bf16)(g / (1.f + expf(-g)) * u);
+        }
+        // one barrier an item: the next one's sums go to the other buffer, if there is one
+        if constexpr (BUFS == 1) lds_barrier();
+        buf ^= BUFS - 1;
+        k = wave;
+        item += gridDim.x;
+      }
+      if (item >= items) break;
     }
-    s_part[wave][0][0][lane] = ag[0];
-    s_part[wave][1][0][lane] = au[0];
-  } else {
-    s_part[wave][0][0][lane] = add_row_parts<RB>(ag, lane);
-    s_part[wave][1][0][lane] = add_row_parts<RB>(au, lane);
   }
 }
 
 template <class P>
 __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
   __shared__ Table s;
-  __shared__ f32x4 s_part[kWaves][2][2][64];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  build_table<32, false>(a, s);
-  const int per = a.inter / 16;
-  const int items = __builtin_amdgcn_readfirstlane(s.segments) * per;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int seg = item / per, b = item % per;
-    const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
-    const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
-    const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
-    if (!P::PAIR_A_LANE && n <= 4)
-      up_item<P, P::PAIR_A_LANE ? 8 : 4, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
-    else if (n <= 8)
-      up_item<P, 8, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
-    else if (n <= 16)
-      up_item<P, 16, P::DEPTH>(a, s, s_part, e, b, pair, n, wave, lane);
-    else
-      up_item<P, 32, P::DEPTH2>(a, s, s_part, e, b, pair, n, wave, lane);
-    __syncthreads();
-    // one value a thread: a pair's row and an output
-    {
-      const int j = tid >> 8, l = (tid >> 2) & 63, i = tid & 3;
-      const int r = j * 16 + (P::PAIR_A_LANE ? l & 15 : (l >> 4) * 4 + i);
-      const int c = P::PAIR_A_LANE ? (l >> 4) * 4 + i : l & 15;
-      if (r < n) {
-        float g = 0.f, u = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          g += s_part[w][0][j][l][i];
-          u += s_part[w][1][j][l][i];
-        }
-        reinterpret_cast<__bf16*>(a.h)[(size_t)(pair + r) * a.inter + b * 16 + c] =
-            (__bf16)(g / (1.f + expf(-g)) * u);
-      }
-    }
-    __syncthreads();
-  }
+  __shared__ f32x4 s_part[1][kWaves][2][2][64];
+  build_table<32>(a, s);
+  const int rows = __builtin_amdgcn_readfirstlane(s.rows);
+  typedef f32x4 (*Narrow)[kWaves][2][1][64];
+  if (rows <= 8 && (P::PAIR_A_LANE || rows == 8))
+    up_items<P, 8>(a, s, reinterpret_cast<Narrow>(s_part));
+  else if (rows == 4)
+    up_items<P, P::PAIR_A_LANE ? 8 : 4>(a, s, reinterpret_cast<Narrow>(s_part));
+  else if (rows == 16)
+    up_items<P, 16>(a, s, reinterpret_cast<Narrow>(s_part));
+  else
+    up_items<P, 32>(a, s, s_part);
 }
 
 // ---- Down-projection and the weighted sum.  A workgroup takes 16 columns of the output; the
@@ -564,10 +610,11 @@ __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
 // The segments are of at most 16 pairs: an expert's weights are read again for its next 16,
 // by the same workgroup and at once.  RB: the rows that the largest segment needs.
 template <class P, int RB>
-__device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, float (*s_out)[16],
-                                           int b, int wave, int lane) {
+__device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, const float* weight,
+                                           float (*s_out)[16], int b, int wave, int lane) {
   typedef typename P::template Rows<RB> Rows;
   const int KT = a.inter / 128;
+  constexpr int DEPTH = P::depth(RB);
   const int segments = __builtin_amdgcn_readfirstlane(s.segments);
   const uint32_t start = P::start(a.w2, b * 16, a.inter);
   struct Step {
@@ -605,17 +652,17 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, flo
     if (move(p.seg, p.k)) enter(p);
   };
   f32x4 acc[RowsOf<RB>::ACCS] = {};
-  Step st[P::DEPTH];
+  Step st[DEPTH];
   int seg = wave / KT, k = wave % KT;
   Place ahead;
   ahead.seg = seg;
   ahead.k = k;
   enter(ahead);
 #pragma unroll
-  for (int d = 0; d < P::DEPTH; ++d) load(st[d], ahead);
+  for (int d = 0; d < DEPTH; ++d) load(st[d], ahead);
   while (seg < segments) {
 #pragma unroll
-    for (int d = 0; d < P::DEPTH; ++d) {
+    for (int d = 0; d < DEPTH; ++d) {
       P::template multiply<RB>(acc, st[d].r, st[d].w);
       __builtin_amdgcn_sched_barrier(0);
       load(st[d], ahead);
@@ -630,7 +677,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, flo
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = (lane >> 4) * 4 + i;
-          if (r < n) s_out[s.token[pair + r]][lane & 15] += s.weight[pair + r] * v[i];
+          if (r < n) s_out[s.token[pair + r]][lane & 15] += weight[pair + r] * v[i];
         }
 #pragma unroll
         for (int j = 0; j < RowsOf<RB>::ACCS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -643,19 +690,20 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, flo
 template <class P>
 __global__ __launch_bounds__(kThreads, 4) void moe_down_kernel(MoeArgs a) {
   __shared__ Table s;
+  __shared__ Weights weights;
   __shared__ float s_out[kWaves][kMoeTokens][16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = lane; i < a.tokens * 16; i += 64) s_out[wave][i >> 4][i & 15] = 0.f;
-  build_table<16, true>(a, s);
+  build_table<16>(a, s, &weights);
   const int b = blockIdx.x, rows = __builtin_amdgcn_readfirstlane(s.rows);
   if (__builtin_amdgcn_readfirstlane(s.segments) > 0) {
     if (rows == 4)
-      down_steps<P, 4>(a, s, s_out[wave], b, wave, lane);
+      down_steps<P, 4>(a, s, weights.pair, s_out[wave], b, wave, lane);
     else if (rows == 8)
-      down_steps<P, 8>(a, s, s_out[wave], b, wave, lane);
+      down_steps<P, 8>(a, s, weights.pair, s_out[wave], b, wave, lane);
     else
-      down_steps<P, 16>(a, s, s_out[wave], b, wave, lane);
+      down_steps<P, 16>(a, s, weights.pair, s_out[wave], b, wave, lane);
   }
   __syncthreads();
   for (int i = tid; i < a.tokens * 8; i += kThreads) {
