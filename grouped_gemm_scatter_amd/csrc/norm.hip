@@ -5,9 +5,9 @@
 //   with r the stored sums and g, h the gradients of y and of the stored sums:
 //   dr = inv (g w - r inv^2 mean(g w r)) + h,   dw = sum over rows of g r inv
 //
-// Both are HBM streams.  A row is spread over `TPR` threads, a thread holding up to kHeld
-// chunks of 8 values in registers between the sum over the row and its use, so that every
-// input is read once; what a row has beyond that (more than 32768 values) is read again.
+// Both are HBM streams.  A row is spread over TPR threads, a thread holding kHeld chunks of 8
+// values in registers between the sum over the row and their use, so that every input is
+// read once; what a row has beyond that (more than 16384 values, EXTRA) is read again.
 // A 128-value block of 8-bit output is 16 neighbouring lanes' chunks.
 #include <algorithm>
 
@@ -17,7 +17,7 @@
 namespace ep {
 namespace {
 
-constexpr int kHeld = 4;
+constexpr int kHeld = 2;
 
 // 8 values of a type: their loads and stores, and the conversions.
 template <int T>
@@ -85,9 +85,12 @@ __device__ __forceinline__ void load_weight(float (&w)[8], const NormArgs& a, in
 
 template <int TPR> constexpr int kBlock = TPR < 256 ? 256 : TPR;
 
+// Rows of a workgroup at a time.
+template <int TPR> constexpr int kSlots = kBlock<TPR> / TPR;
+
 // Sums of N values over the TPR threads of a row, in an order that does not depend on
-// anything but TPR.  `s` is LDS of at least 2 N TPR / 64 floats, of which one half is
-// used by a row and the other by the next.
+// anything but TPR.  `s` is LDS of 2 N kBlock / 64 floats, of which one half is used by one
+// set of rows and the other by the next.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* s, int parity) {
   constexpr int W = TPR < 64 ? TPR : 64;
@@ -96,17 +99,18 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* s, int parity) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d);
   if constexpr (TPR > 64) {
-    constexpr int WAVES = TPR / 64;
-    float* at = s + parity * N * WAVES;
+    constexpr int WAVES = TPR / 64, ALL = kBlock<TPR> / 64;
+    float* at = s + parity * N * ALL;
+    const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) at[i * WAVES + (threadIdx.x >> 6)] = v[i];
+      for (int i = 0; i < N; ++i) at[i * ALL + wave] = v[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = 0.f;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) v[i] += at[i * WAVES + w];
+      for (int w = 0; w < WAVES; ++w) v[i] += at[i * ALL + wave / WAVES * WAVES + w];
     }
   }
 }
@@ -136,10 +140,10 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t row, int 
   if ((c & 15) == 0) a.scales[row * (a.N / 128) + c / 16] = scale;
 }
 
-template <int TPR, int XT, int RT>
+template <int TPR, int XT, int RT, bool EXTRA>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
-  constexpr int SLOTS = kBlock<TPR> / TPR;
-  __shared__ float s_sum[TPR > 64 ? 2 * TPR / 64 : 1];
+  constexpr int SLOTS = kSlots<TPR>;
+  __shared__ float s_sum[2 * kBlock<TPR> / 64];
   const int place = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   const int chunks = a.N / 8;
   int parity = 0;
@@ -149,10 +153,9 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
     const int64_t row = there ? first + slot : a.rows - 1;
     const uint8_t* x = a.x + row * a.N * (Chunk<XT>::BYTES / 8);
     const uint8_t* res = a.residual ? a.residual + row * a.N * (Chunk<RT>::BYTES / 8) : nullptr;
-    uint8_t* kept = a.residual_out + row * a.N * (Chunk<RT>::BYTES / 8);
-    uint8_t* out = a.out + row * a.N * (Chunk<XT>::BYTES / 8);
 
-    auto sum = [&](const Chunk<XT>& xc, const Chunk<RT>& rc, float (&s)[8]) {
+    // s of a chunk; 0 past the row's end, where the last chunk is loaded again
+    auto sum = [&](const Chunk<XT>& xc, const Chunk<RT>& rc, bool in, float (&s)[8]) {
       xc.get(s);
       if (res) {
         float r[8];
@@ -160,33 +163,39 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] += r[i];
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = in ? s[i] : 0.f;
+    };
+    auto load_sum = [&](int c, float (&s)[8]) {
+      Chunk<XT> xc;
+      Chunk<RT> rc{};
+      xc.load(x, c);
+      if (res) rc.load(res, c);
+      sum(xc, rc, true, s);
     };
     float held[kHeld][8], ss[1] = {0.f};
-    Chunk<XT> xc[kHeld];
-    Chunk<RT> rc[kHeld];
+    {
+      Chunk<XT> xc[kHeld];
+      Chunk<RT> rc[kHeld] = {};
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-      if (h * TPR < chunks) {
-        const int c = min(place + h * TPR, chunks - 1);
-        xc[h].load(x, c);
-        if (res) rc[h].load(res, c);
+      for (int h = 0; h < kHeld; ++h) xc[h].load(x, min(place + h * TPR, chunks - 1));
+      if (res)
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) rc[h].load(res, min(place + h * TPR, chunks - 1));
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        sum(xc[h], rc[h], place + h * TPR < chunks, held[h]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss[0] = __builtin_fmaf(held[h][i], held[h][i], ss[0]);
       }
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) held[h][i] = 0.f;
-      if (place + h * TPR < chunks) sum(xc[h], rc[h], held[h]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss[0] = __builtin_fmaf(held[h][i], held[h][i], ss[0]);
     }
-    for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
-      float s[8];
-      xc[0].load(x, c);
-      if (res) rc[0].load(res, c);
-      sum(xc[0], rc[0], s);
+    if constexpr (EXTRA)
+      for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
+        float s[8];
+        load_sum(c, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss[0] = __builtin_fmaf(s[i], s[i], ss[0]);
-    }
+        for (int i = 0; i < 8; ++i) ss[0] = __builtin_fmaf(s[i], s[i], ss[0]);
+      }
     row_sums<TPR>(ss, s_sum, parity);
     const float inv = inverse_rms(ss[0], a.N, a.eps);
 
@@ -198,12 +207,12 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
       if (a.residual_out) {
         Chunk<RT> k;
         k.put(s);
-        k.store(kept, c);
+        k.store(a.residual_out + row * a.N * (Chunk<RT>::BYTES / 8), c);
       }
       if (a.out) {
         Chunk<XT> k;
         k.put(y);
-        k.store(out, c);
+        k.store(a.out + row * a.N * (Chunk<XT>::BYTES / 8), c);
       }
       if (a.codes) store_codes(a, row, c, y);
     };
@@ -211,33 +220,28 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int h = 0; h < kHeld; ++h)
         if (place + h * TPR < chunks) finish(place + h * TPR, held[h]);
-      for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
-        float s[8];
-        xc[0].load(x, c);
-        if (res) rc[0].load(res, c);
-        sum(xc[0], rc[0], s);
-        finish(c, s);
-      }
+      if constexpr (EXTRA)
+        for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
+          float s[8];
+          load_sum(c, s);
+          finish(c, s);
+        }
     }
   }
 }
 
-// A workgroup adds up g r inv of its rows, column by column, in registers (beyond
-// kHeld chunks a thread in its part of the workspace, which nothing else touches), joins
-// the sums of its row slots and leaves them as one row of the workspace.
-template <int TPR, int XT, int RT>
+// A workgroup adds up g r inv of its rows, column by column, in registers (beyond kHeld
+// chunks a thread in its part of the workspace, which nothing else touches), joins the
+// sums of its row slots and leaves them as one row of the workspace.
+template <int TPR, int XT, int RT, bool EXTRA>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs a) {
-  constexpr int SLOTS = kBlock<TPR> / TPR;
-  __shared__ float s_sum[TPR > 64 ? 4 * TPR / 64 : 1];
-  __shared__ float s_dw[SLOTS > 1 ? SLOTS * TPR * kHeld * 8 : 1];
+  constexpr int SLOTS = kSlots<TPR>;
+  __shared__ float s_sum[4 * kBlock<TPR> / 64];
+  __shared__ float s_dw[SLOTS > 1 ? kBlock<TPR> * kHeld * 8 : 1];
   const int place = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   const int chunks = a.N / 8;
   float* mine = a.partial + (size_t)blockIdx.x * a.N;
-  float dw[kHeld][8];
-#pragma unroll
-  for (int h = 0; h < kHeld; ++h)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[h][i] = 0.f;
+  float dw[kHeld][8] = {};
   int parity = 0;
   bool begun = false;
   for (int64_t first = (int64_t)blockIdx.x * SLOTS; first < a.rows;
@@ -249,58 +253,56 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
     const uint8_t *g = a.grad_out + at_x, *r = a.x + at_r;
     const uint8_t* h0 = a.grad_residual ? a.grad_residual + at_r : nullptr;
 
-    Chunk<XT> gc[kHeld];
-    Chunk<RT> rc[kHeld], hc[kHeld];
     float sums[2] = {0.f, 0.f};        // r^2 and g w r
-    auto add = [&](const Chunk<XT>& gk, const Chunk<RT>& rk, int c) {
+    auto add = [&](const Chunk<XT>& gk, const Chunk<RT>& rk, int c, bool in) {
       float gv[8], rv[8], w[8];
       gk.get(gv);
       rk.get(rv);
       load_weight<XT>(w, a, c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sums[0] = __builtin_fmaf(rv[i], rv[i], sums[0]);
-        sums[1] = __builtin_fmaf(gv[i] * w[i], rv[i], sums[1]);
+        const float v = in ? rv[i] : 0.f;
+        sums[0] = __builtin_fmaf(v, v, sums[0]);
+        sums[1] = __builtin_fmaf(in ? gv[i] * w[i] : 0.f, v, sums[1]);
       }
     };
+    Chunk<XT> gc[kHeld];
+    Chunk<RT> rc[kHeld], hc[kHeld] = {};
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-      if (h * TPR < chunks) {
-        const int c = min(place + h * TPR, chunks - 1);
-        gc[h].load(g, c);
-        rc[h].load(r, c);
-        if (h0) hc[h].load(h0, c);
-      }
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-      if (place + h * TPR < chunks) add(gc[h], rc[h], place + h * TPR);
-    for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
-      Chunk<XT> gk;
-      Chunk<RT> rk;
-      gk.load(g, c);
-      rk.load(r, c);
-      add(gk, rk, c);
+    for (int h = 0; h < kHeld; ++h) {
+      const int c = min(place + h * TPR, chunks - 1);
+      gc[h].load(g, c);
+      rc[h].load(r, c);
     }
+    if (h0)
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) hc[h].load(h0, min(place + h * TPR, chunks - 1));
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      add(gc[h], rc[h], min(place + h * TPR, chunks - 1), place + h * TPR < chunks);
+    if constexpr (EXTRA)
+      for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
+        Chunk<XT> gk;
+        Chunk<RT> rk;
+        gk.load(g, c);
+        rk.load(r, c);
+        add(gk, rk, c, true);
+      }
     row_sums<TPR>(sums, s_sum, parity);
     const float inv = inverse_rms(sums[0], a.N, a.eps);
     const float shift = inv * inv * (sums[1] / (float)a.N);    // mean(g w r) inv^2
 
     auto finish = [&](int c, const Chunk<XT>& gk, const Chunk<RT>& rk, const Chunk<RT>& hk,
                       float (&dwc)[8]) {
-      float gv[8], rv[8], d[8];
+      float gv[8], rv[8], hv[8], d[8];
       gk.get(gv);
       rk.get(rv);
+      hk.get(hv);                     // zeros where there is none
       load_weight<XT>(d, a, c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        d[i] = inv * __builtin_fmaf(gv[i], d[i], -rv[i] * shift);
+        d[i] = inv * __builtin_fmaf(gv[i], d[i], -rv[i] * shift) + hv[i];
         dwc[i] = __builtin_fmaf(gv[i], rv[i] * inv, dwc[i]);
-      }
-      if (h0) {
-        float hv[8];
-        hk.get(hv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] += hv[i];
       }
       if (a.grad_x) {
         Chunk<XT> k;
@@ -317,26 +319,23 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
 #pragma unroll
       for (int h = 0; h < kHeld; ++h)
         if (place + h * TPR < chunks) finish(place + h * TPR, gc[h], rc[h], hc[h], dw[h]);
-      for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
-        Chunk<XT> gk;
-        Chunk<RT> rk, hk;
-        gk.load(g, c);
-        rk.load(r, c);
-        if (h0) hk.load(h0, c);
-        Chunk<EP_ROWS_F32> k;
-        float dwc[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dwc[i] = 0.f;
-        if (begun) {
-          k.load_cached(reinterpret_cast<const uint8_t*>(mine), c);
+      if constexpr (EXTRA)
+        for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
+          Chunk<XT> gk;
+          Chunk<RT> rk, hk{};
+          gk.load(g, c);
+          rk.load(r, c);
+          if (h0) hk.load(h0, c);
+          Chunk<EP_ROWS_F32> k{};
+          float dwc[8];
+          if (begun) k.load_cached(reinterpret_cast<const uint8_t*>(mine), c);
           k.get(dwc);
-        }
-        finish(c, gk, rk, hk, dwc);
-        k.put(dwc);
+          finish(c, gk, rk, hk, dwc);
+          k.put(dwc);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          reinterpret_cast<u32x4*>(mine)[2 * (size_t)c + i] = k.v[i];
-      }
+          for (int i = 0; i < 2; ++i)
+            reinterpret_cast<u32x4*>(mine)[2 * (size_t)c + i] = k.v[i];
+        }
     }
     begun = true;
   }
@@ -345,8 +344,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
 #pragma unroll
     for (int h = 0; h < kHeld; ++h)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        s_dw[(slot * TPR * kHeld + place + h * TPR) * 8 + i] = dw[h][i];
+      for (int i = 0; i < 8; ++i) s_dw[((slot * kHeld + h) * TPR + place) * 8 + i] = dw[h][i];
     __syncthreads();
     for (int n = threadIdx.x; n < a.N; n += kBlock<TPR>) {
       float v = 0.f;
@@ -387,31 +385,37 @@ __global__ __launch_bounds__(256) void add_partials_kernel(const float* partial,
   if (g == 0) *reinterpret_cast<f32x4*>(out + n) = s[threadIdx.x];
 }
 
-// Threads a row: enough that they hold it in kHeld chunks each.
+// Threads a row: as few as hold it in kHeld chunks each.
 int threads_per_row(int N) {
-  const int chunks = N / 8;
-  return chunks <= 16 * kHeld ? 16 : chunks <= 64 * kHeld ? 64 : chunks <= 256 * kHeld ? 256 : 1024;
+  int tpr = 16;
+  while (tpr < 1024 && tpr * kHeld < N / 8) tpr *= 2;
+  return tpr;
 }
 
 int rows_per_block(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
 
-template <int TPR, int XT, int RT>
+template <int TPR, int XT, int RT, bool EXTRA = false>
 void launch_one(const NormArgs& a, bool backward, int grid, hipStream_t st) {
   if (backward)
-    hipLaunchKernelGGL((rms_norm_backward_kernel<TPR, XT, RT>), dim3(grid), dim3(kBlock<TPR>), 0,
-                       st, a);
+    hipLaunchKernelGGL((rms_norm_backward_kernel<TPR, XT, RT, EXTRA>), dim3(grid),
+                       dim3(kBlock<TPR>), 0, st, a);
   else
-    hipLaunchKernelGGL((rms_norm_kernel<TPR, XT, RT>), dim3(grid), dim3(kBlock<TPR>), 0, st, a);
+    hipLaunchKernelGGL((rms_norm_kernel<TPR, XT, RT, EXTRA>), dim3(grid), dim3(kBlock<TPR>), 0, st,
+                       a);
 }
 
 template <int XT, int RT>
 void launch_types(const NormArgs& a, bool backward, int tpr, int grid, hipStream_t st) {
   switch (tpr) {
     case 16: return launch_one<16, XT, RT>(a, backward, grid, st);
+    case 32: return launch_one<32, XT, RT>(a, backward, grid, st);
     case 64: return launch_one<64, XT, RT>(a, backward, grid, st);
+    case 128: return launch_one<128, XT, RT>(a, backward, grid, st);
     case 256: return launch_one<256, XT, RT>(a, backward, grid, st);
-    default: return launch_one<1024, XT, RT>(a, backward, grid, st);
+    case 512: return launch_one<512, XT, RT>(a, backward, grid, st);
   }
+  if (a.N / 8 <= 1024 * kHeld) return launch_one<1024, XT, RT>(a, backward, grid, st);
+  launch_one<1024, XT, RT, true>(a, backward, grid, st);
 }
 
 hipError_t launch(const NormArgs& a, bool backward, int tpr, int grid, hipStream_t st) {
@@ -447,7 +451,7 @@ hipError_t launch_rms_norm(const NormArgs& a, int num_cus, hipStream_t st) {
 // Partial rows of the weights' gradient: one for each workgroup.
 int norm_backward_parts(int64_t rows, int N, int num_cus) {
   const int tpr = threads_per_row(N), per = rows_per_block(tpr);
-  return (int)std::min<int64_t>((rows + per - 1) / per, (tpr == 1024 ? 1 : 4) * (int64_t)num_cus);
+  return (int)std::min<int64_t>((rows + per - 1) / per, 1024 / std::max(tpr, 256) * (int64_t)num_cus);
 }
 
 hipError_t launch_rms_norm_backward(const NormArgs& a, int num_cus, hipStream_t st) {
