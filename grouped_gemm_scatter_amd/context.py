@@ -129,6 +129,7 @@ class EpCombine:
                                         self.tile_counter, self.error_word, self.trace,
                                         self.epoch_word)
         self.epoch = 0
+        self._workspaces = {}        # bytes by (call, tokens a rank)
 
     # views of the control words
     @property
@@ -190,6 +191,13 @@ class EpCombine:
         if t.numel() < elems:
             raise ValueError(f"{name}: {t.numel()} elements, at least {elems} needed")
         return self._shape(t, name, t.shape, dtype)
+
+    def _workspace_bytes(self, call, tokens: int) -> int:
+        """What `call` answers for so many tokens a rank, asked once."""
+        need = self._workspaces.get((call, tokens))
+        if need is None:
+            need = self._workspaces[call, tokens] = call(self.handle, tokens)
+        return need
 
     def _empty(self, shape, dtype, stream):
         """Memory for what a call returns, allocated on the stream that it runs on."""
@@ -352,7 +360,7 @@ class EpCombine:
         if grad_weight is None:
             grad_weight = self._empty((N,), torch.float32, stream)
         grad_w_at = self._shape(grad_weight, "grad_weight", (N,), torch.float32)
-        need = B.ep_rms_norm_backward_workspace(self.handle, T)
+        need = self._workspace_bytes(B.ep_rms_norm_backward_workspace, T)
         workspace = self._empty((max(need, 16),), torch.uint8, stream)
         B.ep_rms_norm_backward(self.handle, params, at, res_at, sums_at, weight_at, T, x_at,
                                both_at, grad_w_at, workspace.data_ptr(), need, stream)
@@ -396,7 +404,7 @@ class EpCombine:
         if out is None:
             out = self._empty(shape, torch.bfloat16, stream)
         out_at = self._shape(out, "out", shape, torch.bfloat16)
-        need = B.ep_moe_layer_workspace(self.handle, T)
+        need = self._workspace_bytes(B.ep_moe_layer_workspace, T)
         workspace = self._empty((max(need, 16),), torch.uint8, stream)
         B.ep_moe_layer(self.handle, format1, format2, at, x_scale_at, w1_at, s1_at, w2_at, s2_at,
                        ids_at, w_at, T, out_at, workspace.data_ptr(), need, stream)

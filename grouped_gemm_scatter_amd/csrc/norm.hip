@@ -25,17 +25,25 @@ struct Chunk {
   u32x4 v[T == EP_ROWS_F32 ? 2 : 1];
   static constexpr int BYTES = T == EP_ROWS_F32 ? 32 : 16;
 
+  // STREAM: past the caches' replacement
+  template <bool STREAM = false>
   __device__ __forceinline__ void load(const uint8_t* row, int c) {
 #pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) v[i] = load16_nt(row + (size_t)c * BYTES + i * 16);
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint8_t* p = row + (size_t)c * BYTES + i * 16;
+      v[i] = STREAM && T != EP_ROWS_F32 ? load16_nt(p) : load16(p);
+    }
   }
-  __device__ __forceinline__ void load_cached(const uint8_t* row, int c) {
-#pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) v[i] = load16(row + (size_t)c * BYTES + i * 16);
-  }
+  template <bool STREAM = false>
   __device__ __forceinline__ void store(uint8_t* row, int c) const {
 #pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) store16_nt(row + (size_t)c * BYTES + i * 16, v[i]);
+    for (int i = 0; i < BYTES / 16; ++i) {
+      uint8_t* p = row + (size_t)c * BYTES + i * 16;
+      if constexpr (STREAM && T != EP_ROWS_F32)
+        store16_nt(p, v[i]);
+      else
+        *(global_u32x4*)p = v[i];
+    }
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
@@ -74,11 +82,11 @@ template <int XT>
 __device__ __forceinline__ void load_weight(float (&w)[8], const NormArgs& a, int c) {
   if (a.weight_f32) {
     Chunk<EP_ROWS_F32> k;
-    k.load_cached(a.weight, c);
+    k.load(a.weight, c);
     k.get(w);
   } else {
     Chunk<XT> k;
-    k.load_cached(a.weight, c);
+    k.load(a.weight, c);
     k.get(w);
   }
 }
@@ -140,7 +148,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t row, int 
   if ((c & 15) == 0) a.scales[row * (a.N / 128) + c / 16] = scale;
 }
 
-template <int TPR, int XT, int RT, bool EXTRA>
+template <int TPR, int XT, int RT, bool STREAM, bool EXTRA>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
   constexpr int SLOTS = kSlots<TPR>;
   __shared__ float s_sum[2 * kBlock<TPR> / 64];
@@ -169,8 +177,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
     auto load_sum = [&](int c, float (&s)[8]) {
       Chunk<XT> xc;
       Chunk<RT> rc{};
-      xc.load(x, c);
-      if (res) rc.load(res, c);
+      xc.template load<STREAM>(x, c);
+      if (res) rc.template load<STREAM>(res, c);
       sum(xc, rc, true, s);
     };
     float held[kHeld][8], ss[1] = {0.f};
@@ -178,10 +186,10 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
       Chunk<XT> xc[kHeld];
       Chunk<RT> rc[kHeld] = {};
 #pragma unroll
-      for (int h = 0; h < kHeld; ++h) xc[h].load(x, min(place + h * TPR, chunks - 1));
+      for (int h = 0; h < kHeld; ++h) xc[h].template load<STREAM>(x, min(place + h * TPR, chunks - 1));
       if (res)
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h) rc[h].load(res, min(place + h * TPR, chunks - 1));
+        for (int h = 0; h < kHeld; ++h) rc[h].template load<STREAM>(res, min(place + h * TPR, chunks - 1));
 #pragma unroll
       for (int h = 0; h < kHeld; ++h) {
         sum(xc[h], rc[h], place + h * TPR < chunks, held[h]);
@@ -207,12 +215,12 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
       if (a.residual_out) {
         Chunk<RT> k;
         k.put(s);
-        k.store(a.residual_out + row * a.N * (Chunk<RT>::BYTES / 8), c);
+        k.template store<STREAM>(a.residual_out + row * a.N * (Chunk<RT>::BYTES / 8), c);
       }
       if (a.out) {
         Chunk<XT> k;
         k.put(y);
-        k.store(a.out + row * a.N * (Chunk<XT>::BYTES / 8), c);
+        k.template store<STREAM>(a.out + row * a.N * (Chunk<XT>::BYTES / 8), c);
       }
       if (a.codes) store_codes(a, row, c, y);
     };
@@ -233,7 +241,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_kernel(NormArgs a) {
 // A workgroup adds up g r inv of its rows, column by column, in registers (beyond kHeld
 // chunks a thread in its part of the workspace, which nothing else touches), joins the
 // sums of its row slots and leaves them as one row of the workspace.
-template <int TPR, int XT, int RT, bool EXTRA>
+template <int TPR, int XT, int RT, bool STREAM, bool EXTRA>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs a) {
   constexpr int SLOTS = kSlots<TPR>;
   __shared__ float s_sum[4 * kBlock<TPR> / 64];
@@ -271,12 +279,12 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
       const int c = min(place + h * TPR, chunks - 1);
-      gc[h].load(g, c);
-      rc[h].load(r, c);
+      gc[h].template load<STREAM>(g, c);
+      rc[h].template load<STREAM>(r, c);
     }
     if (h0)
 #pragma unroll
-      for (int h = 0; h < kHeld; ++h) hc[h].load(h0, min(place + h * TPR, chunks - 1));
+      for (int h = 0; h < kHeld; ++h) hc[h].template load<STREAM>(h0, min(place + h * TPR, chunks - 1));
 #pragma unroll
     for (int h = 0; h < kHeld; ++h)
       add(gc[h], rc[h], min(place + h * TPR, chunks - 1), place + h * TPR < chunks);
@@ -284,8 +292,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
       for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
         Chunk<XT> gk;
         Chunk<RT> rk;
-        gk.load(g, c);
-        rk.load(r, c);
+        gk.template load<STREAM>(g, c);
+        rk.template load<STREAM>(r, c);
         add(gk, rk, c, true);
       }
     row_sums<TPR>(sums, s_sum, parity);
@@ -307,12 +315,12 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
       if (a.grad_x) {
         Chunk<XT> k;
         k.put(d);
-        k.store(a.grad_x + at_x, c);
+        k.template store<STREAM>(a.grad_x + at_x, c);
       }
       if (a.grad_sum) {
         Chunk<RT> k;
         k.put(d);
-        k.store(a.grad_sum + at_r, c);
+        k.template store<STREAM>(a.grad_sum + at_r, c);
       }
     };
     if (there) {
@@ -323,12 +331,12 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
         for (int c = place + kHeld * TPR; c < chunks; c += TPR) {
           Chunk<XT> gk;
           Chunk<RT> rk, hk{};
-          gk.load(g, c);
-          rk.load(r, c);
-          if (h0) hk.load(h0, c);
+          gk.template load<STREAM>(g, c);
+          rk.template load<STREAM>(r, c);
+          if (h0) hk.template load<STREAM>(h0, c);
           Chunk<EP_ROWS_F32> k{};
           float dwc[8];
-          if (begun) k.load_cached(reinterpret_cast<const uint8_t*>(mine), c);
+          if (begun) k.load(reinterpret_cast<const uint8_t*>(mine), c);
           k.get(dwc);
           finish(c, gk, rk, hk, dwc);
           k.put(dwc);
@@ -394,28 +402,47 @@ int threads_per_row(int N) {
 
 int rows_per_block(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
 
-template <int TPR, int XT, int RT, bool EXTRA = false>
+template <int TPR, int XT, int RT, bool STREAM, bool EXTRA = false>
 void launch_one(const NormArgs& a, bool backward, int grid, hipStream_t st) {
   if (backward)
-    hipLaunchKernelGGL((rms_norm_backward_kernel<TPR, XT, RT, EXTRA>), dim3(grid),
+    hipLaunchKernelGGL((rms_norm_backward_kernel<TPR, XT, RT, STREAM, EXTRA>), dim3(grid),
                        dim3(kBlock<TPR>), 0, st, a);
   else
-    hipLaunchKernelGGL((rms_norm_kernel<TPR, XT, RT, EXTRA>), dim3(grid), dim3(kBlock<TPR>), 0, st,
-                       a);
+    hipLaunchKernelGGL((rms_norm_kernel<TPR, XT, RT, STREAM, EXTRA>), dim3(grid), dim3(kBlock<TPR>),
+                       0, st, a);
 }
+
+template <int XT, int RT, bool STREAM>
+void launch_types(const NormArgs& a, bool backward, int tpr, int grid, hipStream_t st) {
+  switch (tpr) {
+    case 16: return launch_one<16, XT, RT, STREAM>(a, backward, grid, st);
+    case 32: return launch_one<32, XT, RT, STREAM>(a, backward, grid, st);
+    case 64: return launch_one<64, XT, RT, STREAM>(a, backward, grid, st);
+    case 128: return launch_one<128, XT, RT, STREAM>(a, backward, grid, st);
+    case 256: return launch_one<256, XT, RT, STREAM>(a, backward, grid, st);
+    case 512: return launch_one<512, XT, RT, STREAM>(a, backward, grid, st);
+  }
+  if (a.N / 8 <= 1024 * kHeld) return launch_one<1024, XT, RT, STREAM>(a, backward, grid, st);
+  launch_one<1024, XT, RT, STREAM, true>(a, backward, grid, st);
+}
+
+// Rows of more than this many bytes in all go past the caches' replacement.  Measured on rows
+// of 7168 bf16 values with a residual, us of the norm and of its gradient, streamed and not:
+//    59 MB   13.0 and 12.2    27.1 and 22.8
+//   117 MB   22.7 and 25.6    38.0 and 36.4
+//   235 MB   41.2 and 45.4    58.0 and 57.6
+//   470 MB   82.0 and 87.8    97.3 and 100.6
+// (the loads and stores of 32-bit values, half of every 32 bytes each, never do: 159 MB of
+// which two thirds are such 34.6 and 28.8)
+constexpr int64_t kStreamBytes = 96 << 20;
 
 template <int XT, int RT>
 void launch_types(const NormArgs& a, bool backward, int tpr, int grid, hipStream_t st) {
-  switch (tpr) {
-    case 16: return launch_one<16, XT, RT>(a, backward, grid, st);
-    case 32: return launch_one<32, XT, RT>(a, backward, grid, st);
-    case 64: return launch_one<64, XT, RT>(a, backward, grid, st);
-    case 128: return launch_one<128, XT, RT>(a, backward, grid, st);
-    case 256: return launch_one<256, XT, RT>(a, backward, grid, st);
-    case 512: return launch_one<512, XT, RT>(a, backward, grid, st);
-  }
-  if (a.N / 8 <= 1024 * kHeld) return launch_one<1024, XT, RT>(a, backward, grid, st);
-  launch_one<1024, XT, RT, true>(a, backward, grid, st);
+  const int64_t value = 2 * Chunk<XT>::BYTES / 8 + 2 * Chunk<RT>::BYTES / 8;
+  if (a.rows * a.N * value >= kStreamBytes)
+    launch_types<XT, RT, true>(a, backward, tpr, grid, st);
+  else
+    launch_types<XT, RT, false>(a, backward, tpr, grid, st);
 }
 
 hipError_t launch(const NormArgs& a, bool backward, int tpr, int grid, hipStream_t st) {
@@ -448,9 +475,11 @@ hipError_t launch_rms_norm(const NormArgs& a, int num_cus, hipStream_t st) {
   return launch(a, false, tpr, (int)grid, st);
 }
 
-// Partial rows of the weights' gradient: one for each workgroup.
+// Partial rows of the weights' gradient: one for each workgroup.  Workgroups have at least
+// two sets of rows each, since a partial row costs twice its bytes (512 rows of 7168: one
+// 19.9 us a call, two 16.0, four 16.8, eight 23.2).
 int norm_backward_parts(int64_t rows, int N, int num_cus) {
-  const int tpr = threads_per_row(N), per = rows_per_block(tpr);
+  const int tpr = threads_per_row(N), per = 2 * rows_per_block(tpr);
   return (int)std::min<int64_t>((rows + per - 1) / per, 1024 / std::max(tpr, 256) * (int64_t)num_cus);
 }
 
