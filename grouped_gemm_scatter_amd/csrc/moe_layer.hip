@@ -173,11 +173,29 @@ struct Bf16Rows {
   }
 };
 
+// The blocks of a step of the up-projection: 16 gate rows and their 16 up rows.
+template <class P>
+struct TwoBlocks {
+  typename P::Block g, u;
+  __device__ __forceinline__ void load(const typename P::Source& s, uint32_t gate, uint32_t up,
+                                       int kt, int length) {
+    P::load(g, s, gate, kt, length);
+    P::load(u, s, up, kt, length);
+  }
+  template <int RB, class Rows>
+  __device__ __forceinline__ void multiply(f32x4 (&ag)[RowsOf<RB>::ACCS],
+                                           f32x4 (&au)[RowsOf<RB>::ACCS], const Rows& r) const {
+    P::template multiply<RB>(ag, r, g);
+    P::template multiply<RB>(au, r, u);
+  }
+};
+
 // ---- The three kinds of weights.  Block: 16 rows of them, one step of 128 k, as a wave
 // holds it; Rows: the first operand's 16 rows of the same k.  Wave-uniform: where a
 // block's rows start (`row0`), the step.
 
 struct Bf16 {
+  static constexpr int STEP = 128;                 // k of a step of the down-projection
   // steps in flight, as many as 128 registers hold
   static constexpr int depth(int rows) { return rows > 16 ? 1 : 2; }
   static constexpr bool PAIR_A_LANE = false;
@@ -212,9 +230,10 @@ struct Bf16 {
     return (lane >> 4) * 16 + quarter * 64;
   }
   template <int RB>
-  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, buffer x,
+  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, const uint8_t* x0, int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
-                                                   int kt) {
+                                                   int kt, int) {
+    const buffer x = make_buffer(x0, length);
 #pragma unroll
     for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j)
 #pragma unroll
@@ -319,9 +338,10 @@ struct Fp8Up : Fp8 {
     return (lane >> 4) * 16 + half * 64;
   }
   template <int RB>
-  static __device__ __forceinline__ void load_rows(Rows<RB>& r, buffer x,
+  static __device__ __forceinline__ void load_rows(Rows<RB>& r, const uint8_t* x0, int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
-                                                   int kt) {
+                                                   int kt, int) {
+    const buffer x = make_buffer(x0, length);
 #pragma unroll
     for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j)
 #pragma unroll
@@ -360,15 +380,17 @@ struct Fp8Up : Fp8 {
 
 // Rows in bf16: the down-projection, the codes converted (exactly).
 struct Fp8Down : Fp8 {
+  static constexpr int STEP = 128;
   static constexpr int depth(int) { return 3; }
   template <int RB> using Rows = Bf16Rows<RB>;
   static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
     return (lane >> 4) * 32 + (quarter >> 1) * 128 + (quarter & 1) * 16;
   }
   template <int RB>
-  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, buffer x,
+  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, const uint8_t* x0, int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
-                                                   int kt) {
+                                                   int kt, int) {
+    const buffer x = make_buffer(x0, length);
 #pragma unroll
     for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
       in_order(r.v[q] = buffer_load16(x, row[0] + (q >> 1) * 128 + (q & 1) * 16, kt * 256));
@@ -393,20 +415,23 @@ struct Fp8Down : Fp8 {
 // Packed 4-bit codes: 16 rows x 128 k are one run of 1 KB.  A wave's load is whole lines
 // that no other takes, so it goes past the caches' replacement (6.7 TB/s against 6.1; where a
 // line is two loads of 64 bytes a row, as with the other weights, it is the other way
-// around, 4.3 and 5.5).
+// around, 4.3 and 5.5).  The vector memory path takes about 40 clocks a load of a wave,
+// however few bytes it brings, and 1 KB of codes is 95 clocks of the memory's rate: so two
+// blocks' scales come with one load, the even and the odd 16 lanes each one block's,
+// exchanged in registers.
 template <class F>
 struct W4 {
-  static constexpr int depth(int rows) { return rows > 16 ? 1 : rows > 8 || F::GROUP == 32 ? 2 : 3; }
-  static constexpr bool PAIR_A_LANE = false;
   static constexpr uint32_t SB = 16 * (128 / F::GROUP) * 2;   // scale bytes of a run
+  static constexpr bool PAIR_A_LANE = false;
+  static constexpr int depth(int rows) {
+    return rows > 16 ? 1 : rows > 8 || F::GROUP == 32 ? 2 : 3;
+  }
+  typedef typename F::word word;
   struct Source {
     const uint8_t *w, *s;
     uint32_t lane, lane_s;
+    int odd;                            // all bits in the lanes of the second block
     int kt;                             // runs of a 16-row block
-  };
-  struct Block {
-    u32x4 v;
-    typename F::word s;
   };
   template <int RB> using Rows = Bf16Rows<RB>;
   static __device__ __forceinline__ Source source(const MoeWeights& w, int e, int rows, int k,
@@ -418,33 +443,110 @@ struct W4 {
     s.s = reinterpret_cast<const uint8_t*>(w.scales) + run * SB;
     s.lane = lane * 16;
     s.lane_s = (lane & 15) * (SB / 16);
+    s.odd = -((lane >> 4) & 1);
     return s;
   }
   static __device__ __forceinline__ uint32_t start(const MoeWeights&, int row0, int) {
     return row0 / 16;
   }
-  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int kt,
-                                              int length) {
-    const uint32_t run = start * s.kt + kt;
-    in_order(b.v = buffer_load16_nt(make_buffer(s.w, length), s.lane, run * 1024));
-    in_order(buffer_load_to(b.s, make_buffer(s.s, length), s.lane_s, run * SB));
+  // the scales of the even and of the odd lanes' block, in all lanes
+  static __device__ __forceinline__ void both(word v, word& even, word& odd) {
+    if constexpr (sizeof(word) == 8) {
+      const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32),
+                                                       false, false);
+      even = (uint64_t)hi[0] << 32 | lo[0];
+      odd = (uint64_t)hi[1] << 32 | lo[1];
+    } else {
+      const auto r = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+      even = (word)r[0];
+      odd = (word)r[1];
+    }
   }
   static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
     return Bf16::at(lane, quarter);
   }
   template <int RB>
-  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, buffer x,
+  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, const uint8_t* x, int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
-                                                   int kt) {
-    Bf16::load_rows<RB>(r, x, row, kt);
+                                                   int kt, int) {
+    Bf16::load_rows<RB>(r, x, length, row, kt, 0);
+  }
+  template <int RB>
+  static __device__ __forceinline__ void multiply_block(f32x4 (&acc)[RowsOf<RB>::ACCS],
+                                                        const Bf16Rows<RB>& r, const u32x4& v,
+                                                        word s) {
+    constexpr int QPS = F::GROUP / 32;
+    scaled_multiply<RB, QPS>(
+        acc, r, [&](int q) { return decode8<F::CODES>(v[q]); },
+        [&](int q) { return F::scale((uint16_t)(s >> (16 * (q / QPS)))); });
+  }
+};
+
+template <class F>
+struct TwoBlocks<W4<F>> {
+  typedef W4<F> P;
+  u32x4 g, u;
+  typename P::word s;
+  __device__ __forceinline__ void load(const typename P::Source& src, uint32_t gate, uint32_t up,
+                                       int kt, int length) {
+    const uint32_t rg = gate * src.kt + kt, ru = up * src.kt + kt;
+    in_order(g = buffer_load16_nt(make_buffer(src.w, length), src.lane, rg * 1024));
+    in_order(u = buffer_load16_nt(make_buffer(src.w, length), src.lane, ru * 1024));
+    in_order(buffer_load_to(s, make_buffer(src.s, length),
+                            src.lane_s + (src.odd & (int)((ru - rg) * P::SB)), rg * P::SB));
+  }
+  template <int RB, class Rows>
+  __device__ __forceinline__ void multiply(f32x4 (&ag)[RowsOf<RB>::ACCS],
+                                           f32x4 (&au)[RowsOf<RB>::ACCS], const Rows& r) const {
+    typename P::word sg, su;
+    P::both(s, sg, su);
+    P::template multiply_block<RB>(ag, r, g, sg);
+    P::template multiply_block<RB>(au, r, u, su);
+  }
+};
+
+// The same for the down-projection, where the two blocks are two consecutive 128 k of a row
+// block, of which the second may lie past the end.
+template <class F>
+struct W4Down : W4<F> {
+  typedef W4<F> P;
+  typedef typename P::word word;
+  typedef typename P::Source Source;
+  static constexpr int depth(int rows) { return rows > 8 ? 1 : 2; }
+  static constexpr int STEP = 256;
+  struct Block {
+    u32x4 v[2];
+    word s;
+  };
+  template <int RB>
+  struct Rows {
+    Bf16Rows<RB> r[2];
+    static __device__ __forceinline__ int quarter(int lane) { return Bf16Rows<RB>::quarter(lane); }
+  };
+  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int k,
+                                              int length) {
+    const uint32_t run = start * s.kt + 2 * k;
+    const int second = length & buffer_length(2 * k + 1, s.kt);
+    in_order(b.v[0] = buffer_load16_nt(make_buffer(s.w, length), s.lane, run * 1024));
+    in_order(b.v[1] = buffer_load16_nt(make_buffer(s.w, second), s.lane, run * 1024 + 1024));
+    in_order(buffer_load_to(b.s, make_buffer(s.s, length),
+                            s.lane_s + (s.odd & second & (int)P::SB), run * P::SB));
+  }
+  template <int RB>
+  static __device__ __forceinline__ void load_rows(Rows<RB>& r, const uint8_t* x, int length,
+                                                   const uint32_t (&row)[RowsOf<RB>::BLOCKS],
+                                                   int k, int inter) {
+    Bf16::load_rows<RB>(r.r[0], x, length, row, 2 * k, 0);
+    Bf16::load_rows<RB>(r.r[1], x, length & buffer_length(2 * k + 1, inter / 128), row, 2 * k + 1, 0);
   }
   template <int RB>
   static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                  const Bf16Rows<RB>& r, const Block& b) {
-    constexpr int QPS = F::GROUP / 32;
-    scaled_multiply<RB, QPS>(
-        acc, r, [&](int q) { return decode8<F::CODES>(b.v[q]); },
-        [&](int q) { return F::scale((uint16_t)(b.s >> (16 * (q / QPS)))); });
+                                                  const Rows<RB>& r, const Block& b) {
+    word s0, s1;
+    P::both(b.s, s0, s1);
+    P::template multiply_block<RB>(acc, r.r[0], b.v[0], s0);
+    P::template multiply_block<RB>(acc, r.r[1], b.v[1], s1);
   }
 };
 
@@ -471,7 +573,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
   const int KT = a.hidden / 128, per = a.inter / 16;
   const int items = __builtin_amdgcn_readfirstlane(s.segments) * per;
   struct Step {
-    typename P::Block g, u;
+    TwoBlocks<P> w;
     Rows r;
   };
   struct Place {
@@ -500,9 +602,8 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
   // condition the compiler would wait for all that are in flight.
   auto load = [&](Step& st, Place& p) {
     const int length = buffer_length(p.item, items) & buffer_length(p.k, KT);
-    P::load(st.g, p.src, p.gate, p.k, length);
-    P::load(st.u, p.src, p.up, p.k, length);
-    P::template load_rows<RB>(st.r, make_buffer(a.x, length), p.row, p.k);
+    st.w.load(p.src, p.gate, p.up, p.k, length);
+    P::template load_rows<RB>(st.r, a.x, length, p.row, p.k, a.hidden);
     if constexpr (P::PAIR_A_LANE)
 #pragma unroll
       for (int j = 0; j < BLOCKS; ++j)
@@ -528,8 +629,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       // (a wave without a step of its own multiplies the empty buffer's zeros)
-      P::template multiply<RB>(ag, st[d].r, st[d].g);
-      P::template multiply<RB>(au, st[d].r, st[d].u);
+      st[d].w.template multiply<RB>(ag, au, st[d].r);
       __builtin_amdgcn_sched_barrier(0);
       load(st[d], ahead);
       k += kWaves;
@@ -613,7 +713,7 @@ template <class P, int RB>
 __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, const float* weight,
                                            float (*s_out)[16], int b, int wave, int lane) {
   typedef typename P::template Rows<RB> Rows;
-  const int KT = a.inter / 128;
+  const int KT = (a.inter + P::STEP - 1) / P::STEP;     // steps
   constexpr int DEPTH = P::depth(RB);
   const int segments = __builtin_amdgcn_readfirstlane(s.segments);
   const uint32_t start = P::start(a.w2, b * 16, a.inter);
@@ -648,7 +748,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, con
   auto load = [&](Step& st, Place& p) {
     const int length = buffer_length(p.seg, segments);
     P::load(st.w, p.src, start, p.k, length);
-    P::template load_rows<RB>(st.r, make_buffer(a.h, length), p.row, p.k);
+    P::template load_rows<RB>(st.r, a.h, length, p.row, p.k, a.inter);
     if (move(p.seg, p.k)) enter(p);
   };
   f32x4 acc[RowsOf<RB>::ACCS] = {};
@@ -732,24 +832,21 @@ void launch_down(const MoeArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((moe_down_kernel<P>), dim3(a.hidden / 16), dim3(kThreads), 0, st, a);
 }
 
-template <class P>
-void launch_product(const MoeArgs& a, bool up, int num_cus, hipStream_t st) {
-  up ? launch_up<P>(a, num_cus, st) : launch_down<P>(a, st);
-}
-
 template <int CODES, int GROUP>
 void launch_w4(const MoeArgs& a, bool up, bool f16, int num_cus, hipStream_t st) {
+  typedef Format<CODES, GROUP, true> Half;
+  typedef Format<CODES, GROUP, false> Bf;
   if (f16)
-    launch_product<W4<Format<CODES, GROUP, true>>>(a, up, num_cus, st);
+    up ? launch_up<W4<Half>>(a, num_cus, st) : launch_down<W4Down<Half>>(a, st);
   else
-    launch_product<W4<Format<CODES, GROUP, false>>>(a, up, num_cus, st);
+    up ? launch_up<W4<Bf>>(a, num_cus, st) : launch_down<W4Down<Bf>>(a, st);
 }
 
 hipError_t launch_product_of(const MoeArgs& a, const MoeWeights& w, bool up, int num_cus,
                              hipStream_t st) {
   if (w.group == 0) {
     if (!a.fp8)
-      launch_product<Bf16>(a, up, num_cus, st);
+      up ? launch_up<Bf16>(a, num_cus, st) : launch_down<Bf16>(a, st);
     else
       up ? launch_up<Fp8Up>(a, num_cus, st) : launch_down<Fp8Down>(a, st);
     return hipGetLastError();
