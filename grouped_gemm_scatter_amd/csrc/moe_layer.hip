@@ -196,6 +196,7 @@ struct TwoBlocks {
 
 struct Bf16 {
   static constexpr int STEP = 128;                 // k of a step of the down-projection
+  static constexpr bool SPREAD = true;             // its steps: every eighth, or a run
   // steps in flight, as many as 128 registers hold
   static constexpr int depth(int rows) { return rows > 16 ? 1 : 2; }
   static constexpr bool PAIR_A_LANE = false;
@@ -381,6 +382,7 @@ struct Fp8Up : Fp8 {
 // Rows in bf16: the down-projection, the codes converted (exactly).
 struct Fp8Down : Fp8 {
   static constexpr int STEP = 128;
+  static constexpr bool SPREAD = true;
   static constexpr int depth(int) { return 3; }
   template <int RB> using Rows = Bf16Rows<RB>;
   static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
@@ -515,6 +517,7 @@ struct W4Down : W4<F> {
   typedef typename P::Source Source;
   static constexpr int depth(int rows) { return rows > 8 ? 1 : 2; }
   static constexpr int STEP = 256;
+  static constexpr bool SPREAD = false;
   struct Block {
     u32x4 v[2];
     word s;
@@ -721,10 +724,23 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, con
     typename P::Block w;
     Rows r;
   };
-  // Where a wave's loads are: a segment and a step of its k; a wave takes every eighth
-  // step of all.  What belongs to the segment is looked up when it is entered.
+  // A wave takes `count` of the steps of all segments, every eighth or a run of them.
+  const int steps = segments * KT;
+  const int begin = P::SPREAD ? wave : wave * steps / kWaves;
+  const int count = P::SPREAD ? (steps - wave + kWaves - 1) / kWaves
+                              : (wave + 1) * steps / kWaves - begin;
+  constexpr int STRIDE = P::SPREAD ? kWaves : 1;
+  const int whole = STRIDE / KT, rest = STRIDE % KT;
+  // moves on; true if that left the segment
+  auto move = [&](int& seg, int& k) {
+    const int was = seg, over = k + rest >= KT;
+    seg += whole + over;
+    k += rest - over * KT;
+    return seg != was;
+  };
+  // Where the loads are.  What belongs to the segment is looked up when it is entered.
   struct Place {
-    int seg, k;
+    int seg, k, at;
     decltype(P::source(a.w2, 0, 0, 0, 0)) src;
     uint32_t row[1];
   };
@@ -737,37 +753,31 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, con
     p.row[0] = (uint32_t)(pair + min((lane & 15) % RB, n - 1)) * (uint32_t)a.inter * 2 +
                P::at(lane, Rows::quarter(lane));
   };
-  // moves on by eight steps; true if that left the segment
-  const int whole = kWaves / KT, rest = kWaves % KT;
-  auto move = [&](int& seg, int& k) {
-    const int was = seg, over = k + rest >= KT;
-    seg += whole + over;
-    k += rest - over * KT;
-    return seg != was;
-  };
   auto load = [&](Step& st, Place& p) {
-    const int length = buffer_length(p.seg, segments);
+    const int length = buffer_length(p.at++, count);
     P::load(st.w, p.src, start, p.k, length);
     P::template load_rows<RB>(st.r, a.h, length, p.row, p.k, a.inter);
     if (move(p.seg, p.k)) enter(p);
   };
+  if (count <= 0) return;
   f32x4 acc[RowsOf<RB>::ACCS] = {};
   Step st[DEPTH];
-  int seg = wave / KT, k = wave % KT;
+  int seg = begin / KT, k = begin % KT;
   Place ahead;
   ahead.seg = seg;
   ahead.k = k;
+  ahead.at = 0;
   enter(ahead);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) load(st[d], ahead);
-  while (seg < segments) {
+  for (int at = 0; at < count;) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       P::template multiply<RB>(acc, st[d].r, st[d].w);
       __builtin_amdgcn_sched_barrier(0);
       load(st[d], ahead);
       const int was = seg;
-      if (move(seg, k)) {
+      if (move(seg, k) || at + 1 >= count) {
         const int pair = s.seg_pair[was], n = s.seg_pairs[was];
         f32x4 v;
         if constexpr (RB < 16)
@@ -782,7 +792,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, con
 #pragma unroll
         for (int j = 0; j < RowsOf<RB>::ACCS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-      if (seg >= segments) break;
+      if (++at >= count) break;
     }
   }
 }
