@@ -192,6 +192,13 @@ class EpCombine:
             raise ValueError(f"{name}: {t.numel()} elements, at least {elems} needed")
         return self._shape(t, name, t.shape, dtype)
 
+    def _output(self, t, name: str, shape: tuple, dtype, stream):
+        """(tensor, address) of an output: `t` checked, or a new one."""
+        if t is not None:
+            return t, self._shape(t, name, shape, dtype)
+        t = self._empty(shape, dtype, stream)
+        return t, t.data_ptr()
+
     def _workspace_bytes(self, call, tokens: int) -> int:
         """What `call` answers for so many tokens a rank, asked once."""
         need = self._workspaces.get((call, tokens))
@@ -303,24 +310,17 @@ class EpCombine:
         res_at = kept_at = out_at = codes_at = scales_at = None
         if residual is not None:
             res_at = self._shape(residual, "residual", shape, kept)
-            if residual_out is None:
-                residual_out = self._empty(shape, kept, stream)
-            kept_at = self._shape(residual_out, "residual_out", shape, kept)
+            residual_out, kept_at = self._output(residual_out, "residual_out", shape, kept, stream)
         elif residual_out is not None:
             raise ValueError("residual_out given without a residual")
         if rows:
-            if out is None:
-                out = self._empty(shape, x.dtype, stream)
-            out_at = self._shape(out, "out", shape, x.dtype)
+            out, out_at = self._output(out, "out", shape, x.dtype, stream)
         elif out is not None:
             raise ValueError("out given with rows=False")
         if fp8:
-            if codes is None:
-                codes = self._empty(shape, torch.uint8, stream)
-            if scales is None:
-                scales = self._empty((self.n_ranks, T, N // 128), torch.float32, stream)
-            codes_at = self._shape(codes, "codes", shape, torch.uint8)
-            scales_at = self._shape(scales, "scales", (self.n_ranks, T, N // 128), torch.float32)
+            codes, codes_at = self._output(codes, "codes", shape, torch.uint8, stream)
+            scales, scales_at = self._output(scales, "scales", (self.n_ranks, T, N // 128),
+                                             torch.float32, stream)
         elif codes is not None or scales is not None:
             raise ValueError("codes or scales given with fp8=False")
         elif not rows:
@@ -346,20 +346,15 @@ class EpCombine:
         res_at = both_at = None
         if grad_residual is not None:
             res_at = self._shape(grad_residual, "grad_residual", shape, sums.dtype)
-        if grad_x is None:
-            grad_x = self._empty(shape, grad_out.dtype, stream)
-        x_at = self._shape(grad_x, "grad_x", shape, grad_out.dtype)
+        grad_x, x_at = self._output(grad_x, "grad_x", shape, grad_out.dtype, stream)
         if sums.dtype != grad_out.dtype:
-            if grad_sums is None:
-                grad_sums = self._empty(shape, sums.dtype, stream)
-            both_at = self._shape(grad_sums, "grad_sums", shape, sums.dtype)
+            grad_sums, both_at = self._output(grad_sums, "grad_sums", shape, sums.dtype, stream)
         elif grad_sums is not None:
             raise ValueError("grad_sums given where grad_x serves for both")
         else:
             grad_sums = grad_x
-        if grad_weight is None:
-            grad_weight = self._empty((N,), torch.float32, stream)
-        grad_w_at = self._shape(grad_weight, "grad_weight", (N,), torch.float32)
+        grad_weight, grad_w_at = self._output(grad_weight, "grad_weight", (N,), torch.float32,
+                                              stream)
         need = self._workspace_bytes(B.ep_rms_norm_backward_workspace, T)
         workspace = self._empty((max(need, 16),), torch.uint8, stream)
         B.ep_rms_norm_backward(self.handle, params, at, res_at, sums_at, weight_at, T, x_at,
@@ -401,9 +396,7 @@ class EpCombine:
                                torch.float32)
         elif x_scale is not None or w1_scale is not None or w2_scale is not None:
             raise ValueError("scales are for fp8 handles (packed weights hold their own)")
-        if out is None:
-            out = self._empty(shape, torch.bfloat16, stream)
-        out_at = self._shape(out, "out", shape, torch.bfloat16)
+        out, out_at = self._output(out, "out", shape, torch.bfloat16, stream)
         need = self._workspace_bytes(B.ep_moe_layer_workspace, T)
         workspace = self._empty((max(need, 16),), torch.uint8, stream)
         B.ep_moe_layer(self.handle, format1, format2, at, x_scale_at, w1_at, s1_at, w2_at, s2_at,
