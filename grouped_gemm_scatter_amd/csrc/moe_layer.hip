@@ -23,16 +23,18 @@ namespace {
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kMaxSegments = kMaxLocalExperts + kMoeTokens;
 
-// The pairs of a launch.  A segment is up to ROWS pairs of one expert; pairs are numbered by
-// (expert, token).
+// The pairs of a launch, numbered by (expert, token).  A segment is up to ROWS pairs of one
+// expert.  Few and many pairs take different paths through the products, so that an
+// expert of many tokens does not slow down those of few.
+constexpr int kFew = 8;
 struct Table {
   uint64_t tokens[kMaxLocalExperts];   // expert e: its tokens
   int first[kMaxLocalExperts];         // its first pair
   int seg_expert[kMaxSegments], seg_pair[kMaxSegments], seg_pairs[kMaxSegments];
   int16_t pick[kMoePicks];             // local expert of a pick, or -1
   uint8_t token[kMoePicks];            // pair: its token
-  int segments;
-  int rows;                            // 4, 8, 16 or 32: what the largest segment needs
+  int few, segments;                   // segments of at most kFew pairs come first
+  int few_rows, many_rows;             // rows of the largest of either kind: 4, 8 and 16, 32
 };
 
 // Lanes below this one in a mask of lanes.
@@ -62,34 +64,43 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s, Weights*
   if (tid < 64) {
     // pairs and segments before each expert, 64 experts at a time: counts by their bits, each
     // a ballot (scans through LDS took a microsecond)
-    int pair = 0, seg = 0, rows = 4;
+    auto pairs_of = [&](int e) { return e < a.n_experts ? __popcll(s.tokens[e]) : 0; };
+    int few = 0, pair = 0, few_rows = 4, many_rows = 16;
     for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
-      const int e = e0 + tid;
-      const int n = e < a.n_experts ? __popcll(s.tokens[e]) : 0;
-      int pairs_before = pair, segs_before = seg;
+      const int n = pairs_of(e0 + tid);
+      few += __popcll(__ballot(n > 0 && n <= kFew));
+    }
+    int few_seg = 0, seg = few;
+    for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
+      const int e = e0 + tid, n = pairs_of(e);
+      int pairs_before = pair;
       for (int bit = 0; a.tokens >> bit; ++bit) {
         const uint64_t m = __ballot(n >> bit & 1);
         pairs_before += lanes_below(m) << bit;
         pair += __popcll(m) << bit;
       }
+      const uint64_t mine = __ballot(n > 0 && n <= kFew);
+      int at = n > kFew ? seg : few_seg + lanes_below(mine);
+      few_seg += __popcll(mine);
       for (int i = 0; i * ROWS < a.tokens; ++i) {
-        const uint64_t m = __ballot(n > i * ROWS);
-        segs_before += lanes_below(m);
+        const uint64_t m = __ballot(n > kFew && n > i * ROWS);
+        if (n > kFew) at += lanes_below(m);
         seg += __popcll(m);
       }
-      if (ROWS > 16 && __ballot(n > 16)) rows = 32;
-      if (__ballot(n > 8)) rows = max(rows, 16);
-      if (__ballot(n > 4)) rows = max(rows, 8);
+      if (__ballot(n > 4 && n <= kFew)) few_rows = 8;
+      if (ROWS > 16 && __ballot(n > 16)) many_rows = 32;
       if (e < a.n_experts) s.first[e] = pairs_before;
       for (int i = 0; i * ROWS < n; ++i) {
-        s.seg_expert[segs_before + i] = e;
-        s.seg_pair[segs_before + i] = pairs_before + i * ROWS;
-        s.seg_pairs[segs_before + i] = min(n - i * ROWS, ROWS);
+        s.seg_expert[at + i] = e;
+        s.seg_pair[at + i] = pairs_before + i * ROWS;
+        s.seg_pairs[at + i] = min(n - i * ROWS, ROWS);
       }
     }
     if (tid == 0) {
+      s.few = few;
       s.segments = seg;
-      s.rows = rows;
+      s.few_rows = few_rows;
+      s.many_rows = many_rows;
     }
   }
   __syncthreads();
@@ -566,7 +577,7 @@ __device__ __forceinline__ void lds_barrier() {
 // workgroup's reads of a row are one run.  The loads of the next item's first steps are
 // on their way while an item's sums are joined.
 template <class P, int RB>
-__device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
+__device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s, int seg0, int seg1,
                                          f32x4 (*s_part)[kWaves][2][RowsOf<RB>::BLOCKS][64]) {
   constexpr int BLOCKS = RowsOf<RB>::BLOCKS, ACCS = RowsOf<RB>::ACCS, BUFS = 2 / BLOCKS;
   constexpr int DEPTH = P::depth(RB);
@@ -574,7 +585,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int KT = a.hidden / 128, per = a.inter / 16;
-  const int items = __builtin_amdgcn_readfirstlane(s.segments) * per;
+  const int items = (seg1 - seg0) * per;
   struct Step {
     TwoBlocks<P> w;
     Rows r;
@@ -585,7 +596,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
     uint32_t gate, up, row[BLOCKS], scale_at[BLOCKS];
   };
   auto enter = [&](Place& p) {
-    const int item = min(p.item, items - 1), seg = item / per, b = item % per;
+    const int item = min(p.item, items - 1), seg = seg0 + item / per, b = item % per;
     const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
     const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
     const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
@@ -663,7 +674,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s,
 #pragma unroll
         for (int j = 0; j < ACCS; ++j) ag[j] = au[j] = f32x4{0.f, 0.f, 0.f, 0.f};
         lds_barrier();
-        const int seg = item / per, b = item % per;
+        const int seg = seg0 + item / per, b = item % per;
         const int pair = s.seg_pair[seg], n = s.seg_pairs[seg];
         // one value a thread: a pair's row and an output
         const int j = tid >> 8, l = (tid >> 2) & 63, i = tid & 3;
@@ -695,37 +706,44 @@ __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
   __shared__ Table s;
   __shared__ f32x4 s_part[1][kWaves][2][2][64];
   build_table<32>(a, s);
-  const int rows = __builtin_amdgcn_readfirstlane(s.rows);
-  typedef f32x4 (*Narrow)[kWaves][2][1][64];
-  if (rows <= 8 && (P::PAIR_A_LANE || rows == 8))
-    up_items<P, 8>(a, s, reinterpret_cast<Narrow>(s_part));
-  else if (rows == 4)
-    up_items<P, P::PAIR_A_LANE ? 8 : 4>(a, s, reinterpret_cast<Narrow>(s_part));
-  else if (rows == 16)
-    up_items<P, 16>(a, s, reinterpret_cast<Narrow>(s_part));
-  else
-    up_items<P, 32>(a, s, s_part);
+  const int few = __builtin_amdgcn_readfirstlane(s.few);
+  const int segments = __builtin_amdgcn_readfirstlane(s.segments);
+  typedef f32x4 (*OneBlock)[kWaves][2][1][64];
+  const OneBlock part = reinterpret_cast<OneBlock>(s_part);
+  if (few > 0) {
+    if (!P::PAIR_A_LANE && __builtin_amdgcn_readfirstlane(s.few_rows) == 4)
+      up_items<P, P::PAIR_A_LANE ? 8 : 4>(a, s, 0, few, part);
+    else
+      up_items<P, 8>(a, s, 0, few, part);
+  }
+  if (few < segments) {
+    __syncthreads();       // the sums of the last item are read
+    if (__builtin_amdgcn_readfirstlane(s.many_rows) == 16)
+      up_items<P, 16>(a, s, few, segments, part);
+    else
+      up_items<P, 32>(a, s, few, segments, s_part);
+  }
 }
 
 // ---- Down-projection and the weighted sum.  A workgroup takes 16 columns of the output; the
 // steps of all segments are one run that the waves split evenly.  A wave adds what it has of
 // a segment, times the pairs' weights, to its own sums of the tokens in LDS.
 // The segments are of at most 16 pairs: an expert's weights are read again for its next 16,
-// by the same workgroup and at once.  RB: the rows that the largest segment needs.
+// by the same workgroup and at once.
 template <class P, int RB>
-__device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, const float* weight,
-                                           float (*s_out)[16], int b, int wave, int lane) {
+__device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int seg0, int seg1,
+                                           const float* weight, float (*s_out)[16], int b, int wave,
+                                           int lane) {
   typedef typename P::template Rows<RB> Rows;
   const int KT = (a.inter + P::STEP - 1) / P::STEP;     // steps
   constexpr int DEPTH = P::depth(RB);
-  const int segments = __builtin_amdgcn_readfirstlane(s.segments);
   const uint32_t start = P::start(a.w2, b * 16, a.inter);
   struct Step {
     typename P::Block w;
     Rows r;
   };
   // A wave takes `count` of the steps of all segments, every eighth or a run of them.
-  const int steps = segments * KT;
+  const int steps = (seg1 - seg0) * KT;
   const int begin = P::SPREAD ? wave : wave * steps / kWaves;
   const int count = P::SPREAD ? (steps - wave + kWaves - 1) / kWaves
                               : (wave + 1) * steps / kWaves - begin;
@@ -745,7 +763,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, con
     uint32_t row[1];
   };
   auto enter = [&](Place& p) {
-    const int seg = min(p.seg, segments - 1);
+    const int seg = min(p.seg, seg1 - 1);
     const int e = __builtin_amdgcn_readfirstlane(s.seg_expert[seg]);
     const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
     const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
@@ -762,7 +780,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, con
   if (count <= 0) return;
   f32x4 acc[RowsOf<RB>::ACCS] = {};
   Step st[DEPTH];
-  int seg = begin / KT, k = begin % KT;
+  int seg = seg0 + begin / KT, k = begin % KT;
   Place ahead;
   ahead.seg = seg;
   ahead.k = k;
@@ -806,15 +824,17 @@ __global__ __launch_bounds__(kThreads, 4) void moe_down_kernel(MoeArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = lane; i < a.tokens * 16; i += 64) s_out[wave][i >> 4][i & 15] = 0.f;
   build_table<16>(a, s, &weights);
-  const int b = blockIdx.x, rows = __builtin_amdgcn_readfirstlane(s.rows);
-  if (__builtin_amdgcn_readfirstlane(s.segments) > 0) {
-    if (rows == 4)
-      down_steps<P, 4>(a, s, weights.pair, s_out[wave], b, wave, lane);
-    else if (rows == 8)
-      down_steps<P, 8>(a, s, weights.pair, s_out[wave], b, wave, lane);
+  const int b = blockIdx.x;
+  const int few = __builtin_amdgcn_readfirstlane(s.few);
+  const int segments = __builtin_amdgcn_readfirstlane(s.segments);
+  if (few > 0) {
+    if (__builtin_amdgcn_readfirstlane(s.few_rows) == 4)
+      down_steps<P, 4>(a, s, 0, few, weights.pair, s_out[wave], b, wave, lane);
     else
-      down_steps<P, 16>(a, s, weights.pair, s_out[wave], b, wave, lane);
+      down_steps<P, 8>(a, s, 0, few, weights.pair, s_out[wave], b, wave, lane);
   }
+  if (few < segments)
+    down_steps<P, 16>(a, s, few, segments, weights.pair, s_out[wave], b, wave, lane);
   __syncthreads();
   for (int i = tid; i < a.tokens * 8; i += kThreads) {
     const int t = i >> 3, c = (i & 7) * 2;

@@ -493,3 +493,29 @@ def test_handles_that_cannot():
     with pytest.raises(EpError) as e:
         odd.moe_layer(xb, w, w, ids, ids.float())
     assert e.value.code == B.EP_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "bf16_sliced", "fp8", ("int4", 128, "bf16"),
+                                 ("e2m1", 32, "f16")], ids=_id)
+@pytest.mark.parametrize("counts", [[1, 4, 5, 8], [9, 16, 0, 2], [17, 32, 33, 64],
+                                    [1, 0, 3, 40, 7, 12, 64, 31], [64], [8, 4, 0, 0, 0, 15]],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_experts_of_few_and_of_many_tokens_together(fmt, counts):
+    """Every number of rows that the products tell apart, alone and beside the others."""
+    k = len(counts)
+
+    def edit(ids, tw):
+        # pick j of the first counts[j] tokens is expert j, in another order for each
+        ids[...] = -1
+        for j, n in enumerate(counts):
+            ids[0, np.random.default_rng(j).permutation(64)[:n], j] = k - 1 - j
+    _run(fmt, 1, 64, k, k, 256, 384, edit=edit)
+
+
+@pytest.mark.parametrize("El", [65, 130, 256])
+def test_few_and_many_tokens_among_many_experts(El):
+    def edit(ids, tw):
+        ids[0, :, 0] = El - 1                      # all tokens
+        ids[0, ::3, 1] = 63                        # 22
+        ids[0, 5::7, 1] = 64                       # 9
+    _run(("e2m1", 64, "bf16"), 1, 64, El, 6, 128, 128, edit=edit)
