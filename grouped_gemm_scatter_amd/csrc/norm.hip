@@ -9,6 +9,11 @@
 // values in registers between the sum over the row and their use, so that every input is
 // read once; what a row has beyond that (more than 16384 values, EXTRA) is read again.
 // A 128-value block of 8-bit output is 16 neighbouring lanes' chunks.
+//
+// What they measured: 32768 rows of 7168 bf16 values, residual in and out, rows and codes out
+// (2.12 GB): 373 us, 5.7 TB/s, 95% of the rate of a plain copy (four chunks a thread: 422, three
+// waves a SIMD instead of seven).  Their gradient (1.88 GB): 336 us, 5.6 TB/s, and 7 for
+// the sum of the partial rows.  One row: 4.5 us, a launch and two dependent trips to memory.
 #include <algorithm>
 
 #include "ep_combine.h"

@@ -600,8 +600,10 @@ EP_API int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format
      scales[b] = max |y| / 448 over the 128 values of block b (1 if all are zero, at least
                  2^-126), codes = e4m3fn(y / scales[b]), rounded to nearest even
    everything in binary32 until those roundings (the norm is of s before its rounding).
-   The sum of squares is binary32 too: beyond its range it is infinite and y zero, and
-   an infinity or a NaN in a row makes that row's y NaN, and no other's. */
+   The sum of squares is binary32 too: beyond its range it is infinite and y zero.  A NaN
+   in a row makes all of that row's y NaN, an infinity its own and the others zero (no other
+   row is touched), and so does a row of zeros with eps = 0 (NaN).  A NaN has the code 0x7f
+   or 0xff and no part in its block's scale. */
 #define EP_ROWS_F32 0
 #define EP_ROWS_BF16 1
 #define EP_ROWS_F16 2
@@ -668,7 +670,8 @@ EP_API int64_t ep_rms_norm_backward_workspace(ep_combine_t h, int32_t tokens_per
    product's rows not rounded.  (On fp8 handles silu(g) * u is not put into 8 bits again.)
    A token without local picks gets +0; picks of the same expert by one token add up.
    Neither rows nor weights of one expert change what a token without it gets, not even
-   by infinities or NaN.
+   by infinities or NaN.  Right for any routing; where experts have over about twelve
+   tokens each, the grouped calls are as fast.
    format1, format2  NULL for weights in the handle's dtype, or the formats of 4-bit
             weights packed by ep_pack_weights_w4 (bf16 handles; both or neither).
    x        device, [R][tokens_per_rank][hidden] bf16, or with an fp8 handle e4m3fn codes

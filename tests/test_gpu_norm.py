@@ -260,6 +260,37 @@ def test_a_residual_that_is_x():
     assert torch.equal(got.out, want.out) and torch.equal(got.residual, want.residual)
 
 
+def test_sums_without_a_residual():
+    """At the C boundary: the stored sums are x, in the residual's type."""
+    x, _, w = _inputs(1, 7, 640, ("f16", None, "f16"), 14)
+    ctx = _ctx(1, 7, 640)
+    for t in (torch.float16, torch.float32):
+        p = B.make_norm_params(dtype=torch.float16, residual_dtype=t)
+        kept = torch.empty(1, 7, 640, dtype=t, device="cuda")
+        out = torch.empty_like(x)
+        B.ep_rms_norm(ctx.handle, p, x, None, w, 7, kept, out, None, None)
+        assert torch.equal(kept, x.to(t))
+        assert torch.equal(out, ctx.rms_norm(x, w, eps=1e-6).out)
+
+
+def test_no_eps_and_values_out_of_range():
+    """eps = 0 on a row of zeros, squares past binary32, an infinity, a NaN: as documented."""
+    x = torch.ones(1, 5, 256, device="cuda")
+    x[0, 0] = 0
+    x[0, 1] = 3e19
+    x[0, 2, 7] = float("inf")
+    x[0, 3, 200] = float("nan")
+    w = torch.full((256,), 2.0, device="cuda")
+    y = _ctx(1, 5, 256).rms_norm(x, w, eps=0.0, fp8=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(y.out[0, 0]).all() and torch.all(y.out[0, 1] == 0)
+    assert torch.isnan(y.out[0, 2, 7]) and torch.all(y.out[0, 2, :7] == 0)
+    assert torch.isnan(y.out[0, 3]).all() and torch.all(y.out[0, 4] == 2)
+    assert torch.all((y.codes[0, 3] & 0x7F) == 0x7F) and torch.all((y.codes[0, 0] & 0x7F) == 0x7F)
+    assert (y.codes[0, 2, 7] & 0x7F) == 0x7F and torch.all(y.codes[0, 2, 8:] == 0)
+    assert torch.all(y.scales[0, :4] == 1) and torch.all(y.scales[0, 4] == np.float32(2) / 448)
+
+
 def test_no_tokens():
     ctx = _ctx(2, 4, 256)
     x = torch.empty(2, 0, 256, dtype=torch.bfloat16, device="cuda")
