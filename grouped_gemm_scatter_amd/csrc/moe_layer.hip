@@ -187,7 +187,7 @@ __device__ __forceinline__ f32x4 add_row_parts(const f32x4 (&acc)[RowsOf<RB>::AC
   return v;
 }
 
-// Rows in bf16, k = STRIDE q + 8 (L / 16) .. + 7 for quarter q (bytes: see at()).
+// Rows in bf16: 8 values a lane of each quarter of a step's 128 k (where they lie: at()).
 template <int RB>
 struct Bf16Rows {
   u32x4 v[RB < 16 ? RB / 4 : 4 * RowsOf<RB>::BLOCKS];
@@ -224,8 +224,11 @@ struct TwoBlocks {
 struct Bf16 {
   static constexpr int STEP = 128;                 // k of a step of the down-projection
   static constexpr bool SPREAD = true;             // its steps: every eighth, or a run
-  // steps in flight, as many as 128 registers hold
-  static constexpr int depth(int rows) { return rows > 16 ? 1 : 2; }
+  // Steps on their way beside the one that is multiplied.  One serves where sixteen waves a CU
+  // hold 2 to 8 KB each (two and three were as fast or up to 5% slower in every product,
+  // 4-bit: 77 and 74 us up); in bf16 down, one took 48.9 us where two take 43.8 (one token
+  // of 7168 x 2048; 16 of 4096 x 1024: 24.5 and 25.6).
+  static constexpr int UP_DEPTH = 1, DOWN_DEPTH = 2;
   static constexpr bool PAIR_A_LANE = false;
   struct Source {
     const uint8_t* w;
@@ -350,7 +353,7 @@ struct Fp8 {
 // Rows of codes with a scale for 128 of them: the up-projection.  The weights are the
 // first operand, so that a lane's results are of one pair, whose scale it has loaded.
 struct Fp8Up : Fp8 {
-  static constexpr int depth(int rows) { return rows > 16 ? 2 : 3; }
+  static constexpr int UP_DEPTH = 1;
   static constexpr bool PAIR_A_LANE = true;
   // a row's 128 bytes of a step are two halves of k; with 8 rows a lane loads one of them
   template <int RB>
@@ -406,23 +409,52 @@ struct Fp8Up : Fp8 {
   }
 };
 
-// Rows in bf16: the down-projection, the codes converted (exactly).
+// Rows in bf16: the down-projection, the codes converted (exactly).  A step is 256 k, whose
+// two scales come with one load (as with the 4-bit weights below); the second 128 may lie
+// past the end.
 struct Fp8Down : Fp8 {
-  static constexpr int STEP = 128;
+  static constexpr int STEP = 256;
   static constexpr bool SPREAD = true;
-  static constexpr int depth(int) { return 3; }
-  template <int RB> using Rows = Bf16Rows<RB>;
+  static constexpr int DOWN_DEPTH = 1;
+  struct Block {
+    u32x4 v[2][2];
+    uint32_t s;
+  };
+  template <int RB>
+  struct Rows {
+    Bf16Rows<RB> r[2];
+    static __device__ __forceinline__ int quarter(int lane) { return Bf16Rows<RB>::quarter(lane); }
+  };
+  static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t row0, int k,
+                                              int length) {
+    const int second = length & buffer_length(2 * k + 1, s.kb);
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const buffer w = make_buffer(s.w, o ? second : length);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        in_order(b.v[o][i] = buffer_load16(w, s.lane + i * 64, (row0 * s.kb + 2 * k + o) * 128));
+    }
+    in_order(buffer_load_to(b.s, make_buffer(s.s, length), odd_lanes() & second & 4,
+                            ((row0 >> 7) * s.kb + 2 * k) * 4));
+  }
+  static __device__ __forceinline__ int odd_lanes() { return -((int)(threadIdx.x >> 4) & 1); }
   static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
     return (lane >> 4) * 32 + (quarter >> 1) * 128 + (quarter & 1) * 16;
   }
   template <int RB>
-  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, const uint8_t* x0, int length,
+  static __device__ __forceinline__ void load_rows(Rows<RB>& r, const uint8_t* x0, int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
-                                                   int kt, int) {
-    const buffer x = make_buffer(x0, length);
+                                                   int k, int inter) {
 #pragma unroll
-    for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
-      in_order(r.v[q] = buffer_load16(x, row[0] + (q >> 1) * 128 + (q & 1) * 16, kt * 256));
+    for (int o = 0; o < 2; ++o) {
+      const buffer x =
+          make_buffer(x0, o ? length & buffer_length(2 * k + 1, inter / 128) : length);
+#pragma unroll
+      for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
+        in_order(r.r[o].v[q] = buffer_load16(x, row[0] + (q >> 1) * 128 + (q & 1) * 16,
+                                             (2 * k + o) * 256));
+    }
   }
   static __device__ __forceinline__ bf16x8 values(uint32_t lo, uint32_t hi) {
     const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, 0);
@@ -433,11 +465,16 @@ struct Fp8Down : Fp8 {
   }
   template <int RB>
   static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                  const Bf16Rows<RB>& r, const Block& b) {
-    const float ws = __builtin_bit_cast(float, b.s);
-    scaled_multiply<RB, 4>(
-        acc, r, [&](int q) { return values(b.v[q >> 1][2 * (q & 1)], b.v[q >> 1][2 * (q & 1) + 1]); },
-        [&](int) { return ws; });
+                                                  const Rows<RB>& r, const Block& b) {
+    const auto s = __builtin_amdgcn_permlane16_swap(b.s, b.s, false, false);
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const float ws = __uint_as_float(s[o]);
+      scaled_multiply<RB, 4>(
+          acc, r.r[o],
+          [&](int q) { return values(b.v[o][q >> 1][2 * (q & 1)], b.v[o][q >> 1][2 * (q & 1) + 1]); },
+          [&](int) { return ws; });
+    }
   }
 };
 
@@ -452,9 +489,7 @@ template <class F>
 struct W4 {
   static constexpr uint32_t SB = 16 * (128 / F::GROUP) * 2;   // scale bytes of a run
   static constexpr bool PAIR_A_LANE = false;
-  static constexpr int depth(int rows) {
-    return rows > 16 ? 1 : rows > 8 || F::GROUP == 32 ? 2 : 3;
-  }
+  static constexpr int UP_DEPTH = 1;
   typedef typename F::word word;
   struct Source {
     const uint8_t *w, *s;
@@ -542,7 +577,7 @@ struct W4Down : W4<F> {
   typedef W4<F> P;
   typedef typename P::word word;
   typedef typename P::Source Source;
-  static constexpr int depth(int rows) { return rows > 8 ? 1 : 2; }
+  static constexpr int DOWN_DEPTH = 1;
   static constexpr int STEP = 256;
   static constexpr bool SPREAD = false;
   struct Block {
@@ -596,7 +631,7 @@ template <class P, int RB>
 __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s, int seg0, int seg1,
                                          f32x4 (*s_part)[kWaves][2][RowsOf<RB>::BLOCKS][64]) {
   constexpr int BLOCKS = RowsOf<RB>::BLOCKS, ACCS = RowsOf<RB>::ACCS, BUFS = 2 / BLOCKS;
-  constexpr int DEPTH = P::depth(RB);
+  constexpr int DEPTH = P::UP_DEPTH;
   typedef typename P::template Rows<RB> Rows;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -752,7 +787,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int
                                            int lane) {
   typedef typename P::template Rows<RB> Rows;
   const int KT = (a.inter + P::STEP - 1) / P::STEP;     // steps
-  constexpr int DEPTH = P::depth(RB);
+  constexpr int DEPTH = P::DOWN_DEPTH;
   const uint32_t start = P::start(a.w2, b * 16, a.inter);
   struct Step {
     typename P::Block w;
