@@ -16,15 +16,15 @@
 // up-projection stores; the down-projection's sums are rounded once, as the output.
 //
 // What it measured (kernels alone, us up and down; the bytes at the 5.95 TB/s of a plain copy):
-//   one token, 8 experts of 7168 x 2048    bf16  80 + 44 (118)   fp8 45 + 28 (59)
-//                                          int4, groups of 128   28 + 19 (31)
-//   five tokens of the same in fp8, 25 experts             139 + 80 (185)
-//   64 tokens, 28 of 32 experts, e2m1, groups of 32         76 + 54 (116)
+//   one token, 8 experts of 7168 x 2048    bf16  80 + 44 (118)   fp8 44 + 26 (59)
+//                                          int4, groups of 128   27 + 18 (31)
+//   five tokens of the same in fp8, 25 experts             139 + 78 (185)
+//   64 tokens, 28 of 32 experts, e2m1, groups of 32         74 + 53 (116)
 //   16 tokens, 14 of 16 experts of 4096 x 1024, bf16        46 + 25 (60)
-//   one token, 2 experts of 1024 x 256, bf16                 7 + 5: launches and latency
-// Large up-projections run at 5.2 to 6.0 TB/s, down-projections at 4.3 to 5.3.  Of one int4 token's 47 us, 12 are the two
-// launches' starts (picks, table, the first weights), and its vector instructions, most of
-// them code conversions, are 16 of the 28 of the up-projection.
+//   one token, 2 experts of 1024 x 256, bf16                 6 + 5: launches and latency
+// Large up-projections run at 5.2 to 6.2 TB/s, down-projections at 4.3 to 5.3.  Of one int4
+// token's 45 us, 12 are the two launches' starts (picks, table, the first weights), and its
+// vector instructions, most of them code conversions, are 16 of the 27 of the up-projection.
 // With over about 12 tokens an expert the grouped products are as fast (64 tokens with every
 // one of 32 experts: bf16 701 us here, 647 there; fp8 447 and 402; int4 303 and 205; 32
 // tokens: 570 and 645, 339 and 399, 204 and 190).
