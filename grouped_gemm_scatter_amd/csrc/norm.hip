@@ -3,7 +3,7 @@
 //
 //   s = x + residual (binary32, or x),   inv = 1 / sqrt(mean(s^2) + eps),   y = s inv w
 //   with r the stored sums and g, h the gradients of y and of the stored sums:
-//   dr = inv (g w - r inv^2 mean(g w r)) + h,   dw = sum over rows of g r inv
+//   dr = inv (g w - (r inv) (inv mean(g w r))) + h,   dw = sum over rows of g r inv
 //
 // Both are HBM streams.  A row is spread over TPR threads, a thread holding kHeld chunks of 8
 // values in registers between the sum over the row and their use, so that every input is
@@ -303,7 +303,9 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
       }
     row_sums<TPR>(sums, s_sum, parity);
     const float inv = inverse_rms(sums[0], a.N, a.eps);
-    const float shift = inv * inv * (sums[1] / (float)a.N);    // mean(g w r) inv^2
+    // inv^2 itself may be past binary32 (rows of rms under 2^-64 with an eps as small): one
+    // factor goes to the mean, the other to r
+    const float shift = inv * (sums[1] / (float)a.N);
 
     auto finish = [&](int c, const Chunk<XT>& gk, const Chunk<RT>& rk, const Chunk<RT>& hk,
                       float (&dwc)[8]) {
@@ -314,8 +316,9 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_backward_kernel(NormArgs
       load_weight<XT>(d, a, c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        d[i] = inv * __builtin_fmaf(gv[i], d[i], -rv[i] * shift) + hv[i];
-        dwc[i] = __builtin_fmaf(gv[i], rv[i] * inv, dwc[i]);
+        const float xh = rv[i] * inv;
+        d[i] = inv * __builtin_fmaf(gv[i], d[i], -xh * shift) + hv[i];
+        dwc[i] = __builtin_fmaf(gv[i], xh, dwc[i]);
       }
       if (a.grad_x) {
         Chunk<XT> k;

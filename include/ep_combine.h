@@ -600,7 +600,9 @@ EP_API int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format
      scales[b] = max |y| / 448 over the 128 values of block b (1 if all are zero, at least
                  2^-126), codes = e4m3fn(y / scales[b]), rounded to nearest even
    everything in binary32 until those roundings (the norm is of s before its rounding).
-   The sum of squares is binary32 too: beyond its range it is infinite and y zero.  A NaN
+   The sum of squares is binary32 too: beyond its range it is infinite and y zero, and
+   squares under its normal numbers (values under 2^-63, which count only beside an eps as
+   small as their square) lose bits, under 2^-75 all of them.  A NaN
    in a row makes all of that row's y NaN, an infinity its own and the others zero (no other
    row is touched), and so does a row of zeros with eps = 0 (NaN).  A NaN has the code 0x7f
    or 0xff and no part in its block's scale. */
@@ -636,9 +638,9 @@ EP_API int ep_rms_norm(ep_combine_t h, const ep_norm_params* params, const void*
 
 /* Gradient of ep_rms_norm.  With r the stored sums (residual_out, or x without a residual),
    g the gradient of y and q that of residual_out, inv = 1 / sqrt(mean(r^2) + eps):
-     ds = inv * (g * w - r * inv^2 * mean(g * w * r)) + q
+     ds = inv * (g * w - (r * inv) * (inv * mean(g * w * r))) + q
      grad_weight = sum over all rows of g * r * inv
-   in binary32.  x and the residual are the two terms of s, so ds is the gradient of both:
+   in binary32, products as they stand in brackets (inv^2 alone may be past the range).  x and the residual are the two terms of s, so ds is the gradient of both:
    grad_x is ds in dtype, grad_residual in residual_dtype (where the types are one, one
    of the two serves).  The codes' rounding has no gradient: g is that of the values they
    stand for.
