@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import functools
 from dataclasses import dataclass
+from operator import index
 from typing import NamedTuple
 
 import torch
@@ -27,7 +28,8 @@ def _choice(table: dict, value, name: str) -> int:
 def _route_params(n_experts, logits_dtype, n_groups, topk_groups, score, group_score, renormalize,
                   scale):
     """The options of a routing call as the C boundary takes them (never changed, so one
-    object serves every call with the same options)."""
+    object serves every call with the same options).  Callers pass plain numbers: a tensor
+    would be remembered by its identity, whatever it holds later."""
     return B.make_route_params(
         n_experts=n_experts, logits_dtype=logits_dtype, n_groups=n_groups,
         topk_groups=topk_groups, score=_choice(_SCORES, score, "score"),
@@ -37,7 +39,7 @@ def _route_params(n_experts, logits_dtype, n_groups, topk_groups, score, group_s
 
 @functools.lru_cache(maxsize=64)
 def _norm_params(dtype, residual_dtype, weight_dtype, eps):
-    """The options of a norm as the C boundary takes them."""
+    """The options of a norm as the C boundary takes them (eps a plain number, as above)."""
     return B.make_norm_params(dtype=dtype, residual_dtype=residual_dtype,
                               weight_dtype=weight_dtype, eps=eps)
 
@@ -225,8 +227,8 @@ class EpCombine:
         topk_groups best groups are picked from, by their largest choice ("max") or the
         sum of their two largest ("top2")."""
         R, T, E = logits.shape
-        params = _route_params(E, logits.dtype, n_groups, topk_groups, score, group_score,
-                               renormalize, scale)
+        params = _route_params(E, logits.dtype, index(n_groups), index(topk_groups), score,
+                               group_score, int(renormalize), float(scale))
         shape = (self.n_ranks, T, self.top_k)
         at = self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
         bias_at = None if bias is None else self._shape(bias, "bias", (E,), torch.float32)
@@ -248,7 +250,7 @@ class EpCombine:
         """Gradient of `route`'s topk_w with respect to its logits (in their type), from
         the picks it returned and the gradient grad_w [R][T][top_k] of their weights."""
         R, T, E = logits.shape
-        params = _route_params(E, logits.dtype, 1, 1, score, "max", renormalize, scale)
+        params = _route_params(E, logits.dtype, 1, 1, score, "max", int(renormalize), float(scale))
         shape = (self.n_ranks, T, self.top_k)
         at = self._shape(logits, "logits", (self.n_ranks, T, E), logits.dtype)
         ids_at = self._shape(topk_ids, "topk_ids", shape, torch.int32)
@@ -304,7 +306,7 @@ class EpCombine:
         T, N = x.shape[1], self.hidden_n
         shape = (self.n_ranks, T, N)
         kept = x.dtype if residual is None else residual.dtype
-        params = _norm_params(x.dtype, kept, weight.dtype, eps)
+        params = _norm_params(x.dtype, kept, weight.dtype, float(eps))
         at = self._shape(x, "x", shape, x.dtype)
         weight_at = self._shape(weight, "weight", (N,), weight.dtype)
         res_at = kept_at = out_at = codes_at = scales_at = None
@@ -339,7 +341,7 @@ class EpCombine:
         float32 too.  grad_x may be grad_out itself, grad_sums grad_residual itself."""
         T, N = grad_out.shape[1], self.hidden_n
         shape = (self.n_ranks, T, N)
-        params = _norm_params(grad_out.dtype, sums.dtype, weight.dtype, eps)
+        params = _norm_params(grad_out.dtype, sums.dtype, weight.dtype, float(eps))
         at = self._shape(grad_out, "grad_out", shape, grad_out.dtype)
         sums_at = self._shape(sums, "sums", shape, sums.dtype)
         weight_at = self._shape(weight, "weight", (N,), weight.dtype)
