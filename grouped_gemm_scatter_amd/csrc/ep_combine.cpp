@@ -15,6 +15,7 @@
 
 #include "combine_common.h"
 #include "ep_kernels.h"
+#include "layer_kernels.h"
 
 // Counters of ep_grouped_gemm_scatter_noalloc: R election counters, then E_l
 // per-expert tile counters (the roles of ep_combine_buffers.rank_counter and

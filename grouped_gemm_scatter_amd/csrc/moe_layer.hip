@@ -31,6 +31,7 @@
 #include <algorithm>
 
 #include "ep_kernels.h"
+#include "layer_kernels.h"
 #include "w4_device.h"
 
 namespace ep {

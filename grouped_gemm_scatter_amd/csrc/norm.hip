@@ -18,6 +18,7 @@
 
 #include "ep_combine.h"
 #include "ep_kernels.h"
+#include "layer_kernels.h"
 
 namespace ep {
 namespace {
