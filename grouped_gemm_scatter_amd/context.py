@@ -194,6 +194,13 @@ class EpCombine:
             raise ValueError(f"{name}: {t.numel()} elements, at least {elems} needed")
         return self._shape(t, name, t.shape, dtype)
 
+    def _tokens(self, t, name: str) -> int:
+        """T of a tensor [R][T][hidden_n]; raises unless it has those three dimensions."""
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [{self.n_ranks}][T][{self.hidden_n}], "
+                             f"got {list(t.shape)}")
+        return t.shape[1]
+
     def _output(self, t, name: str, shape: tuple, dtype, stream):
         """(tensor, address) of an output: `t` checked, or a new one."""
         if t is not None:
@@ -269,7 +276,7 @@ class EpCombine:
         [m_total][hidden_n] bfloat16) from grad_out [R][T][hidden_n] and what the step left
         in the receive buffers.  `grad_rows` may be a buffer of more rows, whose rows from
         m_total on stay as they are; rows=False leaves it out (None is returned)."""
-        T, N, m = grad_out.shape[1], self.hidden_n, int(m_total)
+        T, N, m = self._tokens(grad_out, "grad_out"), self.hidden_n, int(m_total)
         shape = (self.n_ranks, T, self.top_k)
         at = self._shape(grad_out, "grad_out", (self.n_ranks, T, N), torch.bfloat16)
         ids_at = self._shape(topk_ids, "topk_ids", shape, torch.int32)
@@ -303,7 +310,7 @@ class EpCombine:
         pass for both; rows=False leaves the rows out).  `weight` [hidden_n] in x's type or
         float32.  Results go into tensors that are given; residual_out may be `residual`
         itself and out `x` itself."""
-        T, N = x.shape[1], self.hidden_n
+        T, N = self._tokens(x, "x"), self.hidden_n
         shape = (self.n_ranks, T, N)
         kept = x.dtype if residual is None else residual.dtype
         params = _norm_params(x.dtype, kept, weight.dtype, float(eps))
@@ -339,7 +346,7 @@ class EpCombine:
         `sums` are (x itself without a residual).  The gradient of the sum is that of x and
         of the residual: in x's type, and where the sums are float32 beside 16-bit rows in
         float32 too.  grad_x may be grad_out itself, grad_sums grad_residual itself."""
-        T, N = grad_out.shape[1], self.hidden_n
+        T, N = self._tokens(grad_out, "grad_out"), self.hidden_n
         shape = (self.n_ranks, T, N)
         params = _norm_params(grad_out.dtype, sums.dtype, weight.dtype, float(eps))
         at = self._shape(grad_out, "grad_out", shape, grad_out.dtype)
@@ -372,7 +379,8 @@ class EpCombine:
         [E_l][hidden_n][hidden_k] in bfloat16 (w2 from pack_weights where the handle has
         w_slice_major), or both from pack_weights_w4; with an fp8 handle uint8 e4m3fn codes
         with w1_scale and w2_scale, and x uint8 codes with x_scale, as `rms_norm` makes them."""
-        T, N, inter, El = x.shape[1], self.hidden_n, self.hidden_k, self.n_experts_per_device
+        T, N = self._tokens(x, "x"), self.hidden_n
+        inter, El = self.hidden_k, self.n_experts_per_device
         fp8 = self.dtype == "fp8"
         row_type = torch.uint8 if fp8 else torch.bfloat16
         shape, picks = (self.n_ranks, T, N), (self.n_ranks, T, self.top_k)

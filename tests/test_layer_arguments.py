@@ -57,3 +57,15 @@ def test_options_of_any_number_type(ctx):
     for bad in (1.5, "2"):
         with pytest.raises(TypeError):
             ctx.route(x, n_groups=bad)
+
+
+@pytest.mark.parametrize("shape", [(), (128,), (3, 128), (1, 1, 3, 128)])
+def test_rows_of_other_than_three_dimensions(ctx, shape):
+    t = torch.zeros(shape, dtype=torch.bfloat16)
+    w, ids = torch.zeros(128), torch.zeros(1, 3, 2, dtype=torch.int32)
+    for call, name in ((lambda: ctx.rms_norm(t, w), "x"),
+                       (lambda: ctx.rms_norm_backward(t, t, w), "grad_out"),
+                       (lambda: ctx.moe_layer(t, t, t, ids, w), "x"),
+                       (lambda: ctx.combine_backward(t, ids, w, None, None, 0), "grad_out")):
+        with pytest.raises(ValueError, match=rf"{name} must be \[1\]\[T\]\[128\]"):
+            call()
