@@ -435,23 +435,37 @@ void launch_types(const NormArgs& a, bool backward, int tpr, int grid, hipStream
   launch_one<1024, XT, RT, STREAM, true>(a, backward, grid, st);
 }
 
-// Rows of more than this many bytes in all go past the caches' replacement.  Measured on rows
-// of 7168 bf16 values with a residual, us of the norm and of its gradient, streamed and not:
-//    59 MB   13.0 and 12.2    27.1 and 22.8
-//   117 MB   22.7 and 25.6    38.0 and 36.4
-//   235 MB   41.2 and 45.4    58.0 and 57.6
-//   470 MB   82.0 and 87.8    97.3 and 100.6
-// (the loads and stores of 32-bit values, half of every 32 bytes each, never do: 159 MB of
-// which two thirds are such 34.6 and 28.8)
-constexpr int64_t kStreamBytes = 96 << 20;
+// Bytes of the rows that a call reads and writes.
+int64_t moved_bytes(const NormArgs& a, bool backward) {
+  const int64_t x = a.dtype == EP_ROWS_F32 ? 4 : 2, s = a.sum_dtype == EP_ROWS_F32 ? 4 : 2;
+  const int64_t value =
+      backward ? x + s + (a.grad_residual ? s : 0) + (a.grad_x ? x : 0) + (a.grad_sum ? s : 0)
+               : x + (a.residual ? s : 0) + (a.residual_out ? s : 0) + (a.out ? x : 0) +
+                     (a.codes ? 1 : 0);
+  return a.rows * a.N * value;
+}
+
+// Calls that move more than this go past the caches' replacement: the loads and stores of
+// 16-bit values, whole lines.  (Those of 32-bit values, half of every 32 bytes each, never
+// do.)  Measured on rows of 7168 values, us streamed and not, by the bytes moved:
+//                      79 MB          99 MB          119 MB         159 MB         479 MB
+//   norm, bf16
+//     alone            17.2 and 16.9  20.7 and 22.9  23.4 and 25.5  30.9 and 33.1   87.3 and  92.3
+//     with a residual  16.5 and 15.7  19.8 and 22.5  23.0 and 27.2  29.4 and 34.0   83.4 and  88.9
+//     and codes        19.2 and 18.1  23.3 and 25.4  26.4 and 29.8  32.9 and 36.4   84.1 and  92.4
+//     beside fp32 sums 17.4 and 16.5  20.3 and 21.4  24.3 and 28.9  34.0 and 35.6   87.2 and  89.9
+//   gradient, bf16
+//     alone            33.8 and 30.2  37.7 and 36.9  40.8 and 39.5  48.7 and 47.8  110.7 and 113.0
+//     with a residual  32.0 and 27.4  34.2 and 31.9  38.7 and 38.0  44.5 and 44.3   98.8 and 102.9
+//     beside fp32 sums 24.7 and 21.5  27.8 and 24.1  31.7 and 32.6  37.8 and 39.7   83.3 and  84.5
+constexpr int64_t kStreamNorm = 88 << 20, kStreamGradient = 128 << 20;
 
 template <int XT, int RT>
 void launch_types(const NormArgs& a, bool backward, int tpr, int grid, hipStream_t st) {
-  const int64_t value = 2 * Chunk<XT>::BYTES / 8 + 2 * Chunk<RT>::BYTES / 8;
-  if (a.rows * a.N * value >= kStreamBytes)
-    launch_types<XT, RT, true>(a, backward, tpr, grid, st);
-  else
-    launch_types<XT, RT, false>(a, backward, tpr, grid, st);
+  if constexpr (XT != EP_ROWS_F32)
+    if (moved_bytes(a, backward) >= (backward ? kStreamGradient : kStreamNorm))
+      return launch_types<XT, RT, true>(a, backward, tpr, grid, st);
+  launch_types<XT, RT, false>(a, backward, tpr, grid, st);
 }
 
 hipError_t launch(const NormArgs& a, bool backward, int tpr, int grid, hipStream_t st) {
