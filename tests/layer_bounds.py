@@ -1,6 +1,7 @@
 """Measures of error for the norm's gradient and the few-token layer that a wrong kernel
 cannot meet: tests of the kernels and of the measures themselves share them."""
 import numpy as np
+import torch
 
 
 def along_rows(norm, gradient, r, w, g, eps, h=2.0 ** -6):
@@ -35,3 +36,42 @@ def gradient_inputs(rows, N, seed):
     w = (0.8 + 0.4 * rng.random(N)).astype(np.float32).astype(np.float64)
     g = (r * w + rng.standard_normal((rows, N))).astype(np.float32).astype(np.float64)
     return r, w, g
+
+
+def layer(x, w1, w2, ids, topk_w, expert_lo=0):
+    """(out, spread) of the few-token layer in float64 torch tensors, on any device: tokens x
+    [n][hidden] with picks ids and weights topk_w [n][k], lists (or functions) w1 and w2 of
+    the local experts' weights.  spread [n][hidden] is the root of the sum of the squares of
+    the terms c w2 h that make an output."""
+    out, square = torch.zeros_like(x), torch.zeros_like(x)
+    for e in range(len(w1)):
+        share = (topk_w * (ids == e + expert_lo)).sum(-1, dtype=torch.float64)
+        t = torch.nonzero((ids == e + expert_lo).any(-1)).flatten()
+        if t.numel() == 0:
+            continue
+        a, b = w1[e].double(), w2[e].double()
+        y = torch.mm(a, x[t].t().contiguous())
+        h = y[:len(y) // 2] / (1 + torch.exp(-y[:len(y) // 2])) * y[len(y) // 2:]
+        out[t] += share[t, None] * torch.mm(b, h).t()
+        square[t] += share[t, None] ** 2 * torch.mm(b * b, h * h).t()
+    return out, square.sqrt()
+
+
+def layer_error(got, want, spread):
+    """How far `got` is off as a part of what is allowed (at most 1 is right).
+
+    A token's whole error: the output's rounding is within 2^-8 of each value, and that of
+    the hidden values to bf16 within 2^-8 of each, which the random weights of the second
+    product carry to 2^-8 of the output's length within a sixth (5 deviations of a sum of
+    1000 squares, above and below): under 0.0092 of the length, and 0.01 is allowed.
+
+    Each value: 2^-8 of it, and the sum of the hidden values' roundings, independent and
+    within 2^-8 of their terms, passes t times 2^-8 of the terms' spread with a probability of
+    2 exp(-t^2 / 2) at most: for t = 8.2 once in 10^14.  Sums in binary32 move a value by far
+    less than 2^-11 of that spread."""
+    off = (got.double() - want).abs()
+    each = off / (2.0 ** -8 * (1 + 2.0 ** -8) * want.abs() +
+                  8.2 * (2.0 ** -8 + 2.0 ** -11) * spread + 1e-38)
+    whole = torch.linalg.vector_norm(off, dim=-1) / (
+        0.01 * torch.linalg.vector_norm(want, dim=-1) + 1e-38)
+    return float(torch.maximum(each.max(), whole.max()))
