@@ -4,16 +4,20 @@
 //                                                      local expert e among its picks
 //   out[t] = bf16( sum over the token's pairs of c_p W2_e h[p] ),  c_p the pick's weight
 //
-// What bounds it is streaming the weights of the experts that have tokens, once.  Every
-// workgroup finds those experts and their pairs by itself from the picks (1.6 us of LDS work
-// in place of the grouping's launches and of a row count that the host would have to
-// read), so the launches' sizes follow from the tokens alone.
+// What bounds it is streaming the weights of the experts that have tokens: once for up to 32
+// tokens of an expert in the up-projection and up to 16 in the down-projection, then again for
+// every further 32 and 16.  Every workgroup finds those experts and their pairs by itself
+// from the picks (1.6 us of LDS work in place of the grouping's launches and of a row count
+// that the host would have to read), so the launches' sizes follow from the tokens alone.
 //
 // The products are 16 x 16 MFMAs with the tokens of an expert as rows of the first operand, 16
 // rows of the weights as the second.  A workgroup is 8 waves that split K (up) or experts and
 // K (down) among them, and join their sums through LDS in the order of the waves.  h is
-// rounded to bf16, which is what the matrix instruction takes and what the grouped
-// up-projection stores; the down-projection's sums are rounded once, as the output.
+// rounded to bf16 with every kind of weights, which is what the matrix instruction takes and
+// what the grouped up-projection stores: with random weights it takes the output's error
+// from the 0.0017 of its own rounding to 0.0024 of its length.  (A second bf16 of what the
+// rounding leaves would be twice the row loads and matrix instructions of the
+// down-projection.)  That product's sums are rounded once, as the output.
 //
 // What it measured (kernels alone, us up and down; the bytes at the 5.95 TB/s of a plain copy):
 //   one token, 8 experts of 7168 x 2048    bf16  80 + 44 (118)   fp8 44 + 26 (59)
@@ -22,12 +26,20 @@
 //   64 tokens, 28 of 32 experts, e2m1, groups of 32         74 + 53 (116)
 //   16 tokens, 14 of 16 experts of 4096 x 1024, bf16        46 + 25 (60)
 //   one token, 2 experts of 1024 x 256, bf16                 6 + 5: launches and latency
-// Large up-projections run at 5.2 to 6.2 TB/s, down-projections at 4.3 to 5.3.  Of one int4
-// token's 45 us, 12 are the two launches' starts (picks, table, the first weights), and its
-// vector instructions, most of them code conversions, are 16 of the 27 of the up-projection.
-// With over about 12 tokens an expert the grouped products are as fast (64 tokens with every
-// one of 32 experts: bf16 701 us here, 647 there; fp8 447 and 402; int4 303 and 205; 32
-// tokens: 570 and 645, 339 and 399, 204 and 190).
+// Large up-projections run at 5.2 to 6.2 TB/s, down-projections at 4.3 to 5.3.  Without a local
+// pick the two launches take 2.8 and 3.5 us (picks, table, zeros), and the first weights' trip
+// to memory follows; there is no gap between the two.  Vector instructions, most of them code
+// conversions, are 16 of the 27 us of one int4 token's up-projection.
+// Beside the grouped calls (group, dispatch, both products, combine, in a graph with the row
+// count known), us here and there, 32 experts of 7168 x 2048, eight picks a token:
+//   tokens an expert       4            6            8            12           16
+//   bf16                466 and 597  489 and 607  504 and 606  556 and 610  650 and 613
+//   fp8                 258 and 368  281 and 369  301 and 370  351 and 371  427 and 372
+//   int4, groups of 128 151 and 178  170 and 180  187 and 180  244 and 189  298 and 196
+//   e2m1, groups of 32  155 and 178  184 and 181  197 and 180  314 and 184  374 and 194
+// (the weights once: 474, 237, 122 and 133).  Many tokens cost here what their rows do, loaded
+// again for every 16 outputs, and weights that are read again; with groups of 32, also 18
+// registers that the up-projection's path of 32 rows spills.
 #include <algorithm>
 
 #include "ep_kernels.h"
@@ -781,7 +793,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
 // steps of all segments are one run that the waves split evenly.  A wave adds what it has of
 // a segment, times the pairs' weights, to its own sums of the tokens in LDS.
 // The segments are of at most 16 pairs: an expert's weights are read again for its next 16,
-// by the same workgroup and at once.
+// by the same workgroup (where its waves take runs of the steps, by another wave of it).
 template <class P, int RB>
 __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int seg0, int seg1,
                                            const float* weight, float (*s_out)[16], int b, int wave,

@@ -11,9 +11,11 @@
 // A 128-value block of 8-bit output is 16 neighbouring lanes' chunks.
 //
 // What they measured: 32768 rows of 7168 bf16 values, residual in and out, rows and codes out
-// (2.12 GB): 373 us, 5.7 TB/s, 95% of the rate of a plain copy (four chunks a thread: 422, three
-// waves a SIMD instead of seven).  Their gradient (1.88 GB): 336 us, 5.6 TB/s, and 7 for
-// the sum of the partial rows.  One row: 4.5 us, a launch and two dependent trips to memory.
+// (2.12 GB): 373 to 383 us, 5.6 TB/s, 95% of the rate of a plain copy (four chunks a thread:
+// 422), with 72 registers and six waves a SIMD, three workgroups of 512.  Their gradient
+// (1.88 GB): 336 us, 5.6 TB/s, and 7 for the sum of the partial rows, with 114 registers and four
+// waves.  One row: 4.6 us, a launch and two dependent trips to memory.  The gradient of 16-bit
+// rows of over 16384 values beside 32-bit sums spills 12 registers.
 #include <algorithm>
 
 #include "ep_combine.h"

@@ -640,10 +640,10 @@ EP_API int ep_rms_norm(ep_combine_t h, const ep_norm_params* params, const void*
    g the gradient of y and q that of residual_out, inv = 1 / sqrt(mean(r^2) + eps):
      ds = inv * (g * w - (r * inv) * (inv * mean(g * w * r))) + q
      grad_weight = sum over all rows of g * r * inv
-   in binary32, products as they stand in brackets (inv^2 alone may be past the range).  x and the residual are the two terms of s, so ds is the gradient of both:
-   grad_x is ds in dtype, grad_residual in residual_dtype (where the types are one, one
-   of the two serves).  The codes' rounding has no gradient: g is that of the values they
-   stand for.
+   in binary32, products as they stand in brackets (inv^2 alone may be past the range).
+   x and the residual are the two terms of s, so ds is the gradient of both: grad_x is ds
+   in dtype, grad_residual in residual_dtype (where the types are one, one of the two
+   serves).  The codes' rounding has no gradient: g is that of the values they stand for.
    grad_out device, [R][tokens_per_rank][N], dtype.
    grad_residual_out  device, the same shape, residual_dtype, or NULL for zeros.
    sums     device, the same shape, residual_dtype (without a residual: x, and
@@ -672,8 +672,10 @@ EP_API int64_t ep_rms_norm_backward_workspace(ep_combine_t h, int32_t tokens_per
    product's rows not rounded.  (On fp8 handles silu(g) * u is not put into 8 bits again.)
    A token without local picks gets +0; picks of the same expert by one token add up.
    Neither rows nor weights of one expert change what a token without it gets, not even
-   by infinities or NaN.  Right for any routing; where experts have over about twelve
-   tokens each, the grouped calls are as fast.
+   by infinities or NaN.  Right for any routing; where experts have many tokens each the
+   grouped calls are faster: with 4-bit weights from about seven (with eight by 4 to 9%,
+   with sixteen in two thirds to half of the time), else from about thirteen (with sixteen by
+   6% in bf16 and 13% in fp8).
    format1, format2  NULL for weights in the handle's dtype, or the formats of 4-bit
             weights packed by ep_pack_weights_w4 (bf16 handles; both or neither).
    x        device, [R][tokens_per_rank][hidden] bf16, or with an fp8 handle e4m3fn codes
