@@ -11,7 +11,7 @@
 // A 128-value block of 8-bit output is 16 neighbouring lanes' chunks.
 //
 // What they measured: 32768 rows of 7168 bf16 values, residual in and out, rows and codes out
-// (2.12 GB): 373 to 383 us, 5.6 TB/s, 95% of the rate of a plain copy (four chunks a thread:
+// (2.12 GB): 370 to 383 us, 5.6 TB/s, 95% of the rate of a plain copy (four chunks a thread:
 // 422), with 72 registers and six waves a SIMD, three workgroups of 512.  Their gradient
 // (1.88 GB): 336 us, 5.6 TB/s, and 7 for the sum of the partial rows, with 114 registers and four
 // waves.  One row: 4.6 us, a launch and two dependent trips to memory.  The gradient of 16-bit
