@@ -876,7 +876,8 @@ bool moe_tokens_ok(const ep_combine_handle* h, int32_t tokens_per_rank) {
 }
 
 uint64_t moe_workspace(const ep_combine_handle* h, int32_t tokens_per_rank) {
-  return uint64_t(h->p.n_ranks) * tokens_per_rank * h->p.top_k * h->p.hidden_k * 2;
+  // two bf16 parts of each hidden value
+  return uint64_t(h->p.n_ranks) * tokens_per_rank * h->p.top_k * h->p.hidden_k * 2 * 2;
 }
 
 // One product's weights of `rows` x k an expert: bytes of an expert's weights, of the

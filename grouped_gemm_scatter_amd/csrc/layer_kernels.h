@@ -51,7 +51,7 @@ struct MoeArgs {
   const float* x_scale;      // [tokens][hidden/128] (fp8)
   const int32_t* topk_ids;   // [tokens][top_k]
   const float* topk_w;       // [tokens][top_k]
-  uint8_t* h;                // workspace: [tokens*top_k][inter] bf16
+  uint8_t* h;                // workspace: [tokens*top_k][2][inter] bf16, two parts of a value
   uint8_t* out;              // [tokens][hidden] bf16
   MoeWeights w1, w2;
   int32_t fp8;

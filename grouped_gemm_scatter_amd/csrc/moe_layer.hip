@@ -1,6 +1,6 @@
 // A whole mixture-of-experts layer for at most 64 tokens, in two launches:
 //
-//   h[p] = bf16( silu(g) u ),  [g; u] = W1_e x[t]      for every pair p of a token t and a
+//   h[p] = silu(g) u,  [g; u] = W1_e x[t]              for every pair p of a token t and a
 //                                                      local expert e among its picks
 //   out[t] = bf16( sum over the token's pairs of c_p W2_e h[p] ),  c_p the pick's weight
 //
@@ -13,32 +13,33 @@
 // The products are 16 x 16 MFMAs with the tokens of an expert as rows of the first operand, 16
 // rows of the weights as the second.  A workgroup is 8 waves that split K (up) or experts and
 // K (down) among them, and join their sums through LDS in the order of the waves.  h is
-// rounded to bf16 with every kind of weights, which is what the matrix instruction takes and
-// what the grouped up-projection stores: with random weights it takes the output's error
-// from the 0.0017 of its own rounding to 0.0024 of its length.  (A second bf16 of what the
-// rounding leaves would be twice the row loads and matrix instructions of the
-// down-projection.)  That product's sums are rounded once, as the output.
+// held as two bf16 values, since the matrix instruction takes bf16: the second is what the
+// first one's rounding leaves, together 2^-17 of the value.  (The first alone takes the
+// output's error from the 0.0017 of its own rounding to 0.0024 of its length.)  They are two
+// rows of the first operand, of which an expert of one or two tokens leaves most unused
+// anyway; of more tokens they cost row loads, 10 to 15% of the down-projection for 2 tokens an
+// expert on average, half of it for 16.  Its sums are rounded once, as the output.
 //
 // What it measured (kernels alone, us up and down; the bytes at the 5.95 TB/s of a plain copy):
-//   one token, 8 experts of 7168 x 2048    bf16  80 + 44 (118)   fp8 44 + 26 (59)
+//   one token, 8 experts of 7168 x 2048    bf16  80 + 45 (118)   fp8 44 + 27 (59)
 //                                          int4, groups of 128   27 + 18 (31)
-//   five tokens of the same in fp8, 25 experts             139 + 78 (185)
-//   64 tokens, 28 of 32 experts, e2m1, groups of 32         74 + 53 (116)
-//   16 tokens, 14 of 16 experts of 4096 x 1024, bf16        46 + 25 (60)
+//   five tokens of the same in fp8, 25 experts             140 + 82 (185)
+//   64 tokens, 28 of 32 experts, e2m1, groups of 32         74 + 61 (116)
+//   16 tokens, 14 of 16 experts of 4096 x 1024, bf16        46 + 26 (60)
 //   one token, 2 experts of 1024 x 256, bf16                 6 + 5: launches and latency
-// Large up-projections run at 5.2 to 6.2 TB/s, down-projections at 4.3 to 5.3.  Without a local
+// Large up-projections run at 5.2 to 6.2 TB/s, down-projections at 3.8 to 5.3.  Without a local
 // pick the two launches take 2.8 and 3.5 us (picks, table, zeros), and the first weights' trip
 // to memory follows; there is no gap between the two.  Vector instructions, most of them code
 // conversions, are 16 of the 27 us of one int4 token's up-projection.
 // Beside the grouped calls (group, dispatch, both products, combine, in a graph with the row
 // count known), us here and there, 32 experts of 7168 x 2048, eight picks a token:
 //   tokens an expert       4            6            8            12           16
-//   bf16                466 and 597  489 and 607  504 and 606  556 and 610  650 and 613
-//   fp8                 258 and 368  281 and 369  301 and 370  351 and 371  427 and 372
-//   int4, groups of 128 151 and 178  170 and 180  187 and 180  244 and 189  298 and 196
-//   e2m1, groups of 32  155 and 178  184 and 181  197 and 180  314 and 184  374 and 194
+//   bf16                499 and 602  531 and 608  575 and 606  662 and 611  779 and 616
+//   fp8                 289 and 367  325 and 369  372 and 369  459 and 372  554 and 373
+//   int4, groups of 128 174 and 178  204 and 179  244 and 183  333 and 189  414 and 196
+//   e2m1, groups of 32  178 and 179  216 and 181  253 and 180  404 and 186  491 and 195
 // (the weights once: 474, 237, 122 and 133).  Many tokens cost here what their rows do, loaded
-// again for every 16 outputs, and weights that are read again; with groups of 32, also 18
+// again for every 16 outputs, and weights that are read again; with groups of 32, also 16
 // registers that the up-projection's path of 32 rows spills.
 #include <algorithm>
 
@@ -53,17 +54,18 @@ constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kMaxSegments = kMaxLocalExperts + kMoeTokens;
 
 // The pairs of a launch, numbered by (expert, token).  A segment is up to ROWS pairs of one
-// expert.  Few and many pairs take different paths through the products, so that an
-// expert of many tokens does not slow down those of few.
-constexpr int kFew = 8;
+// expert.  Up to FEW pairs, up to MID and more of them take different paths through the
+// products, so that an expert of many tokens does not slow down those of few.
 struct Table {
   uint64_t tokens[kMaxLocalExperts];   // expert e: its tokens
   int first[kMaxLocalExperts];         // its first pair
   int seg_expert[kMaxSegments], seg_pair[kMaxSegments], seg_pairs[kMaxSegments];
   int16_t pick[kMoePicks];             // local expert of a pick, or -1
   uint8_t token[kMoePicks];            // pair: its token
-  int few, segments;                   // segments of at most kFew pairs come first
-  int few_rows, many_rows;             // rows of the largest of either kind: 4, 8 and 16, 32
+  int few, mid, segments;              // ends of the segments of few and of up to MID pairs
+                                       // in the list, and of the list
+  int over_half, over16;               // whether experts of FEW / 2 + 1..FEW pairs, and of
+                                       // over 16, are there
 };
 
 // Lanes below this one in a mask of lanes.
@@ -76,7 +78,7 @@ struct Weights {
   float pick[kMoePicks], pair[kMoePicks];
 };
 
-template <int ROWS>
+template <int ROWS, int FEW, int MID>
 __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s, Weights* w = nullptr) {
   const int tid = threadIdx.x, picks = a.tokens * a.top_k;
   for (int e = tid; e < a.n_experts; e += kThreads) s.tokens[e] = 0;
@@ -94,12 +96,15 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s, Weights*
     // pairs and segments before each expert, 64 experts at a time: counts by their bits, each
     // a ballot
     auto pairs_of = [&](int e) { return e < a.n_experts ? __popcll(s.tokens[e]) : 0; };
-    int few = 0, pair = 0, few_rows = 4, many_rows = 16;
+    auto is_few = [](int n) { return n > 0 && n <= FEW; };
+    auto is_mid = [](int n) { return n > FEW && n <= MID; };
+    int few = 0, mid = 0, pair = 0, over_half = 0, over16 = 0;
     for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
       const int n = pairs_of(e0 + tid);
-      few += __popcll(__ballot(n > 0 && n <= kFew));
+      few += __popcll(__ballot(is_few(n)));
+      if constexpr (MID > FEW) mid += __popcll(__ballot(is_mid(n)));
     }
-    int few_seg = 0, seg = few;
+    int few_seg = 0, mid_seg = few, seg = few + mid;
     for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
       const int e = e0 + tid, n = pairs_of(e);
       int pairs_before = pair;
@@ -108,16 +113,21 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s, Weights*
         pairs_before += lanes_below(m) << bit;
         pair += __popcll(m) << bit;
       }
-      const uint64_t mine = __ballot(n > 0 && n <= kFew);
-      int at = n > kFew ? seg : few_seg + lanes_below(mine);
-      few_seg += __popcll(mine);
+      const uint64_t in_few = __ballot(is_few(n));
+      int at = n > FEW ? seg : few_seg + lanes_below(in_few);
+      few_seg += __popcll(in_few);
+      if constexpr (MID > FEW) {
+        const uint64_t in_mid = __ballot(is_mid(n));
+        if (is_mid(n)) at = mid_seg + lanes_below(in_mid);
+        mid_seg += __popcll(in_mid);
+      }
       for (int i = 0; i * ROWS < a.tokens; ++i) {
-        const uint64_t m = __ballot(n > kFew && n > i * ROWS);
-        if (n > kFew) at += lanes_below(m);
+        const uint64_t m = __ballot(n > MID && n > i * ROWS);
+        if (n > MID) at += lanes_below(m);
         seg += __popcll(m);
       }
-      if (__ballot(n > 4 && n <= kFew)) few_rows = 8;
-      if (ROWS > 16 && __ballot(n > 16)) many_rows = 32;
+      over_half |= __ballot(n > FEW / 2 && n <= FEW) != 0;
+      over16 |= __ballot(n > 16) != 0;
       if (e < a.n_experts) s.first[e] = pairs_before;
       for (int i = 0; i * ROWS < n; ++i) {
         s.seg_expert[at + i] = e;
@@ -127,9 +137,10 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s, Weights*
     }
     if (tid == 0) {
       s.few = few;
+      s.mid = few + mid;
       s.segments = seg;
-      s.few_rows = few_rows;
-      s.many_rows = many_rows;
+      s.over_half = over_half;
+      s.over16 = over16;
     }
   }
   __syncthreads();
@@ -159,18 +170,23 @@ __device__ __forceinline__ void build_table(const MoeArgs& a, Table& s, Weights*
     __builtin_amdgcn_sched_barrier(0);   \
   } while (0)
 
-// ---- The first operand's rows, RB of them: 4, 8, 16 or 32 pairs of an expert.
+// ---- The first operand's rows, RB of them: 4, 8, 16 or 32 for pairs of an expert (one a pair
+// in the up-projection, two in the down-projection).
 // An MFMA has 16 rows, and in a step's 128 k four of them follow (by quarters of k).
-// Fewer than 16 pairs would leave its lanes loading one row over and over, four loads a
+// Fewer than 16 rows would leave its lanes loading one row over and over, four loads a
 // step that cost as much of the memory path as the weights (a stream of 4-bit weights by
-// itself 6.1 TB/s, with these loads 4.4).  So lane L % 16 loads pair L % 16 % RB, of a quarter
+// itself 6.1 TB/s, with these loads 4.4).  So lane L % 16 loads row L % 16 % RB, of a quarter
 // of its own, and every quarter's MFMA takes the same register: its rows with another
 // quarter's values come out wrong and are left out, which 16 / RB accumulators, one a
 // quarter (or two quarters), make possible.
-template <int RB>
+// JOINED: the row blocks are parts of the same pairs, and go into one accumulator.
+template <int RB, bool JOINED = false>
 struct RowsOf {
+  static constexpr int ROWS = RB;
   static constexpr int BLOCKS = RB > 16 ? RB / 16 : 1;
-  static constexpr int ACCS = RB < 16 ? 16 / RB : BLOCKS;
+  static constexpr int SUMS = JOINED ? 1 : BLOCKS;       // of one quarter's products
+  static constexpr int ACCS = RB < 16 ? 16 / RB : SUMS;
+  static constexpr int sum(int j) { return JOINED ? 0 : j; }
 };
 
 // The sums of all quarters of a lane's accumulators, RB rows in rows 0..RB - 1 of the result.
@@ -201,12 +217,12 @@ __device__ __forceinline__ f32x4 add_row_parts(const f32x4 (&acc)[RowsOf<RB>::AC
 }
 
 // Rows in bf16: 8 values a lane of each quarter of a step's 128 k (where they lie: at()).
-template <int RB>
-struct Bf16Rows {
+template <int RB, bool JOINED = false>
+struct Bf16Rows : RowsOf<RB, JOINED> {
   u32x4 v[RB < 16 ? RB / 4 : 4 * RowsOf<RB>::BLOCKS];
   // register of row block j and quarter q, and its accumulator
   static constexpr int reg(int j, int q) { return RB < 16 ? q & (RB / 4 - 1) : 4 * j + q; }
-  static constexpr int acc(int j, int q) { return RB < 16 ? q / (RB / 4) : j; }
+  static constexpr int acc(int j, int q) { return RB < 16 ? q / (RB / 4) : JOINED ? 0 : j; }
   // quarter that the lane loads first
   static __device__ __forceinline__ int quarter(int lane) {
     return RB < 16 ? (lane & 15) / RB * (RB / 4) : 0;
@@ -222,11 +238,11 @@ struct TwoBlocks {
     P::load(g, s, gate, kt, length);
     P::load(u, s, up, kt, length);
   }
-  template <int RB, class Rows>
-  __device__ __forceinline__ void multiply(f32x4 (&ag)[RowsOf<RB>::ACCS],
-                                           f32x4 (&au)[RowsOf<RB>::ACCS], const Rows& r) const {
-    P::template multiply<RB>(ag, r, g);
-    P::template multiply<RB>(au, r, u);
+  template <class Rows>
+  __device__ __forceinline__ void multiply(f32x4 (&ag)[Rows::ACCS], f32x4 (&au)[Rows::ACCS],
+                                           const Rows& r) const {
+    P::multiply(ag, r, g);
+    P::multiply(au, r, u);
   }
 };
 
@@ -248,7 +264,7 @@ struct Bf16 {
     uint32_t slice, lane;               // bytes between 64-k slices; of this lane's row
   };
   struct Block { u32x4 v[4]; };
-  template <int RB> using Rows = Bf16Rows<RB>;
+  template <int RB, bool JOINED = false> using Rows = Bf16Rows<RB, JOINED>;
   static __device__ __forceinline__ Source source(const MoeWeights& w, int e, int rows, int k,
                                                   int lane) {
     Source s;
@@ -273,8 +289,9 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
     return (lane >> 4) * 16 + quarter * 64;
   }
-  template <int RB>
-  static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, const uint8_t* x0, int length,
+  template <int RB, bool JOINED>
+  static __device__ __forceinline__ void load_rows(Bf16Rows<RB, JOINED>& r, const uint8_t* x0,
+                                                   int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
                                                    int kt, int) {
     const buffer x = make_buffer(x0, length);
@@ -284,13 +301,13 @@ struct Bf16 {
       for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
         in_order(r.v[4 * j + q] = buffer_load16(x, row[j] + q * 64, kt * 256));
   }
-  template <int RB>
-  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                  const Bf16Rows<RB>& r, const Block& b) {
+  template <class R>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[R::ACCS], const R& r,
+                                                  const Block& b) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j) {
+      for (int j = 0; j < R::BLOCKS; ++j) {
         f32x4& to = acc[r.acc(j, q)];
         to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r.v[r.reg(j, q)]),
                                                      __builtin_bit_cast(bf16x8, b.v[q]), to, 0, 0, 0);
@@ -300,26 +317,26 @@ struct Bf16 {
 
 // One step of weights whose scale holds for QPS quarters: w(q) the values of quarter q,
 // scale(q) its scale.
-template <int RB, int QPS, class W, class S>
-__device__ __forceinline__ void scaled_multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                const Bf16Rows<RB>& r, W w, S scale) {
-  constexpr int BLOCKS = RowsOf<RB>::BLOCKS;
+template <int QPS, class R, class W, class S>
+__device__ __forceinline__ void scaled_multiply(f32x4 (&acc)[R::ACCS], const R& r, W w, S scale) {
   // quarters of one sum: of one scale and one accumulator
-  constexpr int RUN = RB < 16 && RB / 4 < QPS ? RB / 4 : QPS;
+  constexpr int RUN = R::ROWS < 16 && R::ROWS / 4 < QPS ? R::ROWS / 4 : QPS;
 #pragma unroll
   for (int q0 = 0; q0 < 4; q0 += RUN) {
-    f32x4 part[BLOCKS] = {};
+    f32x4 part[R::SUMS] = {};
 #pragma unroll
     for (int q = q0; q < q0 + RUN; ++q) {
       const bf16x8 wq = w(q);
 #pragma unroll
-      for (int j = 0; j < BLOCKS; ++j)
-        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, r.v[r.reg(j, q)]), wq, part[j], 0, 0, 0);
+      for (int j = 0; j < R::BLOCKS; ++j) {
+        f32x4& to = part[R::sum(j)];
+        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, r.v[r.reg(j, q)]), wq, to, 0, 0, 0);
+      }
     }
     const float sc = scale(q0);
 #pragma unroll
-    for (int j = 0; j < BLOCKS; ++j)
+    for (int j = 0; j < R::SUMS; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f32x4& to = acc[r.acc(j, q0)];
@@ -370,7 +387,7 @@ struct Fp8Up : Fp8 {
   static constexpr bool PAIR_A_LANE = true;
   // a row's 128 bytes of a step are two halves of k; with 8 rows a lane loads one of them
   template <int RB>
-  struct Rows {
+  struct Rows : RowsOf<RB> {
     static_assert(RB >= 8, "halves of k");
     u32x4 v[RB < 16 ? 1 : 2 * RowsOf<RB>::BLOCKS];
     uint32_t s[RowsOf<RB>::BLOCKS];
@@ -392,13 +409,13 @@ struct Fp8Up : Fp8 {
       for (int h = 0; h < (RB < 16 ? 1 : 2); ++h)
         in_order(r.v[2 * j + h] = buffer_load16(x, row[j] + h * 64, kt * 128));
   }
-  template <int RB>
-  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                  const Rows<RB>& r, const Block& b) {
+  template <class R>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[R::ACCS], const R& r,
+                                                  const Block& b) {
     const float ws = __builtin_bit_cast(float, b.s);
-    constexpr int PARTS = RB < 16 ? 2 : 1;           // accumulators a step's halves go to
+    constexpr int PARTS = R::ROWS < 16 ? 2 : 1;      // accumulators a step's halves go to
 #pragma unroll
-    for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j) {
+    for (int j = 0; j < R::BLOCKS; ++j) {
       const float sc = __builtin_bit_cast(float, r.s[j]) * ws;
       f32x4 part[PARTS] = {};
 #pragma unroll
@@ -433,9 +450,9 @@ struct Fp8Down : Fp8 {
     u32x4 v[2][2];
     uint32_t s;
   };
-  template <int RB>
-  struct Rows {
-    Bf16Rows<RB> r[2];
+  template <int RB, bool JOINED>
+  struct Rows : RowsOf<RB, JOINED> {
+    Bf16Rows<RB, JOINED> r[2];
     static __device__ __forceinline__ int quarter(int lane) { return Bf16Rows<RB>::quarter(lane); }
   };
   static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t row0, int k,
@@ -455,8 +472,9 @@ struct Fp8Down : Fp8 {
   static __device__ __forceinline__ uint32_t at(int lane, int quarter) {
     return (lane >> 4) * 32 + (quarter >> 1) * 128 + (quarter & 1) * 16;
   }
-  template <int RB>
-  static __device__ __forceinline__ void load_rows(Rows<RB>& r, const uint8_t* x0, int length,
+  template <int RB, bool JOINED>
+  static __device__ __forceinline__ void load_rows(Rows<RB, JOINED>& r, const uint8_t* x0,
+                                                   int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
                                                    int k, int inter) {
 #pragma unroll
@@ -464,9 +482,11 @@ struct Fp8Down : Fp8 {
       const buffer x =
           make_buffer(x0, o ? length & buffer_length(2 * k + 1, inter / 128) : length);
 #pragma unroll
-      for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
-        in_order(r.r[o].v[q] = buffer_load16(x, row[0] + (q >> 1) * 128 + (q & 1) * 16,
-                                             (2 * k + o) * 256));
+      for (int j = 0; j < RowsOf<RB>::BLOCKS; ++j)
+#pragma unroll
+        for (int q = 0; q < (RB < 16 ? RB / 4 : 4); ++q)
+          in_order(r.r[o].v[4 * j + q] = buffer_load16(x, row[j] + (q >> 1) * 128 + (q & 1) * 16,
+                                                       (2 * k + o) * 256));
     }
   }
   static __device__ __forceinline__ bf16x8 values(uint32_t lo, uint32_t hi) {
@@ -476,14 +496,14 @@ struct Fp8Down : Fp8 {
     const bf16x2 s = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, 1);
     return bf16x8{p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
   }
-  template <int RB>
-  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                  const Rows<RB>& r, const Block& b) {
+  template <class R>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[R::ACCS], const R& r,
+                                                  const Block& b) {
     const auto s = __builtin_amdgcn_permlane16_swap(b.s, b.s, false, false);
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       const float ws = __uint_as_float(s[o]);
-      scaled_multiply<RB, 4>(
+      scaled_multiply<4>(
           acc, r.r[o],
           [&](int q) { return values(b.v[o][q >> 1][2 * (q & 1)], b.v[o][q >> 1][2 * (q & 1) + 1]); },
           [&](int) { return ws; });
@@ -510,7 +530,7 @@ struct W4 {
     int odd;                            // all bits in the lanes of the second block
     int kt;                             // runs of a 16-row block
   };
-  template <int RB> using Rows = Bf16Rows<RB>;
+  template <int RB, bool JOINED = false> using Rows = Bf16Rows<RB, JOINED>;
   static __device__ __forceinline__ Source source(const MoeWeights& w, int e, int rows, int k,
                                                   int lane) {
     Source s;
@@ -547,14 +567,13 @@ struct W4 {
   static __device__ __forceinline__ void load_rows(Bf16Rows<RB>& r, const uint8_t* x, int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
                                                    int kt, int) {
-    Bf16::load_rows<RB>(r, x, length, row, kt, 0);
+    Bf16::load_rows(r, x, length, row, kt, 0);
   }
-  template <int RB>
-  static __device__ __forceinline__ void multiply_block(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                        const Bf16Rows<RB>& r, const u32x4& v,
-                                                        word s) {
+  template <class R>
+  static __device__ __forceinline__ void multiply_block(f32x4 (&acc)[R::ACCS], const R& r,
+                                                        const u32x4& v, word s) {
     constexpr int QPS = F::GROUP / 32;
-    scaled_multiply<RB, QPS>(
+    scaled_multiply<QPS>(
         acc, r, [&](int q) { return decode8<F::CODES>(v[q]); },
         [&](int q) { return F::scale((uint16_t)(s >> (16 * (q / QPS)))); });
   }
@@ -573,13 +592,13 @@ struct TwoBlocks<W4<F>> {
     in_order(buffer_load_to(s, make_buffer(src.s, length),
                             src.lane_s + (src.odd & (int)((ru - rg) * P::SB)), rg * P::SB));
   }
-  template <int RB, class Rows>
-  __device__ __forceinline__ void multiply(f32x4 (&ag)[RowsOf<RB>::ACCS],
-                                           f32x4 (&au)[RowsOf<RB>::ACCS], const Rows& r) const {
+  template <class Rows>
+  __device__ __forceinline__ void multiply(f32x4 (&ag)[Rows::ACCS], f32x4 (&au)[Rows::ACCS],
+                                           const Rows& r) const {
     typename P::word sg, su;
     P::both(s, sg, su);
-    P::template multiply_block<RB>(ag, r, g, sg);
-    P::template multiply_block<RB>(au, r, u, su);
+    P::multiply_block(ag, r, g, sg);
+    P::multiply_block(au, r, u, su);
   }
 };
 
@@ -597,9 +616,9 @@ struct W4Down : W4<F> {
     u32x4 v[2];
     word s;
   };
-  template <int RB>
-  struct Rows {
-    Bf16Rows<RB> r[2];
+  template <int RB, bool JOINED>
+  struct Rows : RowsOf<RB, JOINED> {
+    Bf16Rows<RB, JOINED> r[2];
     static __device__ __forceinline__ int quarter(int lane) { return Bf16Rows<RB>::quarter(lane); }
   };
   static __device__ __forceinline__ void load(Block& b, const Source& s, uint32_t start, int k,
@@ -611,20 +630,21 @@ struct W4Down : W4<F> {
     in_order(buffer_load_to(b.s, make_buffer(s.s, length),
                             s.lane_s + (s.odd & second & (int)P::SB), run * P::SB));
   }
-  template <int RB>
-  static __device__ __forceinline__ void load_rows(Rows<RB>& r, const uint8_t* x, int length,
+  template <int RB, bool JOINED>
+  static __device__ __forceinline__ void load_rows(Rows<RB, JOINED>& r, const uint8_t* x,
+                                                   int length,
                                                    const uint32_t (&row)[RowsOf<RB>::BLOCKS],
                                                    int k, int inter) {
-    Bf16::load_rows<RB>(r.r[0], x, length, row, 2 * k, 0);
-    Bf16::load_rows<RB>(r.r[1], x, length & buffer_length(2 * k + 1, inter / 128), row, 2 * k + 1, 0);
+    Bf16::load_rows(r.r[0], x, length, row, 2 * k, 0);
+    Bf16::load_rows(r.r[1], x, length & buffer_length(2 * k + 1, inter / 128), row, 2 * k + 1, 0);
   }
-  template <int RB>
-  static __device__ __forceinline__ void multiply(f32x4 (&acc)[RowsOf<RB>::ACCS],
-                                                  const Rows<RB>& r, const Block& b) {
+  template <class R>
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[R::ACCS], const R& r,
+                                                  const Block& b) {
     word s0, s1;
     P::both(b.s, s0, s1);
-    P::template multiply_block<RB>(acc, r.r[0], b.v[0], s0);
-    P::template multiply_block<RB>(acc, r.r[1], b.v[1], s1);
+    P::multiply_block(acc, r.r[0], b.v[0], s0);
+    P::multiply_block(acc, r.r[1], b.v[1], s1);
   }
 };
 
@@ -634,6 +654,17 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_waitcnt(0xc07f);                // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// A hidden value, as the down-projection multiplies it: in two bf16 parts, the second what
+// the first's rounding leaves (off by 2^-17 of the value at most), in two rows of the
+// workspace.  What is not finite has the first alone.
+__device__ __forceinline__ void store_hidden(const MoeArgs& a, int pair, int n, float v) {
+  const __bf16 hi = (__bf16)v;
+  const float rest = __builtin_isfinite((float)hi) ? v - (float)hi : 0.f;
+  __bf16* h = reinterpret_cast<__bf16*>(a.h) + (size_t)pair * 2 * a.inter + n;
+  h[0] = hi;
+  h[a.inter] = (__bf16)rest;
 }
 
 // ---- Up-projection and SwiGLU.  An item is a segment and 16 outputs: 16 gate rows and the 16
@@ -681,7 +712,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s, int s
   auto load = [&](Step& st, Place& p) {
     const int length = buffer_length(p.item, items) & buffer_length(p.k, KT);
     st.w.load(p.src, p.gate, p.up, p.k, length);
-    P::template load_rows<RB>(st.r, a.x, length, p.row, p.k, a.hidden);
+    P::load_rows(st.r, a.x, length, p.row, p.k, a.hidden);
     if constexpr (P::PAIR_A_LANE)
 #pragma unroll
       for (int j = 0; j < BLOCKS; ++j)
@@ -707,7 +738,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s, int s
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       // (a wave without a step of its own multiplies the empty buffer's zeros)
-      st[d].w.template multiply<RB>(ag, au, st[d].r);
+      st[d].w.multiply(ag, au, st[d].r);
       __builtin_amdgcn_sched_barrier(0);
       load(st[d], ahead);
       k += kWaves;
@@ -751,8 +782,7 @@ __device__ __forceinline__ void up_items(const MoeArgs& a, const Table& s, int s
             g += part[w][0][j][l][i];
             u += part[w][1][j][l][i];
           }
-          reinterpret_cast<__bf16*>(a.h)[(size_t)(pair + r) * a.inter + b * 16 + c] =
-              (__bf16)(g / (1.f + expf(-g)) * u);
+          store_hidden(a, pair + r, b * 16 + c, g / (1.f + expf(-g)) * u);
         }
         // one barrier an item: the next one's sums go to the other buffer, if there is one
         if constexpr (BUFS == 1) lds_barrier();
@@ -769,20 +799,20 @@ template <class P>
 __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
   __shared__ Table s;
   __shared__ f32x4 s_part[1][kWaves][2][2][64];
-  build_table<32>(a, s);
+  build_table<32, 8, 8>(a, s);
   const int few = __builtin_amdgcn_readfirstlane(s.few);
   const int segments = __builtin_amdgcn_readfirstlane(s.segments);
   typedef f32x4 (*OneBlock)[kWaves][2][1][64];
   const OneBlock part = reinterpret_cast<OneBlock>(s_part);
   if (few > 0) {
-    if (!P::PAIR_A_LANE && __builtin_amdgcn_readfirstlane(s.few_rows) == 4)
+    if (!P::PAIR_A_LANE && !__builtin_amdgcn_readfirstlane(s.over_half))
       up_items<P, P::PAIR_A_LANE ? 8 : 4>(a, s, 0, few, part);
     else
       up_items<P, 8>(a, s, 0, few, part);
   }
   if (few < segments) {
     __syncthreads();       // the sums of the last item are read
-    if (__builtin_amdgcn_readfirstlane(s.many_rows) == 16)
+    if (!__builtin_amdgcn_readfirstlane(s.over16))
       up_items<P, 16>(a, s, few, segments, part);
     else
       up_items<P, 32>(a, s, few, segments, s_part);
@@ -792,13 +822,22 @@ __global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs a) {
 // ---- Down-projection and the weighted sum.  A workgroup takes 16 columns of the output; the
 // steps of all segments are one run that the waves split evenly.  A wave adds what it has of
 // a segment, times the pairs' weights, to its own sums of the tokens in LDS.
+// A pair is two rows, the parts of its h: of RB rows the first half are the first parts, and
+// with 32 rows a row block each, joined in one accumulator.  Three classes of experts, of up
+// to 4 pairs (8 rows, or 4 where none has over 2), up to 8 (16) and more (32): us of the
+// down-projection of 64 tokens in e2m1 and of 16 in bf16 (2 pairs an expert on average)
+//   classes up to 4, 8 and more   61.4 and 26.3     up to 8 and more        67.9 and 26.3
+//   up to 2, 8 and more           60.3 and 27.0     up to 2, 4, 8 and more  59.5 and 27.2
+// (a class more is a start of the loads more, a class less are rows that most experts lack).
 // The segments are of at most 16 pairs: an expert's weights are read again for its next 16,
 // by the same workgroup (where its waves take runs of the steps, by another wave of it).
 template <class P, int RB>
 __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int seg0, int seg1,
                                            const float* weight, float (*s_out)[16], int b, int wave,
                                            int lane) {
-  typedef typename P::template Rows<RB> Rows;
+  constexpr bool JOINED = RB > 16;
+  typedef typename P::template Rows<RB, JOINED> Rows;
+  constexpr int BLOCKS = Rows::BLOCKS, PAIRS = RB / 2;
   const int KT = (a.inter + P::STEP - 1) / P::STEP;     // steps
   constexpr int DEPTH = P::DOWN_DEPTH;
   const uint32_t start = P::start(a.w2, b * 16, a.inter);
@@ -824,7 +863,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int
   struct Place {
     int seg, k, at;
     decltype(P::source(a.w2, 0, 0, 0, 0)) src;
-    uint32_t row[1];
+    uint32_t row[BLOCKS];
   };
   auto enter = [&](Place& p) {
     const int seg = min(p.seg, seg1 - 1);
@@ -832,17 +871,21 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int
     const int pair = __builtin_amdgcn_readfirstlane(s.seg_pair[seg]);
     const int n = __builtin_amdgcn_readfirstlane(s.seg_pairs[seg]);
     p.src = P::source(a.w2, e, a.hidden, a.inter, lane);
-    p.row[0] = (uint32_t)(pair + min((lane & 15) % RB, n - 1)) * (uint32_t)a.inter * 2 +
-               P::at(lane, Rows::quarter(lane));
+    const int r = (lane & 15) % RB;
+#pragma unroll
+    for (int j = 0; j < BLOCKS; ++j)
+      p.row[j] = (uint32_t)(2 * (pair + min(r % PAIRS, n - 1)) + (JOINED ? j : r / PAIRS)) *
+                     (uint32_t)a.inter * 2 +
+                 P::at(lane, Rows::quarter(lane));
   };
   auto load = [&](Step& st, Place& p) {
     const int length = buffer_length(p.at++, count);
     P::load(st.w, p.src, start, p.k, length);
-    P::template load_rows<RB>(st.r, a.h, length, p.row, p.k, a.inter);
+    P::load_rows(st.r, a.h, length, p.row, p.k, a.inter);
     if (move(p.seg, p.k)) enter(p);
   };
   if (count <= 0) return;
-  f32x4 acc[RowsOf<RB>::ACCS] = {};
+  f32x4 acc[Rows::ACCS] = {};
   Step st[DEPTH];
   int seg = seg0 + begin / KT, k = begin % KT;
   Place ahead;
@@ -855,7 +898,7 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int
   for (int at = 0; at < count;) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      P::template multiply<RB>(acc, st[d].r, st[d].w);
+      P::multiply(acc, st[d].r, st[d].w);
       __builtin_amdgcn_sched_barrier(0);
       load(st[d], ahead);
       const int was = seg;
@@ -866,13 +909,20 @@ __device__ __forceinline__ void down_steps(const MoeArgs& a, const Table& s, int
           v = add_row_parts<RB>(acc, lane);
         else
           v = acc[0];
+        // the two parts' rows, 2, 4 or 8 apart
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (RB == 4) v[i] += v[(i + 2) & 3];
+          if constexpr (RB == 8) v[i] = add_quarters(v[i]);
+          if constexpr (RB == 16) v[i] = add_halves(v[i]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = (lane >> 4) * 4 + i;
           if (r < n) s_out[s.token[pair + r]][lane & 15] += weight[pair + r] * v[i];
         }
 #pragma unroll
-        for (int j = 0; j < RowsOf<RB>::ACCS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < Rows::ACCS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       if (++at >= count) break;
     }
@@ -887,18 +937,20 @@ __global__ __launch_bounds__(kThreads, 4) void moe_down_kernel(MoeArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = lane; i < a.tokens * 16; i += 64) s_out[wave][i >> 4][i & 15] = 0.f;
-  build_table<16>(a, s, &weights);
+  build_table<16, 4, 8>(a, s, &weights);
   const int b = blockIdx.x;
   const int few = __builtin_amdgcn_readfirstlane(s.few);
   const int segments = __builtin_amdgcn_readfirstlane(s.segments);
+  const int mid = __builtin_amdgcn_readfirstlane(s.mid);
+  float(*out)[16] = s_out[wave];
   if (few > 0) {
-    if (__builtin_amdgcn_readfirstlane(s.few_rows) == 4)
-      down_steps<P, 4>(a, s, 0, few, weights.pair, s_out[wave], b, wave, lane);
+    if (!__builtin_amdgcn_readfirstlane(s.over_half))
+      down_steps<P, 4>(a, s, 0, few, weights.pair, out, b, wave, lane);
     else
-      down_steps<P, 8>(a, s, 0, few, weights.pair, s_out[wave], b, wave, lane);
+      down_steps<P, 8>(a, s, 0, few, weights.pair, out, b, wave, lane);
   }
-  if (few < segments)
-    down_steps<P, 16>(a, s, few, segments, weights.pair, s_out[wave], b, wave, lane);
+  if (few < mid) down_steps<P, 16>(a, s, few, mid, weights.pair, out, b, wave, lane);
+  if (mid < segments) down_steps<P, 32>(a, s, mid, segments, weights.pair, out, b, wave, lane);
   __syncthreads();
   for (int i = tid; i < a.tokens * 8; i += kThreads) {
     const int t = i >> 3, c = (i & 7) * 2;

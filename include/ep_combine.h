@@ -668,14 +668,15 @@ EP_API int64_t ep_rms_norm_backward_workspace(ep_combine_t h, int32_t tokens_per
      out[rk][t][:] = bf16( sum over the local picks k of topk_w[rk][t][k] *
                            W2_e (silu(g) * u) ),   [g; u] = W1_e x[rk][t]
    over the experts e of this GPU, as ep_grouped_gemm_swiglu, ep_grouped_gemm_scatter and
-   ep_combine_reduce together give it, with silu(g) * u rounded to bf16 and the second
-   product's rows not rounded.  (On fp8 handles silu(g) * u is not put into 8 bits again.)
+   ep_combine_reduce together give it, with silu(g) * u kept to 2^-17 of its value (two bf16
+   parts) where they round it to bf16 or, on fp8 handles, put it into 8 bits again, and the
+   second product's rows not rounded.
    A token without local picks gets +0; picks of the same expert by one token add up.
    Neither rows nor weights of one expert change what a token without it gets, not even
    by infinities or NaN.  Right for any routing; where experts have many tokens each the
-   grouped calls are faster: with 4-bit weights from about seven (with eight by 4 to 9%,
-   with sixteen in two thirds to half of the time), else from about thirteen (with sixteen by
-   6% in bf16 and 13% in fp8).
+   grouped calls are faster: with 4-bit weights from about five (with eight by a quarter,
+   with sixteen in under half of the time), with fp8 from about nine and with bf16 from about
+   eleven (with sixteen by a third and by a fifth).
    format1, format2  NULL for weights in the handle's dtype, or the formats of 4-bit
             weights packed by ep_pack_weights_w4 (bf16 handles; both or neither).
    x        device, [R][tokens_per_rank][hidden] bf16, or with an fp8 handle e4m3fn codes

@@ -184,7 +184,7 @@ def moe_layer(x, w1, w2, ids, topk_w, expert_lo=0):
     [E][hidden][I] that their picks ids [n][k] name: out[t] = sum over local picks of
     topk_w * w2 (silu(g) u).  Returns (out, bound): bound [n][hidden] is what rounding may
     move it by where the products are summed in binary32 and silu(g) u is rounded to
-    bf16.  Each product of K terms: the matrix unit's additions are within 2^-23 of a
+    bf16 or finer.  Each product of K terms: the matrix unit's additions are within 2^-23 of a
     partial sum each, and scales and joins add at most K / 16 + 32 operations of 2^-24."""
     x, topk_w = np.asarray(x, dtype=np.float64), np.asarray(topk_w, dtype=np.float64)
     out, bound = np.zeros_like(x), np.zeros_like(x)

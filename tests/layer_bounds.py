@@ -60,18 +60,13 @@ def layer(x, w1, w2, ids, topk_w, expert_lo=0):
 def layer_error(got, want, spread):
     """How far `got` is off as a part of what is allowed (at most 1 is right).
 
-    A token's whole error: the output's rounding is within 2^-8 of each value, and that of
-    the hidden values to bf16 within 2^-8 of each, which the random weights of the second
-    product carry to 2^-8 of the output's length within a sixth (5 deviations of a sum of
-    1000 squares, above and below): under 0.0092 of the length, and 0.01 is allowed.
-
-    Each value: 2^-8 of it, and the sum of the hidden values' roundings, independent and
-    within 2^-8 of their terms, passes t times 2^-8 of the terms' spread with a probability of
-    2 exp(-t^2 / 2) at most: for t = 8.2 once in 10^14.  Sums in binary32 move a value by far
-    less than 2^-11 of that spread."""
-    off = (got.double() - want).abs()
-    each = off / (2.0 ** -8 * (1 + 2.0 ** -8) * want.abs() +
-                  8.2 * (2.0 ** -8 + 2.0 ** -11) * spread + 1e-38)
-    whole = torch.linalg.vector_norm(off, dim=-1) / (
-        0.01 * torch.linalg.vector_norm(want, dim=-1) + 1e-38)
-    return float(torch.maximum(each.max(), whole.max()))
+    The hidden values are two bf16 parts, within 2^-17 of what they stand for.  Their
+    roundings are independent, so their sum passes t times 2^-17 of the spread of an output's
+    terms with a probability of 2 exp(-t^2 / 2) at most: for t = 8.2 once in 10^14.  The sums
+    in binary32 are a few hundred additions within 2^-23 of a partial sum each, those of a
+    hidden value and of an output alike, whose signs are as good as random: 2 (300)^(1/2)
+    2^-23 is under 2^-17, of partial sums of up to a few spreads; 2^-13 is allowed for them.
+    The output is rounded once: half a step of bf16."""
+    delta = 8.2 * (2.0 ** -17 + 2.0 ** -13) * spread
+    half = torch.exp2(torch.floor(torch.log2(want.abs() + delta + 1e-38)) - 8)
+    return float(((got.double() - want).abs() / (half + delta + 1e-38)).max())

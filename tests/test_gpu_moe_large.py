@@ -75,7 +75,8 @@ class Layer:
         more = {}
         if self.fp8:
             # codes and scales as the norm makes them
-            y = self.ctx.rms_norm(x, torch.ones(self.shape[-1], device="cuda"), rows=False, fp8=True)
+            ones = torch.ones(self.shape[-1], device="cuda")
+            y = self.ctx.rms_norm(x, ones, rows=False, fp8=True)
             more = dict(x_scale=y.scales, w1_scale=self.w1.scale, w2_scale=self.w2.scale)
             rows = y.codes
             x = (y.codes.view(torch.float8_e4m3fn).double() *
@@ -118,3 +119,29 @@ def test_experts_behind_four_gib():
     assert 255 * layer.w1.w[0].numel() * 2 > 1 << 32
     ids = torch.tensor([[[255, 0], [254, 255], [3, 200], [-1, 255]]], dtype=torch.int32)
     layer.check(ids.cuda())
+
+
+@pytest.mark.parametrize("T", [1, 3, 7, 20])
+def test_a_hidden_value_past_the_range(T):
+    """silu(g) u of one hidden value is past binary32: infinite, with the sign of its weight;
+    its second part adds nothing.  The other experts' tokens are as they were."""
+    N = I = 128
+    ctx = EpCombine(n_ranks=1, top_k=1, max_tokens_per_rank=T + 1, n_experts_per_device=2,
+                    hidden_k=I, hidden_n=N)
+    w1 = torch.zeros(2, 2 * I, N, device="cuda")
+    w2 = torch.zeros(2, N, I, device="cuda")
+    w1[:, :, 0] = 1.0
+    w1[0, 0, 0] = w1[0, I, 0] = 1e20
+    w2[:, :, :] = 0.5
+    w2[0, :, 0] = torch.where(torch.arange(N, device="cuda") % 2 == 0, 2.0, -2.0)
+    x = torch.zeros(1, T + 1, N, device="cuda").bfloat16()
+    x[..., 0] = 4.0
+    ids = torch.zeros(1, T + 1, 1, dtype=torch.int32, device="cuda")
+    ids[0, T] = 1
+    tw = torch.ones(1, T + 1, 1, device="cuda")
+    out = ctx.moe_layer(x, w1.bfloat16(), w2.bfloat16(), ids, tw).float()
+    assert torch.all(out[0, :T, ::2] == float("inf"))
+    assert torch.all(out[0, :T, 1::2] == -float("inf"))
+    four = torch.tensor(4.0, dtype=torch.float64)
+    want = 0.5 * I * (four * four / (1 + torch.exp(-four))).item()
+    assert torch.all((out[0, T] - want).abs() <= 2.0 ** -8 * want)

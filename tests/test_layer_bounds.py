@@ -56,8 +56,10 @@ class Planted:
         self.topk_w = torch.tensor([[0.9, 0.1], [0.6, 0.4]])
         self.want, self.spread = L.layer(self.x, self.w1, self.w2, self.ids, self.topk_w)
 
-    def out(self, *, up=None, down=None, swap=False, ids=None, topk_w=None, columns=None):
-        """up, down: slices of k that the products leave out."""
+    def out(self, *, up=None, down=None, swap=False, ids=None, topk_w=None, columns=None,
+            parts=2):
+        """up, down: slices of k that the products leave out; parts: of bf16 that a hidden
+        value is held in."""
         ids = self.ids if ids is None else ids
         topk_w = self.topk_w if topk_w is None else topk_w
         out = torch.zeros_like(self.x)
@@ -70,7 +72,10 @@ class Planted:
                 gate, up_ = y[:self.inter], y[self.inter:]
                 if swap:
                     gate, up_ = up_, gate
-                h = (gate / (1 + torch.exp(-gate)) * up_).bfloat16().double()
+                exact = gate / (1 + torch.exp(-gate)) * up_
+                h = exact.bfloat16().double()
+                if parts == 2:
+                    h += (exact - h).bfloat16().double()
                 if down is not None and j == 0:
                     h[down] = 0
                 out[t] += topk_w[t, j] * (self.w2[e].double() @ h)
@@ -88,12 +93,12 @@ def planted():
 
 
 def test_the_layer_as_it_is_meets_its_bound(planted):
-    assert planted.error(planted.out()) < 0.7
+    assert planted.error(planted.out()) <= 1
 
 
 @pytest.mark.parametrize("mistake", [
     dict(up=slice(640, 768)), dict(up=slice(7136, 7168)), dict(down=slice(1920, 2048)),
-    dict(down=slice(32, 64)), dict(swap=True), dict(columns=slice(7152, 7168)),
+    dict(down=slice(32, 64)), dict(parts=1), dict(swap=True), dict(columns=slice(7152, 7168)),
     dict(columns=slice(16, 17)), dict(ids=torch.tensor([[1, 0], [1, 2]])),
     dict(ids=torch.tensor([[2, 1], [1, 2]])), dict(topk_w=torch.tensor([[0.9, 0.0], [0.6, 0.4]])),
     dict(topk_w=torch.tensor([[0.9, 0.1], [0.4, 0.6]])),
