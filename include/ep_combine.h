@@ -604,8 +604,9 @@ EP_API int ep_grouped_gemm_scatter_w4(ep_combine_t h, const ep_w4_format* format
    squares under its normal numbers (values under 2^-63, which count only beside an eps as
    small as their square) lose bits, under 2^-75 all of them.  A NaN
    in a row makes all of that row's y NaN, an infinity its own and the others zero (no other
-   row is touched), and so does a row of zeros with eps = 0 (NaN).  A NaN has the code 0x7f
-   or 0xff and no part in its block's scale. */
+   row is touched), and a row of zeros with eps = 0 is all NaN.  A NaN has the code 0x7f or
+   0xff and no part in its block's scale; an infinite y (an infinite weight, a product past
+   the range) has that code too, and makes the scale of its block infinite. */
 #define EP_ROWS_F32 0
 #define EP_ROWS_BF16 1
 #define EP_ROWS_F16 2

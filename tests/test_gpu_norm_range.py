@@ -73,3 +73,19 @@ def test_norm_of_the_same_rows(kind):
     err = np.abs(_np(y.out) - want)
     assert np.all(err <= (2.0 ** -17 + 2.0 ** -19 + _half(x.dtype) * 1.01) * np.abs(want))
     assert torch.equal(y.residual, x.to(res.dtype))
+
+
+def test_an_infinite_output_and_its_block():
+    """An infinite weight: its own value infinite, the code NaN, the block's scale infinite;
+    the other block as it was."""
+    x, w = torch.ones(1, 3, 256, device="cuda"), torch.ones(256, device="cuda")
+    ctx = make_ctx(TINY.replace(n_ranks=1, tokens_per_rank=3, n=256))
+    want = ctx.rms_norm(x, w, fp8=True)
+    w[3] = float("inf")
+    y = ctx.rms_norm(x, w, fp8=True)
+    assert torch.all(y.out[..., 3] == float("inf")) and torch.all((y.codes[..., 3] & 127) == 127)
+    assert torch.all(y.scales[..., 0] == float("inf"))
+    keep = torch.arange(256) != 3
+    assert torch.equal(y.out[..., keep], want.out[..., keep])
+    assert torch.equal(y.codes[..., 128:], want.codes[..., 128:])
+    assert torch.equal(y.scales[..., 1], want.scales[..., 1])
